@@ -269,7 +269,9 @@ kda_status kda_check_wait_timeout(void* workspace, size_t workspace_bytes, uint6
 static kda_status decode_impl(const void* q, const void* k, const void* v, const void* alpha,
                               kda_gate_format gate, const float* beta, float* S, int32_t B,
                               int32_t H, int32_t d_k, int32_t d_v, kda_dtype dtype, void* o,
-                              kda_stream_t stream, bool additive = false) {
+                              kda_stream_t stream, bool additive = false,
+                              const float* S_in = nullptr, const int32_t* parents = nullptr,
+                              int32_t num_rows = 0) {
     if (B < 0 || H < 1 || d_v < 1) return KDA_ERR_INVALID_ARG;
     if (gate != KDA_GATE_CHANNEL_F32 && gate != KDA_GATE_HEAD_F32 &&
         gate != KDA_GATE_CHANNEL_LOG_BF16)
@@ -297,11 +299,19 @@ static kda_status decode_impl(const void* q, const void* k, const void* v, const
         if (overlaps(S, n_s, ins[i], in_n[i]) || overlaps(o, n_o, ins[i], in_n[i]))
             return KDA_ERR_INVALID_ARG;
     if (overlaps(o, n_o, S, n_s)) return KDA_ERR_INVALID_ARG;
+    if (parents) {   // the states are read from S_in: no output may overlap it or parents
+        const size_t n_in = (size_t)num_rows * H * d_v * d_k * sizeof(float);
+        const size_t n_p = (size_t)B * sizeof(int32_t);
+        if (overlaps(S, n_s, S_in, n_in) || overlaps(o, n_o, S_in, n_in) ||
+            overlaps(S, n_s, parents, n_p) || overlaps(o, n_o, parents, n_p))
+            return KDA_ERR_INVALID_ARG;
+    }
 
     kda::DecodeArgs a;
     a.q = q; a.k = k; a.v = v; a.alpha = alpha; a.beta = beta; a.S = S;
     a.B = B; a.H = H; a.d_k = d_k; a.d_v = d_v; a.dtype = dtype; a.o = o; a.gate = gate;
     a.additive = additive ? 1 : 0;
+    a.S_in = S_in; a.parents = parents; a.num_rows = num_rows;
     return kda::launch_decode(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? KDA_OK
                : KDA_ERR_CUDA;
@@ -510,6 +520,264 @@ kda_status attnres_layer(const void* blocks, int32_t num_blocks, const float* pa
                    cudaSuccess
                ? KDA_OK
                : KDA_ERR_CUDA;
+}
+
+// Sizes and layouts the gated linear recurrence takes (rows: tokens or decode rows).
+static kda_status linrec_check(int64_t rows, int32_t num_seqs, int32_t H, int32_t d,
+                               kda_dtype dtype, kda_gate_format gate, linrec_input input) {
+    if (rows < 0 || num_seqs < 0 || H < 1 || d < 1) return KDA_ERR_INVALID_ARG;
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    if (gate != KDA_GATE_CHANNEL_F32 && gate != KDA_GATE_HEAD_F32 &&
+        gate != KDA_GATE_CHANNEL_LOG_BF16)
+        return KDA_ERR_INVALID_ARG;
+    if (input != LINREC_PLAIN && input != LINREC_COMPLEMENT) return KDA_ERR_INVALID_ARG;
+    if (d > 65536 || (int64_t)H * d > (1 << 20) || rows > (int64_t)INT32_MAX - LINREC_CHUNK)
+        return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)num_seqs * H * d >= (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+static size_t linrec_gate_bytes(int64_t rows, int32_t H, int32_t d, kda_gate_format gate) {
+    return gate == KDA_GATE_HEAD_F32 ? (size_t)rows * H * sizeof(float)
+           : gate == KDA_GATE_CHANNEL_LOG_BF16 ? (size_t)rows * H * d * 2
+                                               : (size_t)rows * H * d * sizeof(float);
+}
+
+size_t linrec_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t H,
+                                     int32_t d) {
+    if (linrec_check(total_tokens, num_seqs, H, d, KDA_BF16, KDA_GATE_CHANNEL_F32,
+                     LINREC_PLAIN) != KDA_OK)
+        return 0;
+    return kda::linrec_prefill_bytes(num_seqs, total_tokens, (int64_t)H * d);
+}
+
+kda_status linrec_prefill(const void* x, const void* gate, kda_gate_format gate_format,
+                          const float* S0, const int32_t* cu_seqlens, int32_t num_seqs,
+                          int64_t total_tokens, int32_t H, int32_t d, kda_dtype dtype,
+                          linrec_input input, void* y, float* S_T, float* states,
+                          void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+    const kda_status st = linrec_check(total_tokens, num_seqs, H, d, dtype, gate_format, input);
+    if (st != KDA_OK) return st;
+    if (!cu_seqlens || !workspace || (num_seqs > 0 && !S_T)) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!x || !gate || !y)) return KDA_ERR_INVALID_ARG;
+    const int64_t D = (int64_t)H * d;
+    if (workspace_bytes < kda::linrec_prefill_bytes(num_seqs, total_tokens, D))
+        return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, gate, S0, cu_seqlens, y, S_T, states, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    // no output may overlap an input, the workspace or another output, except S_T == S0
+    const size_t esz = dtype == KDA_BF16 ? 2 : 4;
+    const size_t n_x = (size_t)total_tokens * D * esz, n_s = (size_t)num_seqs * D * sizeof(float);
+    const size_t n_c = (size_t)(total_tokens + LINREC_CHUNK - 1) / LINREC_CHUNK * D * sizeof(float);
+    const void* ins[] = {x, gate, S0, cu_seqlens, workspace};
+    const size_t in_n[] = {n_x, linrec_gate_bytes(total_tokens, H, d, gate_format), n_s,
+                           ((size_t)num_seqs + 1) * sizeof(int32_t), workspace_bytes};
+    const void* outs[] = {y, S_T, states};
+    const size_t out_n[] = {n_x, n_s, n_c};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 5; ++i) {
+            if (o == 1 && i == 2 && S_T == S0) continue;   // in place
+            if (overlaps(outs[o], out_n[o], ins[i], in_n[i])) return KDA_ERR_INVALID_ARG;
+        }
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlaps(outs[o], out_n[o], outs[o2], out_n[o2])) return KDA_ERR_INVALID_ARG;
+    }
+
+    kda::LinrecArgs a = {};
+    a.x = x; a.gate = gate; a.S0 = S0; a.cu_seqlens = cu_seqlens;
+    a.total_tokens = total_tokens; a.num_seqs = num_seqs; a.H = H; a.d = d; a.dtype = dtype;
+    a.gate_format = gate_format; a.complement = input == LINREC_COMPLEMENT;
+    a.y = y; a.S_T = S_T; a.states = states;
+    return kda::launch_linrec_prefill(a, static_cast<char*>(workspace),
+                                      static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+size_t linrec_backward_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t H,
+                                      int32_t d, kda_gate_format gate_format,
+                                      int32_t with_states) {
+    if (linrec_check(total_tokens, num_seqs, H, d, KDA_BF16, gate_format, LINREC_PLAIN) != KDA_OK)
+        return 0;
+    return kda::linrec_backward_bytes(num_seqs, total_tokens, H, d, gate_format, with_states != 0);
+}
+
+kda_status linrec_backward(const void* x, const void* gate, kda_gate_format gate_format,
+                           const float* S0, const int32_t* cu_seqlens, int32_t num_seqs,
+                           int64_t total_tokens, int32_t H, int32_t d, kda_dtype dtype,
+                           linrec_input input, const void* dy, const float* dS_T,
+                           const float* states, float* dx, float* dgate, float* dS0,
+                           void* workspace, size_t workspace_bytes, kda_stream_t stream) {
+    const kda_status st = linrec_check(total_tokens, num_seqs, H, d, dtype, gate_format, input);
+    if (st != KDA_OK) return st;
+    if (!cu_seqlens || !workspace) return KDA_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!x || !gate || !dy || !dx || !dgate)) return KDA_ERR_INVALID_ARG;
+    if (workspace_bytes < kda::linrec_backward_bytes(num_seqs, total_tokens, H, d, gate_format,
+                                                     states != nullptr))
+        return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, gate, S0, cu_seqlens, dy, dS_T, states, dx, dgate, dS0, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    // no output may overlap an input, the workspace or another output
+    const int64_t D = (int64_t)H * d;
+    const size_t esz = dtype == KDA_BF16 ? 2 : 4;
+    const size_t n_x = (size_t)total_tokens * D * esz, n_s = (size_t)num_seqs * D * sizeof(float);
+    const size_t n_c = (size_t)(total_tokens + LINREC_CHUNK - 1) / LINREC_CHUNK * D * sizeof(float);
+    const size_t n_f = (size_t)total_tokens * D * sizeof(float);
+    const void* ins[] = {x, gate, S0, cu_seqlens, dy, dS_T, states, workspace};
+    const size_t in_n[] = {n_x, linrec_gate_bytes(total_tokens, H, d, gate_format), n_s,
+                           ((size_t)num_seqs + 1) * sizeof(int32_t), n_x, n_s, n_c,
+                           workspace_bytes};
+    const void* outs[] = {dx, dgate, dS0};
+    const size_t out_n[] = {n_f, gate_format == KDA_GATE_HEAD_F32
+                                     ? (size_t)total_tokens * H * sizeof(float) : n_f, n_s};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 8; ++i)
+            if (overlaps(outs[o], out_n[o], ins[i], in_n[i])) return KDA_ERR_INVALID_ARG;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlaps(outs[o], out_n[o], outs[o2], out_n[o2])) return KDA_ERR_INVALID_ARG;
+    }
+
+    kda::LinrecArgs a = {};
+    a.x = x; a.gate = gate; a.S0 = S0; a.cu_seqlens = cu_seqlens;
+    a.total_tokens = total_tokens; a.num_seqs = num_seqs; a.H = H; a.d = d; a.dtype = dtype;
+    a.gate_format = gate_format; a.complement = input == LINREC_COMPLEMENT;
+    a.states = const_cast<float*>(states);
+    a.dy = dy; a.dS_T = dS_T; a.dx = dx; a.dgate = dgate; a.dS0 = dS0;
+    return kda::launch_linrec_backward(a, static_cast<char*>(workspace),
+                                       static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+kda_status linrec_decode_step(const void* x, const void* gate, kda_gate_format gate_format,
+                              const float* S, int32_t num_rows, const int32_t* parents,
+                              int32_t B, int32_t H, int32_t d, kda_dtype dtype,
+                              linrec_input input, void* y, float* S_out, kda_stream_t stream) {
+    if (num_rows < 0) return KDA_ERR_INVALID_ARG;
+    const kda_status st = linrec_check(B, num_rows, H, d, dtype, gate_format, input);
+    if (st != KDA_OK) return st;
+    if (!parents && num_rows != B) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    if (!x || !gate || (num_rows > 0 && !S) || !y || !S_out) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {x, gate, S, parents, y, S_out};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    const int64_t D = (int64_t)H * d;
+    const size_t n_x = (size_t)B * D * (dtype == KDA_BF16 ? 2 : 4);
+    const size_t n_out = (size_t)B * D * sizeof(float);
+    const void* ins[] = {x, gate, parents, S};
+    const size_t in_n[] = {n_x, linrec_gate_bytes(B, H, d, gate_format),
+                           (size_t)B * sizeof(int32_t), (size_t)num_rows * D * sizeof(float)};
+    for (int i = 0; i < 4; ++i) {
+        if (overlaps(y, n_x, ins[i], in_n[i])) return KDA_ERR_INVALID_ARG;
+        if (i == 3 && !parents && S_out == S) continue;   // in place
+        if (overlaps(S_out, n_out, ins[i], in_n[i])) return KDA_ERR_INVALID_ARG;
+    }
+    if (overlaps(y, n_x, S_out, n_out)) return KDA_ERR_INVALID_ARG;
+
+    kda::LinrecStepArgs a = {};
+    a.x = x; a.gate = gate; a.S = S; a.parents = parents; a.num_rows = num_rows; a.B = B;
+    a.H = H; a.d = d; a.dtype = dtype; a.gate_format = gate_format;
+    a.complement = input == LINREC_COMPLEMENT; a.y = y; a.S_out = S_out;
+    return kda::launch_linrec_step(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+static kda_status beam_select_check(int32_t B, int32_t K, int32_t V, int32_t num_out) {
+    if (B < 0 || K < 1 || V < 1 || num_out < 1) return KDA_ERR_INVALID_ARG;
+    if ((int64_t)num_out > (int64_t)K * V) return KDA_ERR_INVALID_ARG;
+    if (K > BEAM_MAX_BEAMS || num_out > BEAM_MAX_SELECT || V > (1 << 20) ||
+        (int64_t)B * K > (1 << 20))
+        return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+size_t beam_select_workspace_size(int32_t B, int32_t K, int32_t V, int32_t num_out) {
+    if (beam_select_check(B, K, V, num_out) != KDA_OK) return 0;
+    return kda::beam_select_bytes(B, K, V, num_out);
+}
+
+kda_status beam_select(const void* logits, int64_t ld, const float* scores,
+                       const uint8_t* finished, int32_t B, int32_t K, int32_t V,
+                       int32_t num_out, int32_t eos, kda_dtype dtype, float* out_scores,
+                       int32_t* out_parents, int32_t* out_tokens, void* workspace,
+                       size_t workspace_bytes, kda_stream_t stream) {
+    if (dtype != KDA_BF16 && dtype != KDA_FP32) return KDA_ERR_INVALID_ARG;
+    const kda_status st = beam_select_check(B, K, V, num_out);
+    if (st != KDA_OK) return st;
+    const int64_t esz = dtype == KDA_BF16 ? 2 : 4;
+    if (ld < V || (ld != V && ld * esz % 16 != 0)) return KDA_ERR_INVALID_ARG;
+    if (ld > (int64_t)1 << 32) return KDA_ERR_UNSUPPORTED;
+    if (finished && (eos < 0 || eos >= V)) return KDA_ERR_INVALID_ARG;
+    if (B == 0) return KDA_OK;
+    if (!logits || !scores || !out_scores || !out_parents || !out_tokens || !workspace)
+        return KDA_ERR_INVALID_ARG;
+    if (workspace_bytes < kda::beam_select_bytes(B, K, V, num_out)) return KDA_ERR_INVALID_ARG;
+    const void* ptrs[] = {logits, scores, finished, out_scores, out_parents, out_tokens, workspace};
+    for (const void* p : ptrs)
+        if (p && !aligned16(p)) return KDA_ERR_INVALID_ARG;
+    const size_t rows = (size_t)B * K, n_out = (size_t)B * num_out * 4;
+    const void* ins[] = {logits, scores, finished, workspace};
+    const size_t in_n[] = {((rows - 1) * ld + V) * esz, rows * 4, rows, workspace_bytes};
+    const void* outs[] = {out_scores, out_parents, out_tokens};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 4; ++i)
+            if (overlaps(outs[o], n_out, ins[i], in_n[i])) return KDA_ERR_INVALID_ARG;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlaps(outs[o], n_out, outs[o2], n_out)) return KDA_ERR_INVALID_ARG;
+    }
+
+    kda::BeamSelectArgs a = {};
+    a.logits = logits; a.ld = ld; a.scores = scores; a.finished = finished; a.B = B; a.K = K;
+    a.V = V; a.num_out = num_out; a.eos = eos; a.dtype = dtype; a.out_scores = out_scores;
+    a.out_parents = out_parents; a.out_tokens = out_tokens;
+    return kda::launch_beam_select(a, static_cast<char*>(workspace),
+                                   static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+kda_status beam_reorder(const beam_state* states, int32_t num_states, const int32_t* parents,
+                        int32_t B, int32_t K, kda_stream_t stream) {
+    if (num_states < 0 || B < 0 || K < 1) return KDA_ERR_INVALID_ARG;
+    if (K > BEAM_MAX_BEAMS || (int64_t)B * K > (1 << 20)) return KDA_ERR_UNSUPPORTED;
+    if (num_states == 0 || B == 0) return KDA_OK;
+    if (!states || !parents || !aligned16(parents)) return KDA_ERR_INVALID_ARG;
+    const size_t rows = (size_t)B * K;
+    for (int i = 0; i < num_states; ++i) {
+        if (states[i].row_bytes < 0) return KDA_ERR_INVALID_ARG;
+        if (states[i].row_bytes > (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
+        const size_t n = rows * states[i].row_bytes;
+        if (n == 0) continue;
+        if (!states[i].data || !aligned16(states[i].data)) return KDA_ERR_INVALID_ARG;
+        if (overlaps(states[i].data, n, parents, rows * sizeof(int32_t)))
+            return KDA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(states[i].data, n, states[j].data, rows * states[j].row_bytes))
+                return KDA_ERR_INVALID_ARG;
+    }
+    return kda::launch_beam_reorder(states, num_states, parents, B, K,
+                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
+kda_status kda_decode_step_parents(const void* q, const void* k, const void* v,
+                                   const void* alpha, kda_gate_format gate_format,
+                                   const float* beta, const float* S_in, int32_t num_rows,
+                                   const int32_t* parents, float* S_out, int32_t B, int32_t H,
+                                   int32_t d_k, int32_t d_v, kda_dtype dtype, void* o,
+                                   kda_stream_t stream) {
+    if (num_rows < 0) return KDA_ERR_INVALID_ARG;
+    if (B > 0 && (!parents || (num_rows > 0 && !S_in))) return KDA_ERR_INVALID_ARG;
+    if ((parents && !aligned16(parents)) || (S_in && !aligned16(S_in)))
+        return KDA_ERR_INVALID_ARG;
+    if ((int64_t)num_rows * H > (int64_t)INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    return decode_impl(q, k, v, alpha, gate_format, beta, S_out, B, H, d_k, d_v, dtype, o, stream,
+                       false, S_in, parents, num_rows);
 }
 
 const char* kda_status_string(kda_status s) {

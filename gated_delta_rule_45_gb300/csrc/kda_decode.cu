@@ -47,12 +47,17 @@ __device__ __forceinline__ float gate_of(const void* alpha, int bh, size_t vi) {
     return static_cast<const float*>(alpha)[vi];
 }
 
-template <int DK, typename T, int GATE>
+// PARENTS (kda_decode_step_parents): sequence b's state is read from row
+// parents[b] of S_in, a zero state for an entry outside [0, num_rows), and
+// written to row b of S.  Beams that share a parent read the same bytes; the
+// rest of the step is the same, so moving the states costs nothing of its own.
+template <int DK, typename T, int GATE, bool PARENTS>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
 kda_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
                   const void* __restrict__ alpha, const float* __restrict__ beta,
                   float* __restrict__ S, int32_t H, int32_t d_v, T* __restrict__ o,
-                  int32_t additive) {
+                  int32_t additive, const float* __restrict__ S_in,
+                  const int32_t* __restrict__ parents, int32_t num_rows) {
     using Sh = DecodeShape<DK>;
     const int bh = blockIdx.x;                  // b * H + h
     const int lane = threadIdx.x & 31;
@@ -76,15 +81,27 @@ kda_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __r
     kq = group_sum<Sh::LPR>(kq);
     const float bt = beta[bh];
 
+    const float* src_bh = S + (size_t)bh * d_v * DK;
+    bool live = true;
+    if (PARENTS) {
+        const int b = bh / H;
+        const int p = parents[b];
+        live = p >= 0 && p < num_rows;
+        src_bh = S_in + ((size_t)(live ? p : 0) * H + (bh - b * H)) * d_v * DK;
+    }
+
     const int row0 = blockIdx.y * Sh::ROWS_PER_CTA + warp * (Sh::RPW * kDecodeUnroll);
     float4 s[kDecodeUnroll][Sh::VEC];
 #pragma unroll
     for (int u = 0; u < kDecodeUnroll; ++u) {
         const int r = row0 + u * Sh::RPW + grp;
         if (r < d_v) {
-            const float4* src = reinterpret_cast<const float4*>(S + ((size_t)bh * d_v + r) * DK);
+            const float4* src = reinterpret_cast<const float4*>(src_bh + (size_t)r * DK);
 #pragma unroll
-            for (int j = 0; j < Sh::VEC; ++j) s[u][j] = __ldcs(src + j * Sh::LPR + sub);
+            for (int j = 0; j < Sh::VEC; ++j) {
+                if (!PARENTS) s[u][j] = __ldcs(src + j * Sh::LPR + sub);
+                else s[u][j] = live ? __ldg(src + j * Sh::LPR + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
     }
 #pragma unroll
@@ -126,9 +143,12 @@ template <int DK, typename T, int GATE>
 cudaError_t launch_decode_g(const DecodeArgs& a, cudaStream_t stream) {
     using Sh = DecodeShape<DK>;
     dim3 grid(a.B * a.H, (a.d_v + Sh::ROWS_PER_CTA - 1) / Sh::ROWS_PER_CTA);
-    kda_decode_kernel<DK, T, GATE><<<grid, kDecodeWarps * 32, 0, stream>>>(
+    auto kernel = a.parents ? kda_decode_kernel<DK, T, GATE, true>
+                            : kda_decode_kernel<DK, T, GATE, false>;
+    kernel<<<grid, kDecodeWarps * 32, 0, stream>>>(
         static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v),
-        a.alpha, a.beta, a.S, a.H, a.d_v, static_cast<T*>(a.o), a.additive);
+        a.alpha, a.beta, a.S, a.H, a.d_v, static_cast<T*>(a.o), a.additive, a.S_in, a.parents,
+        a.num_rows);
     return cudaGetLastError();
 }
 

@@ -5,7 +5,9 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include "beam.h"
 #include "kda.h"
+#include "linrec.h"
 
 namespace kda {
 
@@ -111,12 +113,63 @@ struct DecodeArgs {
     const void* v;
     const void* alpha;   // layout by gate (kda_gate_format)
     const float* beta;
-    float* S;
+    float* S;            // read and overwritten; with parents, written only
     int32_t B, H, d_k, d_v;
     kda_dtype dtype;
     void* o;
     int32_t gate = 0;    // kda_gate_format
     int32_t additive = 0;   // additive update of linear attention instead of the delta rule
+    // kda_decode_step_parents: sequence b's state is row parents[b] of S_in
+    const float* S_in = nullptr;
+    const int32_t* parents = nullptr;
+    int32_t num_rows = 0;
+};
+
+// Gated linear recurrence (linrec.cu), arguments as in linrec.h.
+struct LinrecArgs {
+    const void* x;
+    const void* gate;
+    const float* S0;
+    const int32_t* cu_seqlens;
+    int64_t total_tokens;
+    int32_t num_seqs, H, d;
+    kda_dtype dtype;
+    int32_t gate_format;
+    int32_t complement;
+    // prefill
+    void* y = nullptr;
+    float* S_T = nullptr;
+    float* states = nullptr;   // backward: an input
+    // backward
+    const void* dy = nullptr;
+    const float* dS_T = nullptr;
+    float *dx = nullptr, *dgate = nullptr, *dS0 = nullptr;
+    int32_t* status = nullptr;   // device, in the workspace
+};
+
+struct LinrecStepArgs {
+    const void* x;
+    const void* gate;
+    const float* S;
+    const int32_t* parents;   // or null
+    int32_t num_rows, B, H, d;
+    kda_dtype dtype;
+    int32_t gate_format;
+    int32_t complement;
+    void* y;
+    float* S_out;
+};
+
+// Beam search's selection (beam.cu), arguments as in beam.h.
+struct BeamSelectArgs {
+    const void* logits;
+    int64_t ld;
+    const float* scores;
+    const uint8_t* finished;
+    int32_t B, K, V, num_out, eos;
+    kda_dtype dtype;
+    float* out_scores;
+    int32_t *out_parents, *out_tokens;
 };
 
 // Backward pass (kda_backward.cu).  Buffers appended to the base workspace:
@@ -194,6 +247,20 @@ cudaError_t launch_attnres(const void* blocks, int32_t nb, const float* partial,
                            const void* h_last, float* partial_out, void* block_out,
                            const float* q, float scale, int64_t T, int32_t d, kda_dtype dtype,
                            void* h, cudaStream_t stream);
+
+// Gated linear recurrence (ws: the workspace base, status word first; linrec.cu).
+size_t linrec_prefill_bytes(int32_t num_seqs, int64_t total_tokens, int64_t D);
+size_t linrec_backward_bytes(int32_t num_seqs, int64_t total_tokens, int32_t H, int32_t d,
+                             int gate_format, bool with_states);
+cudaError_t launch_linrec_prefill(LinrecArgs a, char* ws, cudaStream_t stream);
+cudaError_t launch_linrec_backward(LinrecArgs a, char* ws, cudaStream_t stream);
+cudaError_t launch_linrec_step(const LinrecStepArgs& a, cudaStream_t stream);
+// Beam search (beam.cu).
+size_t beam_select_bytes(int32_t B, int32_t K, int32_t V, int32_t num_out);
+cudaError_t launch_beam_select(const BeamSelectArgs& a, char* ws, cudaStream_t stream);
+cudaError_t launch_beam_reorder(const beam_state* states, int32_t num_states,
+                                const int32_t* parents, int32_t B, int32_t K,
+                                cudaStream_t stream);
 
 int sm_count();   // of the current device, cached per device
 

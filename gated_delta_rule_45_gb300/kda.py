@@ -12,10 +12,14 @@ The names follow the C ABI: ``prefill`` / ``prefill_into`` wrap
 ``device_status`` wraps ``kda_prefill_device_status`` and ``backward`` /
 ``backward_into`` / ``backward_workspace_size`` wrap ``kda_backward`` and
 ``kda_backward_workspace_size``; ``attnres_layer`` wraps the Blocked Attention
-Residuals call of ``include/attnres.h``.
+Residuals call of ``include/attnres.h``; the ``linrec_*`` functions wrap the
+gated linear recurrence of ``include/linrec.h``, and ``beam_select``,
+``beam_reorder`` and ``decode_step_parents`` the beam search calls of
+``include/beam.h``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -104,6 +108,30 @@ def load(path: str | None = None):
     lib.attnres_layer.restype = ctypes.c_int
     lib.attnres_layer.argtypes = [vp, i32, vp, vp, vp, vp, vp, ctypes.c_float, i64, i32,
                                   ctypes.c_int, vp, vp]
+    lib.linrec_prefill_workspace_size.restype = sz
+    lib.linrec_prefill_workspace_size.argtypes = [i32, i64, i32, i32]
+    lib.linrec_prefill.restype = ctypes.c_int
+    lib.linrec_prefill.argtypes = [vp, vp, ctypes.c_int, vp, vp, i32, i64, i32, i32,
+                                   ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, sz, vp]
+    lib.linrec_backward_workspace_size.restype = sz
+    lib.linrec_backward_workspace_size.argtypes = [i32, i64, i32, i32, ctypes.c_int, i32]
+    lib.linrec_backward.restype = ctypes.c_int
+    lib.linrec_backward.argtypes = [vp, vp, ctypes.c_int, vp, vp, i32, i64, i32, i32,
+                                    ctypes.c_int, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, sz,
+                                    vp]
+    lib.linrec_decode_step.restype = ctypes.c_int
+    lib.linrec_decode_step.argtypes = [vp, vp, ctypes.c_int, vp, i32, vp, i32, i32, i32,
+                                       ctypes.c_int, ctypes.c_int, vp, vp, vp]
+    lib.beam_select_workspace_size.restype = sz
+    lib.beam_select_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.beam_select.restype = ctypes.c_int
+    lib.beam_select.argtypes = [vp, i64, vp, vp, i32, i32, i32, i32, i32, ctypes.c_int, vp, vp,
+                                vp, vp, sz, vp]
+    lib.beam_reorder.restype = ctypes.c_int
+    lib.beam_reorder.argtypes = [vp, i32, vp, i32, i32, vp]
+    lib.kda_decode_step_parents.restype = ctypes.c_int
+    lib.kda_decode_step_parents.argtypes = [vp, vp, vp, vp, ctypes.c_int, vp, vp, i32, vp, vp,
+                                            i32, i32, i32, i32, ctypes.c_int, vp, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_version.restype = i32
@@ -544,3 +572,324 @@ def attnres_layer(blocks, q, *, partial=None, h_last=None, partial_out=None, blo
     if st != OK:
         raise KdaError(st, "attnres_layer")
     return h
+
+
+# ---- gated linear recurrence (include/linrec.h) and beam search (include/beam.h)
+
+_DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: FP32}
+LINREC_CHUNK = 128
+BEAM_MAX_BEAMS, BEAM_MAX_SELECT = 32, 64
+
+
+class _BeamState(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_bytes", ctypes.c_int64)]
+
+
+def _check(what: str, t, dtype, shape) -> None:
+    """One tensor argument: its type (TypeError), then its shape (ValueError)."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _place(stream, *ts) -> int:
+    """Raw stream to launch on; every tensor must be contiguous on the current device."""
+    dev = torch.cuda.current_device() if ts[0].is_cuda else -1
+    for t in ts:
+        if t is not None and (not t.is_cuda or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous CUDA tensors")
+        if t is not None and t.get_device() != dev:
+            raise ValueError("all tensors must be on the current CUDA device")
+    if stream is None:
+        stream = torch.cuda.current_stream()
+    elif stream.device_index != dev:
+        raise ValueError("the stream must belong to the current CUDA device")
+    return stream.cuda_stream
+
+
+def _alloc(stream):
+    """Context in which memory is allocated for work on `stream`: the caching
+    allocator hands a block freed there only to later work of the same stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _linrec_args(x, a, gate: str, rows: str):
+    """(H, d, dtype code, gate code) of x [rows, H, d] and its gate."""
+    code = _DTYPE_CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"the storage dtype must be bfloat16 or float32, got {x.dtype}")
+    if x.dim() != 3:
+        raise ValueError(f"x must be [{rows}, H, d], got {tuple(x.shape)}")
+    gcode, adt, arank = _GATES[gate]
+    _check(f"the gate (layout {gate!r})", a, adt, x.shape[:arank])
+    return x.shape[1], x.shape[2], code, gcode
+
+
+def linrec_workspace_size(num_seqs: int, total_tokens: int, H: int, d: int) -> int:
+    """linrec_prefill_workspace_size: bytes of workspace (0: size not supported)."""
+    return load().linrec_prefill_workspace_size(num_seqs, total_tokens, H, d)
+
+
+def linrec_prefill_into(x, a, S0, cu_seqlens, y, S_T, workspace, *, states=None,
+                        gate: str = "channel", complement: bool = False, stream=None) -> None:
+    """Enqueue linrec_prefill into preallocated outputs: h_t = a_t h_{t-1} + u_t per
+    channel, u = x or, with `complement`, (1 - a) x.
+
+    x, y: [T, H, d] (bf16 or fp32); a: the forget gate in layout `gate` as for
+    ``prefill_gates_into`` ("channel" [T, H, d] fp32, "head" [T, H] fp32,
+    "log_bf16" log a [T, H, d] bf16); S0: [N, H, d] fp32 or None; cu_seqlens:
+    int32 [N+1] on the device; S_T: [N, H, d] fp32 (may be S0); states:
+    [ceil(T / LINREC_CHUNK), H, d] fp32 or None, kept for ``linrec_backward``;
+    workspace: uint8, at least ``linrec_workspace_size`` bytes.
+    """
+    H, d, code, gcode = _linrec_args(x, a, gate, "T")
+    T, N = x.shape[0], cu_seqlens.numel() - 1
+    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
+    _check("y", y, x.dtype, x.shape)
+    _check("S_T", S_T, torch.float32, (N, H, d))
+    if S0 is not None:
+        _check("S0", S0, torch.float32, (N, H, d))
+    if states is not None:
+        _check("states", states, torch.float32, (-(-T // LINREC_CHUNK), H, d))
+    raw = _place(stream, x, a, S0, cu_seqlens, y, S_T, states, workspace)
+    st = load().linrec_prefill(_p(x), _p(a), gcode, _p(S0), _p(cu_seqlens), N, T, H, d, code,
+                               int(complement), _p(y), _p(S_T), _p(states), _p(workspace),
+                               workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "linrec_prefill")
+
+
+def linrec_prefill(x, a, S0, cu_seqlens, *, gate: str = "channel", complement: bool = False,
+                   save_states: bool = False, stream=None, check_device_status: bool = False):
+    """Allocate outputs with PyTorch and run linrec_prefill; returns (y, S_T), or with
+    `save_states` (y, S_T, states) for ``linrec_backward``.  y of tokens past
+    cu_seqlens[-1] is not written."""
+    H, d, _, _ = _linrec_args(x, a, gate, "T")
+    T, N, dev = x.shape[0], cu_seqlens.numel() - 1, x.device
+    nbytes = linrec_workspace_size(N, T, H, d)
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED, "linrec_prefill")
+    with _alloc(stream):
+        y = torch.empty_like(x)
+        S_T = torch.empty((N, H, d), dtype=torch.float32, device=dev)
+        states = torch.empty((-(-T // LINREC_CHUNK), H, d), dtype=torch.float32,
+                             device=dev) if save_states else None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    linrec_prefill_into(x, a, S0, cu_seqlens, y, S_T, ws, states=states, gate=gate,
+                        complement=complement, stream=stream)
+    if check_device_status:
+        device_status(ws, stream=stream)
+    return (y, S_T, states) if save_states else (y, S_T)
+
+
+def linrec_backward_workspace_size(num_seqs: int, total_tokens: int, H: int, d: int, *,
+                                   gate: str = "channel", with_states: bool = True) -> int:
+    """linrec_backward_workspace_size: bytes of workspace (0: size not supported)."""
+    return load().linrec_backward_workspace_size(num_seqs, total_tokens, H, d, _GATES[gate][0],
+                                                 int(with_states))
+
+
+def linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, workspace, *, states=None,
+                         gate: str = "channel", complement: bool = False, stream=None) -> None:
+    """Enqueue linrec_backward into preallocated fp32 gradients.
+
+    Inputs as ``linrec_prefill_into``; dy: like x; dS_T: [N, H, d] fp32 or None;
+    states: what linrec_prefill saved, or None (the forward scan runs again);
+    grads: dict with "dx" [T, H, d], "dgate" (shaped like the gate; with respect
+    to log a for "log_bf16") and optionally "dS0" [N, H, d]; workspace: uint8, at
+    least ``linrec_backward_workspace_size`` bytes.
+    """
+    H, d, code, gcode = _linrec_args(x, a, gate, "T")
+    T, N = x.shape[0], cu_seqlens.numel() - 1
+    dx, dgate, dS0 = grads["dx"], grads["dgate"], grads.get("dS0")
+    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
+    _check("dy", dy, x.dtype, x.shape)
+    for what, t in (("S0", S0), ("dS_T", dS_T), ("dS0", dS0)):
+        if t is not None:
+            _check(what, t, torch.float32, (N, H, d))
+    if states is not None:
+        _check("states", states, torch.float32, (-(-T // LINREC_CHUNK), H, d))
+    _check("dx", dx, torch.float32, x.shape)
+    _check("dgate", dgate, torch.float32, a.shape)
+    raw = _place(stream, x, a, S0, cu_seqlens, dy, dS_T, states, dx, dgate, dS0, workspace)
+    st = load().linrec_backward(_p(x), _p(a), gcode, _p(S0), _p(cu_seqlens), N, T, H, d, code,
+                                int(complement), _p(dy), _p(dS_T), _p(states), _p(dx),
+                                _p(dgate), _p(dS0), _p(workspace),
+                                workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "linrec_backward")
+
+
+def linrec_backward(x, a, S0, cu_seqlens, dy, dS_T=None, *, states=None, gate: str = "channel",
+                    complement: bool = False, stream=None, check_device_status: bool = False):
+    """Allocate fp32 gradients with PyTorch and run linrec_backward; returns a dict with
+    dx, dgate and dS0.  Rows of tokens past cu_seqlens[-1] are not written."""
+    H, d, _, _ = _linrec_args(x, a, gate, "T")
+    T, N, dev = x.shape[0], cu_seqlens.numel() - 1, x.device
+    nbytes = linrec_backward_workspace_size(N, T, H, d, gate=gate, with_states=states is not None)
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED, "linrec_backward")
+    with _alloc(stream):
+        grads = {"dx": torch.empty(x.shape, dtype=torch.float32, device=dev),
+                 "dgate": torch.empty(a.shape, dtype=torch.float32, device=dev),
+                 "dS0": torch.empty((N, H, d), dtype=torch.float32, device=dev)}
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, ws, states=states, gate=gate,
+                         complement=complement, stream=stream)
+    if check_device_status:
+        device_status(ws, stream=stream)
+    return grads
+
+
+def linrec_decode_step(x, a, S, y=None, *, parents=None, S_out=None, gate: str = "channel",
+                       complement: bool = False, stream=None):
+    """Enqueue linrec_decode_step: one token for each of B sequences; returns y [B, H, d].
+
+    x: [B, H, d]; a: as for ``linrec_prefill_into`` with B in T's place; S: fp32
+    [B, H, d], updated in place unless S_out is given.  parents: int32 [B] or None:
+    sequence b continues row parents[b] of S [rows, H, d] (a zero state for an entry
+    outside it) and S_out [B, H, d] must be given."""
+    H, d, code, gcode = _linrec_args(x, a, gate, "B")
+    B = x.shape[0]
+    if parents is None:
+        _check("S", S, torch.float32, (B, H, d))
+    else:
+        _check("parents", parents, torch.int32, (B,))
+        _check("S", S, torch.float32, (S.shape[0], H, d))
+        if S_out is None:
+            raise ValueError("parents need S_out: the states cannot move in place")
+    if S_out is None:
+        S_out = S
+    else:
+        _check("S_out", S_out, torch.float32, (B, H, d))
+    if y is None:
+        with _alloc(stream):
+            y = torch.empty_like(x)
+    else:
+        _check("y", y, x.dtype, x.shape)
+    raw = _place(stream, x, a, S, parents, S_out, y)
+    st = load().linrec_decode_step(_p(x), _p(a), gcode, _p(S), S.shape[0], _p(parents), B, H, d,
+                                   code, int(complement), _p(y), _p(S_out), raw)
+    if st != OK:
+        raise KdaError(st, "linrec_decode_step")
+    return y
+
+
+def decode_step_parents(q, k, v, alpha, beta, S_in, parents, S_out, o=None, *,
+                        gate: str = "channel", stream=None):
+    """Enqueue kda_decode_step_parents: ``decode_step_gates`` with sequence b's state read
+    from row parents[b] of S_in [rows, H, d_v, d_k] (a zero state for an entry outside it)
+    and written to row b of S_out [B, H, d_v, d_k]; returns o [B, H, d_v]."""
+    B, H, d_k = q.shape
+    d_v = v.shape[2]
+    code = _DTYPE_CODES.get(q.dtype)
+    if code is None:
+        raise TypeError(f"the storage dtype must be bfloat16 or float32, got {q.dtype}")
+    gcode, adt, arank = _GATES[gate]
+    _check("k", k, q.dtype, q.shape)
+    _check("v", v, q.dtype, (B, H, d_v))
+    _check(f"alpha (layout {gate!r})", alpha, adt, v.shape[:arank])
+    _check("beta", beta, torch.float32, (B, H))
+    _check("S_in", S_in, torch.float32, (S_in.shape[0], H, d_v, d_k))
+    _check("S_out", S_out, torch.float32, (B, H, d_v, d_k))
+    _check("parents", parents, torch.int32, (B,))
+    if o is None:
+        with _alloc(stream):
+            o = torch.empty_like(v)
+    else:
+        _check("o", o, q.dtype, v.shape)
+    raw = _place(stream, q, k, v, alpha, beta, S_in, parents, S_out, o)
+    st = load().kda_decode_step_parents(_p(q), _p(k), _p(v), _p(alpha), gcode, _p(beta),
+                                        _p(S_in), S_in.shape[0], _p(parents), _p(S_out), B, H,
+                                        d_k, d_v, code, _p(o), raw)
+    if st != OK:
+        raise KdaError(st, "kda_decode_step_parents")
+    return o
+
+
+def beam_select(logits, scores, num_out: int, *, finished=None, eos: int = 0, out=None,
+                workspace=None, stream=None):
+    """Enqueue beam_select: the num_out best continuations of each request over its beams
+    and the vocabulary; returns (scores fp32, parents int32, tokens int32), each
+    [B, num_out], best first.  parents are rows of `logits`.
+
+    logits: [B K, V] (bf16 or fp32; rows may be strided: a padded vocabulary); scores:
+    [B, K] fp32; finished: uint8 or bool [B, K] or None: a finished beam's one candidate
+    is token `eos` at its score; out: the three outputs to write to; workspace: uint8, at
+    least ``beam_select_workspace_size`` bytes (allocated when not given)."""
+    code = _DTYPE_CODES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"the storage dtype must be bfloat16 or float32, got {logits.dtype}")
+    if scores.dim() != 2 or logits.dim() != 2:
+        raise ValueError("logits must be [B K, V] and scores [B, K]")
+    B, K = scores.shape
+    V = logits.shape[1]
+    _check("scores", scores, torch.float32, (B, K))
+    _check("logits", logits, logits.dtype, (B * K, V))
+    if finished is not None:
+        if finished.dtype == torch.bool:
+            finished = finished.view(torch.uint8)
+        _check("finished", finished, torch.uint8, (B, K))
+    ld = logits.stride(0) if B * K > 1 else V
+    if V > 1 and logits.stride(1) != 1:
+        raise ValueError("each row of logits must be contiguous")
+    lib = load()
+    nbytes = lib.beam_select_workspace_size(B, K, V, num_out)
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED if 1 <= num_out <= K * V else ERR_INVALID_ARG,
+                       "beam_select")
+    with _alloc(stream):
+        if out is None:
+            buf = torch.empty((3, B, num_out), dtype=torch.int32, device=scores.device) \
+                if B * num_out % 4 == 0 else None
+            out = (buf[0].view(torch.float32), buf[1], buf[2]) if buf is not None else \
+                tuple(torch.empty((B, num_out), dtype=t, device=scores.device)
+                      for t in (torch.float32, torch.int32, torch.int32))
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=scores.device)
+    for what, t, dt in zip(("out scores", "out parents", "out tokens"), out,
+                           (torch.float32, torch.int32, torch.int32)):
+        _check(what, t, dt, (B, num_out))
+    if not logits.is_cuda or logits.get_device() != scores.get_device():
+        raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+    raw = _place(stream, scores, finished, *out, workspace)
+    st = lib.beam_select(_p(logits), ld, _p(scores), _p(finished), B, K, V, num_out, eos, code,
+                         _p(out[0]), _p(out[1]), _p(out[2]), _p(workspace),
+                         workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "beam_select")
+    return out
+
+
+def beam_select_workspace_size(B: int, K: int, V: int, num_out: int) -> int:
+    """beam_select_workspace_size: bytes of workspace (0: size not supported)."""
+    return load().beam_select_workspace_size(B, K, V, num_out)
+
+
+def beam_reorder(states, parents, beams: int, *, stream=None) -> None:
+    """Enqueue beam_reorder: row i of each tensor becomes its old row parents[i], in place.
+
+    states: tensors whose first axis is the B x beams rows (any type, contiguous);
+    parents: int32, B x beams entries, each a row of the same request (an entry that is
+    not leaves its row as it is)."""
+    if parents.dtype != torch.int32:
+        raise TypeError("parents must be int32")
+    rows = parents.numel()
+    if beams < 1 or rows % beams:
+        raise ValueError(f"parents must have a multiple of {beams} entries, got {rows}")
+    descr = (_BeamState * len(states))()
+    for s, t in zip(descr, states):
+        if t.dim() < 1 or t.shape[0] != rows:
+            raise ValueError(f"every state must have {rows} rows, got {tuple(t.shape)}")
+        s.data = t.data_ptr()
+        s.row_bytes = t.numel() * t.element_size() // rows if rows else 0
+    raw = _place(stream, parents, *states)
+    st = load().beam_reorder(ctypes.byref(descr), len(states), _p(parents), rows // beams, beams,
+                             raw)
+    if st != OK:
+        raise KdaError(st, "beam_reorder")
