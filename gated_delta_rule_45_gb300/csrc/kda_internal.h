@@ -144,7 +144,6 @@ struct LinrecArgs {
     const void* dy = nullptr;
     const float* dS_T = nullptr;
     float *dx = nullptr, *dgate = nullptr, *dS0 = nullptr;
-    int32_t* status = nullptr;   // device, in the workspace
 };
 
 struct LinrecStepArgs {
@@ -252,8 +251,8 @@ cudaError_t launch_attnres(const void* blocks, int32_t nb, const float* partial,
 size_t linrec_prefill_bytes(int32_t num_seqs, int64_t total_tokens, int64_t D);
 size_t linrec_backward_bytes(int32_t num_seqs, int64_t total_tokens, int32_t H, int32_t d,
                              int gate_format, bool with_states);
-cudaError_t launch_linrec_prefill(LinrecArgs a, char* ws, cudaStream_t stream);
-cudaError_t launch_linrec_backward(LinrecArgs a, char* ws, cudaStream_t stream);
+cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t stream);
+cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t stream);
 cudaError_t launch_linrec_step(const LinrecStepArgs& a, cudaStream_t stream);
 // Beam search (beam.cu).
 size_t beam_select_bytes(int32_t B, int32_t K, int32_t V, int32_t num_out);
