@@ -15,12 +15,15 @@
 // multiplied by zero: a state that is not finite stays in its sequence), and a
 // tile with such a token needs nothing from before it for what follows.
 //
-// Between tiles: each publishes its (A, B), looks back over the tiles before it
-// for the nearest state that is already known, and applies the (A, B) of the
-// tiles between in token order.  The arithmetic is the same whichever tile that
-// is, so results do not depend on timing.  Tiles are handed out in time order by
-// a ticket, so a tile's predecessors are always running or done; every wait is
-// bounded all the same.
+// Between tiles: each publishes its (A, B) as one 8-byte record a channel, and once
+// the state that leaves it is known, that state as the map (0, h).  A tile reads
+// the records of the eight tiles before it (a warp each), as far back as it takes
+// to meet a map with A = 0, and applies them in token order: the arithmetic is
+// the same wherever that is, so results do not depend on timing.  A record is one
+// atomic word that is valid as soon as it is not the pattern the workspace was
+// filled with, so neither side needs a fence (with flags and fences a tile took
+// 13.7 us instead of 4.4).  Tiles are handed out in time order by a ticket, so a
+// tile's predecessors are always running or done; every wait is bounded all the same.
 //
 // The backward pass is the same recurrence on reversed tokens:
 // r_t = a_t (dy_t + r_{t+1}), g_t = dy_t + r_{t+1}, with dS_T replacing r at a
@@ -34,39 +37,32 @@ namespace kda {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRows = LINREC_CHUNK / kWarps;   // tokens a warp
+constexpr int kFwdRows = 32;   // tokens a warp
+constexpr int kBwdRows = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSelfCheck = 1024;   // most sequences whose offsets every CTA checks by itself
 constexpr uint64_t kWaitNs = 2000000000ull;
-static_assert(kRows == 16, "row masks and the four-row groups are written for 16");
+static_assert(kWarps * kFwdRows % LINREC_CHUNK == 0 && kWarps * kBwdRows == LINREC_CHUNK,
+              "the forward tiles hold whole chunks, a backward tile is one");
 
-// Head of the workspace: zeroed before each launch whose time axis has several tiles.
-//   [0, 4) status, [4, 8) ticket, [16, ..) uint32 flag[tiles][channel tiles]
-// then float2 agg[tiles][Dp] and float inc[tiles][Dp] (Dp: channels padded to tiles).
-enum : uint32_t { kNone = 0, kAggregate = 1, kInclusive = 2 };
-
+// The workspace, filled with 0xff bytes before each launch whose time axis has
+// several tiles (so the first ticket is 2^32 - 1, and a record that is all ones has
+// not been published: a computed NaN never has that pattern).
+//   [0, 4) status, [4, 8) ticket, [256, ..) uint64 record[tiles][Dp], Dp the
+//   channels padded to whole tiles: A in the low half, B in the high half
 struct TileSpace {
     int32_t* status;
     uint32_t* ticket;
-    uint32_t* flag;
-    float2* agg;
-    float* inc;
+    uint64_t* record;
     int32_t nt, ct;      // tiles along tokens and channels
     int64_t Dp;
 };
+constexpr size_t kRecords = 256;
 
 __device__ __forceinline__ uint64_t now_ns() {
     uint64_t t;
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
-}
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
-    return v;
-}
-__device__ __forceinline__ void st_release(uint32_t* p, uint32_t v) {
-    asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
 
 // VEC neighbouring channels in fp32; two take the packed instructions.
@@ -196,118 +192,130 @@ struct Gate<KDA_GATE_CHANNEL_LOG_BF16, VEC> {
     }
 };
 
-// How a warp's rows reach its registers.
-//   kStaged: 16-byte asynchronous copies into the warp's own part of shared
-//     memory, issued while the tile before is worked on (rows on a 16-byte
-//     grid: D a multiple of 8, and a head gate's d even)
-//   kDirect: plain loads
-enum : int { kDirect = 0, kStaged = 1 };
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {
-    const int n = on ? 16 : 0;   // 0: the destination is filled with zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
+// A warp's rows of x and dy lie in its own part of shared memory (R rows of 32
+// lanes x VEC channels; every lane reads back its own channels only), the gates in
+// registers: with both in registers only three CTAs fit an SM, which is enough to
+// keep HBM busy without the look-back but not with it.
+__device__ __forceinline__ uint32_t shared_addr(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool on) {
-    const int n = on ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                     : "memory");
 }
 __device__ __forceinline__ void copies_done() {
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
 }
 
-// Bytes of one warp's rows of an array of E-byte elements in shared memory.
-template <int E>
-constexpr int staged_bytes() { return kRows * 64 * E; }
-template <int GATE>
-constexpr int gate_bytes() {
-    return GATE == KDA_GATE_HEAD_F32 ? kRows * 32 * 4
-                                     : staged_bytes<GATE == KDA_GATE_CHANNEL_LOG_BF16 ? 2 : 4>();
-}
-
-// Issues the copies of a warp's 16 rows x 64 channels of src ([T][D], E-byte
-// elements) from token t0, channel c0; outside the tensor zeros.
-template <int E>
-__device__ __forceinline__ void stage_rows(uint32_t dst, const void* src, int64_t t0, int64_t T,
-                                           int64_t D, int64_t c0, int lane) {
-    constexpr int kPieces = 64 * E / 16;             // 16-byte pieces a row
-    constexpr int kStep = 32 / kPieces;              // rows a pass
-    const int row = lane / kPieces, piece = lane % kPieces;
-    const int64_t c = c0 + piece * (16 / E);
-    const char* p = static_cast<const char*>(src) + ((t0 + row) * D + c) * E;
-    const int64_t step = D * kStep * E;
-    const int left = c < D ? (int)(T - t0 < kRows ? T - t0 : kRows) - row : 0;
-    const uint32_t at = dst + row * 64 * E + piece * 16;
+// Starts the copies of rows [0, left) of src from element row0 (first row, first
+// channel of the tile; the same in all lanes) to dst.  Whole tiles on a 16-byte grid
+// go in 16-byte pieces, others by each lane's own channels.
+template <int R, typename T, int VEC>
+__device__ __forceinline__ void stage_rows(T* dst, const void* src, int64_t row0, int64_t D,
+                                           bool wide, int left, bool on, int lane) {
+    constexpr int E = sizeof(T);
+    if (VEC == 2 && wide) {
+        constexpr int kPieces = 64 * E / 16;     // 16-byte pieces a row
+        constexpr int kStep = 32 / kPieces;      // rows a pass
+        const int row = lane / kPieces, piece = lane % kPieces;
+        const char* q = static_cast<const char*>(src) + (row0 + row * D) * E + piece * 16;
+        const uint32_t at = shared_addr(dst) + lane * 16;
 #pragma unroll
-    for (int j = 0; j < kRows / kStep; ++j) {
-        const bool on = j * kStep < left;
-        copy16(at + j * kStep * 64 * E, on ? p : src, on);
-        p += step;
+        for (int j = 0; j < R / kStep; ++j)
+            copy_async<16>(at + j * 512, q + j * kStep * D * E);
+        return;
     }
-}
-// A head gate: lane's own head, one value a row.
-__device__ __forceinline__ void stage_heads(uint32_t dst, const void* src, int64_t t0, int64_t T,
-                                            int H, int head, bool on, int lane) {
-    const char* p = static_cast<const char*>(src) + (t0 * H + head) * 4;
-    const int left = on ? (int)(T - t0 < kRows ? T - t0 : kRows) : 0;
+    const T* q = static_cast<const T*>(src) + row0 + lane * VEC;
+    T* d = dst + lane * VEC;
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        copy4(dst + (r * 32 + lane) * 4, r < left ? p : src, r < left);
-        p += H * 4;
-    }
-}
-
-// One warp's rows of an array in registers: from its staged copy, or by plain
-// loads (left: rows to read, 0 for a lane without channels).
-template <int PATH, typename T, int VEC>
-__device__ __forceinline__ void take_rows(Piece<T, VEC> (&x)[kRows], const char* staged,
-                                          const void* src, int64_t at, int64_t D, int left,
-                                          int lane) {
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-        if (PATH == kStaged) {
-            x[r].load(reinterpret_cast<const T*>(staged) + r * 64 + lane * VEC);
-        } else {
-            x[r] = Piece<T, VEC>{};
-            if (r < left) x[r].load(static_cast<const T*>(src) + at + r * D);
+    for (int r = 0; r < R; ++r) {
+        if (on && r < left) {
+            if constexpr (VEC * E >= 4) copy_async<VEC * E>(shared_addr(d + r * 32 * VEC), q + r * D);
+            else d[r * 32 * VEC] = q[r * D];
         }
     }
 }
-template <int PATH, int GATE, int VEC>
-__device__ __forceinline__ void take_gate(Gate<GATE, VEC> (&a)[kRows], const char* staged,
-                                          const void* src, int64_t t0, int64_t D, int64_t ch,
-                                          int H, int d, int left, int lane) {
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<VEC> staged(const T* rows, int r, int lane) {
+    Piece<T, VEC> q;
+    q.load(rows + r * 32 * VEC + lane * VEC);
+    return q.get();
+}
+
+// The gates of a warp's rows, in registers.
+template <int R, int GATE, int VEC>
+__device__ __forceinline__ void take_gate(Gate<GATE, VEC> (&a)[R], const LinrecArgs& p,
+                                          int64_t t0, int64_t D, int c0, bool full, int left,
+                                          bool on, int lane) {
     if constexpr (GATE == KDA_GATE_HEAD_F32) {
-        const int h0 = (int)(ch / d), h1 = (int)((ch + VEC - 1) / d);
+        const int ch = c0 + lane * VEC, last = (int)D - 1;
+        const int h0 = min(ch, last) / p.d, h1 = min(ch + VEC - 1, last) / p.d;
+        const float* g = static_cast<const float*>(p.gate) + t0 * p.H;
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            if (PATH == kStaged) {
-                a[r].f = fill<VEC>(reinterpret_cast<const float*>(staged)[r * 32 + lane]);
-            } else {
-                a[r].f = fill<VEC>(0.f);
-                if (r < left) {
-                    const float* g = static_cast<const float*>(src) + (t0 + r) * H;
-                    a[r].f.v[0] = g[h0];
-                    a[r].f.v[VEC - 1] = g[h1];
-                }
+        for (int r = 0; r < R; ++r) {
+            a[r].f = fill<VEC>(0.f);
+            if (full || r < left) {
+                a[r].f.v[0] = g[r * p.H + h0];
+                a[r].f.v[VEC - 1] = VEC == 2 && h1 != h0 ? g[r * p.H + h1] : a[r].f.v[0];
             }
         }
-    } else if constexpr (GATE == KDA_GATE_CHANNEL_LOG_BF16) {
-        Piece<__nv_bfloat16, VEC> raw[kRows];
-        take_rows<PATH, __nv_bfloat16, VEC>(raw, staged, src, t0 * D + ch, D, left, lane);
+    } else {
+        using G = std::conditional_t<GATE == KDA_GATE_CHANNEL_LOG_BF16, __nv_bfloat16, float>;
+        const G* g = static_cast<const G*>(p.gate) + t0 * D + c0;
+        Piece<G, VEC> q[R];
+        if (full) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) {
-            a[r].raw = raw[r];
-            const Vec<VEC> la = raw[r].get();
+            for (int r = 0; r < R; ++r) q[r].load(g + r * D + lane * VEC);
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                q[r] = Piece<G, VEC>{};
+                if (on && r < left) q[r].load(g + r * D + lane * VEC);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if constexpr (GATE == KDA_GATE_CHANNEL_LOG_BF16) a[r].raw = q[r];
+            else a[r].f = q[r].get();
+        }
+    }
+}
+// Once all loads are under way: a from log a.
+template <int R, int GATE, int VEC>
+__device__ __forceinline__ void expand_gate(Gate<GATE, VEC> (&a)[R]) {
+    if constexpr (GATE == KDA_GATE_CHANNEL_LOG_BF16) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const Vec<VEC> la = a[r].raw.get();
 #pragma unroll
             for (int v = 0; v < VEC; ++v) a[r].f.v[v] = expf(la.v[v]);
         }
-    } else {
-        Piece<float, VEC> raw[kRows];
-        take_rows<PATH, float, VEC>(raw, staged, src, t0 * D + ch, D, left, lane);
+    }
+}
+
+// The inputs u = (1 - a) x of the complement, in fp32 over the 4 bytes a value that
+// the warp's rows have (bf16 values were copied into the upper half, and the lower
+// rows are written before the upper ones are read).
+template <int R, typename T, int GATE, int VEC>
+__device__ __forceinline__ void complement_rows(float* u, const T* x, const Gate<GATE, VEC> (&a)[R],
+                                                int lane) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) a[r].f = raw[r].get();
+    for (int half = 0; half < 2; ++half) {
+        Piece<T, VEC> q[R / 2];
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r)
+            q[r].load(x + (half * (R / 2) + r) * 32 * VEC + lane * VEC);
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < R / 2; ++r) {
+            const int row = half * (R / 2) + r;
+            store(u + row * 32 * VEC + lane * VEC, mul(a[row].na(), q[r].get()));
+        }
     }
 }
 
@@ -367,11 +375,12 @@ struct Rows {
     uint32_t start, last;
     int n, live;
 };
+template <int R>
 __device__ __forceinline__ Rows rows_of(const Offsets& o, const int32_t* cu, int N, int64_t t0,
                                         int64_t end, int lane) {
     Rows w;
     const int64_t t = t0 + lane;
-    const bool live = lane < kRows && t < end;
+    const bool live = lane < R && t < end;
     bool s = false, l = false;
     w.n = 0;
     if (live) {
@@ -381,8 +390,15 @@ __device__ __forceinline__ Rows rows_of(const Offsets& o, const int32_t* cu, int
     }
     w.start = __ballot_sync(0xffffffffu, s);
     w.last = __ballot_sync(0xffffffffu, l);
-    w.live = end <= t0 ? 0 : end - t0 < kRows ? (int)(end - t0) : kRows;
+    w.live = end <= t0 ? 0 : end - t0 < R ? (int)(end - t0) : R;
     return w;
+}
+
+// The status word: without a fill of the workspace it is simply set; else it turns
+// from the fill's pattern to OK unless an error was recorded before.
+__device__ __forceinline__ void clear_status(const TileSpace& w, int N) {
+    if (w.nt == 1 && N <= kSelfCheck) *w.status = KDA_OK;
+    else atomicCAS(reinterpret_cast<uint32_t*>(w.status), ~0u, (uint32_t)KDA_OK);
 }
 
 // dst[n] = src[n] (zeros without src) for the sequences without tokens.
@@ -395,252 +411,319 @@ __device__ void copy_empty(const int32_t* cu, int N, int64_t D, const float* src
     }
 }
 
-// One warp finds the state that enters tile i of channel tile c: the nearest tile
-// before it (in scan order, step = -1: towards lower indices, +1: higher) whose
-// state is known, then the maps of the tiles between.  Lane's VEC channels from
-// ch.  Gives zeros when the wait ran out or another warp's did.
+// Records of a lane's VEC channels.
 template <int VEC>
-__device__ Vec<VEC> look_back(const TileSpace& w, int i, int c, int step, int64_t ch, int lane) {
-    Vec<VEC> H = fill<VEC>(0.f);
-    int base = i + step;   // lane j looks at base + j * step
-    int found = -1;
-    uint64_t t0 = 0;
-    for (uint32_t round = 0;; ++round) {
-        const int idx = base + lane * step;
-        uint32_t f = kNone;
-        if (idx >= 0 && idx < w.nt) f = ld_acquire(w.flag + (int64_t)idx * w.ct + c);
-        const uint32_t inc = __ballot_sync(0xffffffffu, f == kInclusive);
-        const uint32_t any = __ballot_sync(0xffffffffu, f != kNone);
-        if (inc) {
-            const int first = __ffs(inc) - 1;
-            const uint32_t before = (1u << first) - 1;
-            if ((any & before) == before) {
-                found = base + first * step;
-                break;
-            }
-        } else if (any == 0xffffffffu) {
-            base += 32 * step;
-            continue;
-        }
-        if ((round & 63) == 63) {
-            // bounded: give up after kWaitNs, or as soon as another wait has
-            const uint64_t t = now_ns();
-            if (t0 == 0) t0 = t;
-            int stop = 0;
-            if (lane == 0) {
-                if (t - t0 > kWaitNs) atomicExch(w.status, (int32_t)KDA_ERR_DEVICE_TIMEOUT);
-                stop = *reinterpret_cast<volatile int32_t*>(w.status) != 0;
-            }
-            if (__shfl_sync(0xffffffffu, stop, 0)) return H;
-        }
+struct Record {
+    uint64_t r[VEC];
+    __device__ __forceinline__ void read(const uint64_t* p) {
+        if constexpr (VEC == 2)
+            asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];"
+                         : "=l"(r[0]), "=l"(r[1]) : "l"(p) : "memory");
+        else
+            asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(r[0]) : "l"(p) : "memory");
     }
-    __syncwarp();
-    // the padded channels have entries too, so every lane reads
+    __device__ __forceinline__ void write(uint64_t* p) const {
+        if constexpr (VEC == 2)
+            asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};"
+                         ::"l"(p), "l"(r[0]), "l"(r[1]) : "memory");
+        else
+            asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(r[0]) : "memory");
+    }
+    __device__ __forceinline__ bool ready() const {
+        bool all = true;
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) H.v[v] = __ldcg(w.inc + (int64_t)found * w.Dp + ch + v);
-    for (int k = found - step; k != i; k -= step) {
+        for (int v = 0; v < VEC; ++v) all &= r[v] != ~0ull;
+        return all;
+    }
+    __device__ __forceinline__ void set(const Vec<VEC>& A, const Vec<VEC>& B) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            const float2 m = __ldcg(w.agg + (int64_t)k * w.Dp + ch + v);
-            H.v[v] = fmaf(m.x, H.v[v], m.y);
-        }
+        for (int v = 0; v < VEC; ++v)
+            r[v] = (uint64_t)__float_as_uint(B.v[v]) << 32 | __float_as_uint(A.v[v]);
     }
-    return H;
-}
-
-// Publishes a tile's map or its leaving state (one warp).
-template <int VEC>
-__device__ __forceinline__ void publish(const TileSpace& w, int i, int c, int64_t ch, int lane,
-                                        uint32_t kind, const Vec<VEC>& A, const Vec<VEC>& B) {
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        if (kind == kInclusive) w.inc[(int64_t)i * w.Dp + ch + v] = B.v[v];
-        else w.agg[(int64_t)i * w.Dp + ch + v] = make_float2(A.v[v], B.v[v]);
-    }
-    __threadfence();
-    __syncwarp();
-    if (lane == 0) st_release(w.flag + (int64_t)i * w.ct + c, kind);
-}
-
-// Warp maps of a tile.  Two buffers, for tiles in turn, save the barrier between
-// one tile's last reads and the next one's writes.
-template <int VEC, int BUFS>
-struct Maps {
-    Vec<VEC> A[BUFS][kWarps][32];
-    Vec<VEC> B[BUFS][kWarps][32];
-    uint32_t reset[BUFS][kWarps];   // the warp's rows hold a boundary: B alone counts
-
-    __device__ __forceinline__ void put(int buf, int warp, int lane, const Vec<VEC>& a,
-                                        const Vec<VEC>& b, uint32_t boundary) {
-        A[buf][warp][lane] = a;
-        B[buf][warp][lane] = b;
-        if (lane == 0) reset[buf][warp] = boundary;
-    }
-    // The state after warp j's rows from the state before them.
-    __device__ __forceinline__ Vec<VEC> step(int buf, int j, int lane, const Vec<VEC>& h) const {
-        const Vec<VEC> b = B[buf][j][lane];
-        return reset[buf][j] ? b : fma(A[buf][j][lane], h, b);
+    __device__ __forceinline__ float A(int v) const { return __uint_as_float((uint32_t)r[v]); }
+    __device__ __forceinline__ float B(int v) const {
+        return __uint_as_float((uint32_t)(r[v] >> 32));
     }
 };
 
+// A product of gates as published: a NaN in its one computed form, not all ones.
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> known(Vec<VEC> A) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v)
+        if (isnan(A.v[v])) A.v[v] = __uint_as_float(0x7fffffffu);
+    return A;
+}
+
+// Publishes a tile's map, or with A = 0 the state that leaves it (one warp).
+template <int VEC>
+__device__ __forceinline__ void publish(const TileSpace& w, int i, int64_t ch,
+                                        const Vec<VEC>& A, const Vec<VEC>& B) {
+    Record<VEC> r;
+    r.set(A, B);
+    r.write(w.record + (int64_t)i * w.Dp + ch);
+}
+
+// The state that enters tile i, for the lane's VEC channels from ch: warp j waits
+// for the record of the tile j + 1 steps before (step = -1: towards lower indices,
+// +1: higher), then every warp applies the eight from the farthest to the nearest;
+// a map with A = 0 is where the walk can end.  Tiles from `tiles` on hold no
+// sequence and publish nothing.  All warps call it together.  When a
+// wait runs out, here or elsewhere, the status word says so and the walk ends.
+template <int VEC>
+__device__ Vec<VEC> look_back(const TileSpace& w, int i, int step, int64_t tiles, int64_t ch,
+                              int warp, int lane, Record<VEC> (*records)[32]) {
+    for (int far = 0;; far += kWarps) {
+        if (far) __syncthreads();   // the records before are read
+        const int64_t idx = i + (int64_t)step * (far + warp + 1);
+        Record<VEC> r;
+        r.set(fill<VEC>(0.f), fill<VEC>(0.f));
+        bool stop = false;
+        if (idx >= 0 && idx < tiles) {
+            const uint64_t* p = w.record + idx * w.Dp + ch;
+            uint64_t t0 = 0;
+            r.read(p);
+            for (uint32_t round = 1; !r.ready(); ++round) {
+                if ((round & 63) == 0) {
+                    const uint64_t t = now_ns();
+                    if (t0 == 0) t0 = t;
+                    if (t - t0 > kWaitNs) atomicExch(w.status, (int32_t)KDA_ERR_DEVICE_TIMEOUT);
+                    if (*reinterpret_cast<volatile int32_t*>(w.status) == KDA_ERR_DEVICE_TIMEOUT) {
+                        stop = true;
+                        break;
+                    }
+                }
+                r.read(p);
+            }
+        }
+        records[warp][lane] = r;
+        if (__syncthreads_or(stop)) return fill<VEC>(0.f);
+        bool open = false;   // a channel whose walk goes on past these eight
+        Vec<VEC> H = fill<VEC>(0.f);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            bool met = false;
+#pragma unroll
+            for (int j = kWarps - 1; j >= 0; --j) {
+                const Record<VEC>& q = records[j][lane];
+                const bool last = q.A(v) == 0.f;
+                met |= last;
+                H.v[v] = last ? q.B(v) : fmaf(q.A(v), H.v[v], q.B(v));
+            }
+            open |= !met;
+        }
+        if (!__any_sync(0xffffffffu, open)) {   // the same answer in every warp
+            if (far == 0) return H;
+            // the farther records once more, all known by now, in token order
+            H = fill<VEC>(0.f);
+            for (int j = far + kWarps; j >= 1; --j) {
+                const int64_t k = i + (int64_t)step * j;
+                if (k < 0 || k >= tiles) continue;
+                Record<VEC> q;
+                q.read(w.record + k * w.Dp + ch);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    H.v[v] = q.A(v) == 0.f ? q.B(v) : fmaf(q.A(v), H.v[v], q.B(v));
+            }
+            return H;
+        }
+    }
+}
+
+// Warp maps of a tile.
+template <int VEC>
+struct Maps {
+    Vec<VEC> A[kWarps][32];
+    Vec<VEC> B[kWarps][32];
+    uint32_t reset[kWarps];   // the warp's rows hold a boundary: B alone counts
+
+    __device__ __forceinline__ void put(int warp, int lane, const Vec<VEC>& a, const Vec<VEC>& b,
+                                        uint32_t boundary) {
+        A[warp][lane] = a;
+        B[warp][lane] = b;
+        if (lane == 0) reset[warp] = boundary;
+    }
+    // The state after warp j's rows from the state before them.
+    __device__ __forceinline__ Vec<VEC> step(int j, int lane, const Vec<VEC>& h) const {
+        const Vec<VEC> b = B[j][lane];
+        return reset[j] ? b : fma(A[j][lane], h, b);
+    }
+};
+
+// Tickets count from the filled workspace's 2^32 - 1.
+__device__ __forceinline__ uint32_t take_ticket(const TileSpace& w) {
+    return atomicAdd(w.ticket, 1u) + 1u;
+}
 // The first tile of a CTA, broadcast: with several tiles along time by ticket.
 __device__ __forceinline__ int64_t first_tile(const TileSpace& w, uint32_t* shared) {
     if (w.nt == 1) return blockIdx.x;
-    if (threadIdx.x == 0) *shared = atomicAdd(w.ticket, 1u);
+    if (threadIdx.x == 0) *shared = take_ticket(w);
     __syncthreads();
     return *shared;
 }
 
-// CTAs an SM: 48 registers a thread hold a tile of bf16 inputs (32 of gates, 16 of
-// inputs), so that three CTAs fit; fp32 inputs, and log gates with the complement,
-// which keep both log a and a, leave room for two.
-template <typename T, int GATE, bool COMP, int PATH>
-constexpr int fwd_ctas() {
-    return PATH == kStaged && sizeof(T) == 2 && !(COMP && GATE == KDA_GATE_CHANNEL_LOG_BF16) ? 3 : 2;
-}
+// Values that replace the carried one at a boundary row (S0 at a first token, dS_T at a
+// last one): that of the first boundary among the warp's rows is loaded with the
+// tile, those of more (sequences shorter than the warp's rows) when they are met.
+template <int VEC>
+struct Boundary {
+    Vec<VEC> value;
+    int row;
+    __device__ __forceinline__ Boundary(const float* src, uint32_t mask, int n, int64_t D, int ch,
+                                        bool on) {
+        row = __ffs(mask) - 1;
+        value = fill<VEC>(0.f);
+        if (row >= 0) value = load(src, row, n, D, ch, on);
+    }
+    __device__ __forceinline__ static Vec<VEC> load(const float* src, int r, int n, int64_t D,
+                                                    int ch, bool on) {
+        const int64_t seq = __shfl_sync(0xffffffffu, n, r);
+        return src && on ? load_f32<VEC>(src + seq * D + ch) : fill<VEC>(0.f);
+    }
+    __device__ __forceinline__ Vec<VEC> at(int r, const float* src, int n, int64_t D, int ch,
+                                           bool on) const {
+        return r == row ? value : load(src, r, n, D, ch, on);
+    }
+};
 
-template <typename T, int GATE, bool COMP, int VEC, int PATH>
-__global__ void __launch_bounds__(kThreads, fwd_ctas<T, GATE, COMP, PATH>())
+// Rows of x in shared memory; of the complement the inputs u, in fp32.
+template <typename T, bool COMP, int VEC>
+struct FwdRows {
+    static constexpr int R = kFwdRows;
+    static constexpr int kBytes = R * 32 * VEC * (COMP ? 4 : (int)sizeof(T));
+    // the copies land in the upper half of a row area twice as large
+    static constexpr int kAt = COMP ? kBytes - R * 32 * VEC * (int)sizeof(T) : 0;
+};
+
+template <typename T, int GATE, bool COMP, int VEC>
+__global__ void __launch_bounds__(kThreads, 2)
 linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
-    extern __shared__ __align__(16) char staging[];
+    constexpr int R = kFwdRows, kTile = kWarps * R;
+    using Area = FwdRows<T, COMP, VEC>;
+    using U = std::conditional_t<COMP, float, T>;
+    extern __shared__ __align__(16) char row_area[];
     __shared__ Offsets off;
-    __shared__ Maps<VEC, 2> maps;
-    __shared__ Vec<VEC> carry[32];
+    __shared__ Maps<VEC> maps;
+    __shared__ Record<VEC> records[kWarps][32];
     __shared__ uint32_t next_ticket;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int N = p.num_seqs;
     const int64_t D = (int64_t)p.H * p.d;
     const int32_t* cu = p.cu_seqlens;
-    constexpr int kX = staged_bytes<sizeof(T)>();
-    char* sx = staging + warp * (kX + gate_bytes<GATE>());
-    char* sg = sx + kX;
-    const uint32_t sx32 = (uint32_t)__cvta_generic_to_shared(sx);
-
-    auto stage = [&](int64_t tile) {
-        if constexpr (PATH == kStaged) {
-            const int i = (int)(tile / w.ct), c = (int)(tile % w.ct);
-            const int64_t t0 = (int64_t)i * LINREC_CHUNK + warp * kRows, c0 = (int64_t)c * 64;
-            const int64_t T_ = p.total_tokens;
-            stage_rows<sizeof(T)>(sx32, p.x, t0, T_, D, c0, lane);
-            if constexpr (GATE == KDA_GATE_HEAD_F32) {
-                const int64_t ch = c0 + lane * 2;
-                stage_heads(sx32 + kX, p.gate, t0, T_, p.H, ch < D ? (int)(ch / p.d) : 0, ch < D,
-                            lane);
-            } else {
-                stage_rows<GATE == KDA_GATE_CHANNEL_LOG_BF16 ? 2 : 4>(sx32 + kX, p.gate, t0, T_, D,
-                                                                      c0, lane);
-            }
-        }
-    };
+    U* u = reinterpret_cast<U*>(row_area + warp * Area::kBytes);
+    T* x = reinterpret_cast<T*>(row_area + warp * Area::kBytes + Area::kAt);
 
     const int64_t tiles = (int64_t)w.nt * w.ct;
     int64_t tile = first_tile(w, &next_ticket);
-    if (tile < tiles) stage(tile);
     if (!read_offsets(off, cu, N, p.total_tokens, w.status)) {
-        copies_done();
         if (blockIdx.x == 0 && threadIdx.x == 0) *w.status = KDA_ERR_DEVICE_INPUT;
         return;
     }
-    if (w.nt == 1 && N <= kSelfCheck && blockIdx.x == 0 && threadIdx.x == 0) *w.status = KDA_OK;
-    const int64_t end = cu[N];
+    if (blockIdx.x == 0 && threadIdx.x == 0) clear_status(w, N);
+    const int64_t end = cu[N], live_tiles = (end + kTile - 1) / kTile;
     copy_empty(cu, N, D, p.S0, p.S_T);
 
-    for (int buf = 0; tile < tiles; buf ^= 1) {
-        const int i = (int)(tile / w.ct), c = (int)(tile % w.ct);
-        const int64_t t0 = (int64_t)i * LINREC_CHUNK + warp * kRows;
-        const int64_t ch = (int64_t)c * 32 * VEC + lane * VEC;   // this lane's channels
+    while (tile < tiles) {
+        const int i = (int)((uint32_t)tile / (uint32_t)w.ct);
+        const int64_t t0 = (int64_t)i * kTile + warp * R;
+        const int c0 = (int)((uint32_t)tile % (uint32_t)w.ct) * 32 * VEC;
+        const int ch = c0 + lane * VEC;   // this lane's channels
         const bool on = ch < D;
-        const Rows rows = rows_of(off, cu, N, t0, end, lane);
-        const bool edge = (rows.start | rows.last) != 0 || rows.live < kRows;
+        const int left = t0 < end ? (int)min(end - t0, (int64_t)R) : 0;
+        const bool full = left == R && c0 + 32 * VEC <= D;
 
-        // the tile, into registers
-        Piece<T, VEC> x[kRows];
-        Gate<GATE, VEC> a[kRows];
-        if (PATH == kStaged) {
-            copies_done();
-            __syncwarp();
-        }
-        const int left = on ? rows.live : 0;
-        take_rows<PATH, T, VEC>(x, sx, p.x, t0 * D + ch, D, left, lane);
-        take_gate<PATH, GATE, VEC>(a, sg, p.gate, t0, D, ch, p.H, p.d, left, lane);
-        auto input = [&](int r) {
-            if constexpr (COMP) return mul(a[r].na(), x[r].get());
-            else return x[r].get();
-        };
+        stage_rows<R, T, VEC>(x, p.x, t0 * D + c0, D, full && D % 8 == 0, left, on, lane);
+        const Rows rows = rows_of<R>(off, cu, N, t0, end, lane);
+        const bool edge = (rows.start | rows.last) != 0 || !full;
+        const Boundary<VEC> first_start(p.S0, rows.start, rows.n, D, ch, on);
+        Gate<GATE, VEC> a[R];
+        take_gate<R, GATE, VEC>(a, p, t0, D, c0, full, left, on, lane);
+        expand_gate<R, GATE, VEC>(a);
+        copies_done();
+        if constexpr (COMP) complement_rows<R, T, GATE, VEC>(u, x, a, lane);
+        auto input = [&](int r) { return staged<U, VEC>(u, r, lane); };
         // the state that replaces the carried one at a sequence's first token
-        auto start = [&](int r) {
-            Vec<VEC> h0 = fill<VEC>(0.f);
-            const int n = __shfl_sync(0xffffffffu, rows.n, r);
-            if (p.S0 && on) h0 = load_f32<VEC>(p.S0 + n * D + ch);
-            return h0;
-        };
+        auto start = [&](int r) { return first_start.at(r, p.S0, rows.n, D, ch, on); };
 
         Vec<VEC> A = fill<VEC>(1.f), B = fill<VEC>(0.f);
         if (!edge) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < R; ++r) {
                 B = fma(a[r].a(), B, input(r));
                 A = mul(A, a[r].a());
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < R; ++r) {
                 if (rows.start >> r & 1) B = start(r);
                 B = fma(a[r].a(), B, input(r));
                 A = mul(A, a[r].a());
             }
         }
-        maps.put(buf, warp, lane, A, B, rows.start);
-        if (threadIdx.x == 32 && w.nt > 1) next_ticket = atomicAdd(w.ticket, 1u);
+        maps.put(warp, lane, A, B, rows.start);
         __syncthreads();
-        tile = w.nt > 1 ? (int64_t)next_ticket : tile + gridDim.x;
-        if (tile < tiles) stage(tile);   // the warp's rows are in registers: their place is free
 
-        if (warp == 0) {
-            bool reset = false;
+        // a state enters the tile, unless its first row starts a sequence; the first
+        // warp hands the tile's map on, and later the state that leaves it
+        const int64_t first = (int64_t)i * kTile;
+        const bool needed = first < end && !(maps.reset[0] & 1);
+        const bool wanted = w.nt > 1 && first + kTile < end;
+        bool reset = false;
+        if (warp == 0 && wanted) {
             A = fill<VEC>(1.f);
             B = fill<VEC>(0.f);
 #pragma unroll
             for (int j = 0; j < kWarps; ++j) {
-                reset |= maps.reset[buf][j] != 0;
-                B = maps.step(buf, j, lane, B);
-                A = mul(A, maps.A[buf][j][lane]);
+                reset |= maps.reset[j] != 0;
+                B = maps.step(j, lane, B);
+                A = mul(A, maps.A[j][lane]);
             }
-            const bool needed = t0 < end && !(rows.start & 1);   // row 0 continues a sequence
-            const bool wanted = w.nt > 1 && t0 + LINREC_CHUNK < end;   // a tile comes after
-            Vec<VEC> H = fill<VEC>(0.f);
-            if (wanted) publish<VEC>(w, i, c, ch, lane, reset ? kInclusive : kAggregate, A, B);
-            if (needed) {
-                H = look_back<VEC>(w, i, c, -1, ch, lane);
-                if (wanted && !reset)
-                    publish<VEC>(w, i, c, ch, lane, kInclusive, A, fma(A, H, B));
-            }
-            if (p.states && on) store(p.states + i * D + ch, H);
-            carry[lane] = H;
+            if (reset) A = fill<VEC>(0.f);
+            publish<VEC>(w, i, ch, known(A), B);
         }
-        __syncthreads();
-
-        Vec<VEC> h = carry[lane];
-        for (int j = 0; j < warp; ++j) h = maps.step(buf, j, lane, h);
-        T* y = p.y ? static_cast<T*>(p.y) + t0 * D + ch : nullptr;
-        if (!edge) {
+        Vec<VEC> h = fill<VEC>(0.f);
+        if (needed) {
+            h = look_back<VEC>(w, i, -1, live_tiles, ch, warp, lane, records);
+            if (warp == 0 && wanted && !reset) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                h = fma(a[r].a(), h, input(r));
-                if (on && y) store(y + r * D, h);
+                for (int v = 0; v < VEC; ++v)
+                    if (A.v[v] != 0.f) B.v[v] = fmaf(A.v[v], h.v[v], B.v[v]);
+                publish<VEC>(w, i, ch, fill<VEC>(0.f), B);
+            }
+        }
+        // The next tile is claimed only now: a tile claimed before the look-back would
+        // not be started while this CTA waits, and its successors would wait for both
+        // (that made the long prefill twice as slow).
+        if (threadIdx.x == 0 && w.nt > 1) next_ticket = take_ticket(w);
+
+        for (int j = 0; j < warp; ++j) h = maps.step(j, lane, h);
+        if (p.states && on && t0 % LINREC_CHUNK == 0 && t0 < p.total_tokens)
+            store(p.states + t0 / LINREC_CHUNK * D + ch,
+                  t0 < end && !(rows.start & 1) ? h : fill<VEC>(0.f));
+        T* y = p.y ? static_cast<T*>(p.y) + (t0 * D + c0) : nullptr;
+        if (!edge) {
+            if (y) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    h = fma(a[r].a(), h, input(r));
+                    store(y + r * D + lane * VEC, h);
+                }
             }
         } else {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < R; ++r) {
                 if (rows.start >> r & 1) h = start(r);
                 h = fma(a[r].a(), h, input(r));
-                if (on && y && r < rows.live) store(y + r * D, h);
+                if (on && y && r < left) store(y + r * D + lane * VEC, h);
                 if (rows.last >> r & 1) {
                     const int n = __shfl_sync(0xffffffffu, rows.n, r);
                     if (p.S_T && on) store(p.S_T + n * D + ch, h);
                 }
             }
         }
+        __syncthreads();   // maps, records and the ticket: this tile is done with them
+        tile = w.nt > 1 ? (int64_t)next_ticket : tile + gridDim.x;
     }
 }
 
@@ -651,218 +734,209 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
 //     that neither divide 64 nor are a multiple of it)
 enum : int { kNoHead = 0, kHeadRow = 1, kHeadWide = 2 };
 
-template <typename T, int GATE, bool COMP, int VEC, int PATH>
-__global__ void __launch_bounds__(kThreads, 2)
+// Per warp: rows of x and dy as stored, and of f in fp32 (see below).  Three CTAs an SM
+// with bf16 inputs, two with fp32 ones.
+template <typename T, int VEC>
+struct BwdRows {
+    static constexpr int R = kBwdRows;
+    static constexpr int kRaw = R * 32 * VEC * (int)sizeof(T), kF = R * 32 * VEC * 4;
+    static constexpr int kBytes = 2 * kRaw + kF;
+    static constexpr int kCtas = sizeof(T) == 2 ? 3 : 2;
+};
+
+template <typename T, int GATE, bool COMP, int VEC>
+__global__ void __launch_bounds__(kThreads, BwdRows<T, VEC>::kCtas)
 linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict__ states,
                   float* dgate, int head_mode) {
-    extern __shared__ __align__(16) char staging[];
+    constexpr int R = kBwdRows;
+    using Area = BwdRows<T, VEC>;
+    extern __shared__ __align__(16) char row_area[];
     __shared__ Offsets off;
-    // one buffer: with two, two CTAs of fp32 inputs would not fit an SM
-    __shared__ Maps<VEC, 1> maps;    // of the state, tokens forward
-    __shared__ Maps<VEC, 1> rmaps;   // of the gradient, tokens backward
-    __shared__ Vec<VEC> carry[32];
+    __shared__ Maps<VEC> maps;    // of the state, tokens forward
+    __shared__ Maps<VEC> rmaps;   // of the gradient, tokens backward
+    __shared__ Record<VEC> records[kWarps][32];
     __shared__ uint32_t next_ticket;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0);   // uniform
     const int N = p.num_seqs;
     const int64_t D = (int64_t)p.H * p.d;
     const int32_t* cu = p.cu_seqlens;
-    constexpr int kX = staged_bytes<sizeof(T)>();
-    char* sx = staging + warp * (2 * kX + gate_bytes<GATE>());
-    char* sy = sx + kX;
-    char* sg = sy + kX;
-    const uint32_t sx32 = (uint32_t)__cvta_generic_to_shared(sx);
-
-    auto stage = [&](int64_t tile) {
-        if constexpr (PATH == kStaged) {
-            const int i = w.nt - 1 - (int)(tile / w.ct), c = (int)(tile % w.ct);
-            const int64_t t0 = (int64_t)i * LINREC_CHUNK + warp * kRows, c0 = (int64_t)c * 64;
-            const int64_t T_ = p.total_tokens;
-            stage_rows<sizeof(T)>(sx32, p.x, t0, T_, D, c0, lane);
-            stage_rows<sizeof(T)>(sx32 + kX, p.dy, t0, T_, D, c0, lane);
-            if constexpr (GATE == KDA_GATE_HEAD_F32) {
-                const int64_t ch = c0 + lane * 2;
-                stage_heads(sx32 + 2 * kX, p.gate, t0, T_, p.H, ch < D ? (int)(ch / p.d) : 0,
-                            ch < D, lane);
-            } else {
-                stage_rows<GATE == KDA_GATE_CHANNEL_LOG_BF16 ? 2 : 4>(sx32 + 2 * kX, p.gate, t0,
-                                                                      T_, D, c0, lane);
-            }
-        }
-    };
+    T* x = reinterpret_cast<T*>(row_area + warp * Area::kBytes);
+    T* dy = reinterpret_cast<T*>(row_area + warp * Area::kBytes + Area::kRaw);
+    float* f = reinterpret_cast<float*>(row_area + warp * Area::kBytes + 2 * Area::kRaw);
 
     const int64_t tiles = (int64_t)w.nt * w.ct;
     int64_t tile = first_tile(w, &next_ticket);
-    if (tile < tiles) stage(tile);
     if (!read_offsets(off, cu, N, p.total_tokens, w.status)) {
-        copies_done();
         if (blockIdx.x == 0 && threadIdx.x == 0) *w.status = KDA_ERR_DEVICE_INPUT;
         return;
     }
-    if (w.nt == 1 && N <= kSelfCheck && blockIdx.x == 0 && threadIdx.x == 0) *w.status = KDA_OK;
-    const int64_t end = cu[N];
+    if (blockIdx.x == 0 && threadIdx.x == 0) clear_status(w, N);
+    const int64_t end = cu[N], live_tiles = (end + LINREC_CHUNK - 1) / LINREC_CHUNK;
     copy_empty(cu, N, D, p.dS_T, p.dS0);
 
     while (tile < tiles) {
-        const int i = w.nt - 1 - (int)(tile / w.ct), c = (int)(tile % w.ct);
-        const int64_t t0 = (int64_t)i * LINREC_CHUNK + warp * kRows;
-        const int64_t ch = (int64_t)c * 32 * VEC + lane * VEC;
+        const int i = w.nt - 1 - (int)((uint32_t)tile / (uint32_t)w.ct);
+        const int64_t t0 = (int64_t)i * LINREC_CHUNK + warp * R;
+        const int c0 = (int)((uint32_t)tile % (uint32_t)w.ct) * 32 * VEC;
+        const int ch = c0 + lane * VEC;
         const bool on = ch < D;
-        const Rows rows = rows_of(off, cu, N, t0, end, lane);
-        const bool edge = (rows.start | rows.last) != 0 || rows.live < kRows;
+        const int left = t0 < end ? (int)min(end - t0, (int64_t)R) : 0;
+        const bool full = left == R && c0 + 32 * VEC <= D;
+
+        stage_rows<R, T, VEC>(x, p.x, t0 * D + c0, D, full && D % 8 == 0, left, on, lane);
+        stage_rows<R, T, VEC>(dy, p.dy, t0 * D + c0, D, full && D % 8 == 0, left, on, lane);
+        const Rows rows = rows_of<R>(off, cu, N, t0, end, lane);
+        const bool edge = (rows.start | rows.last) != 0 || !full;
+        const Boundary<VEC> first_start(p.S0, rows.start, rows.n, D, ch, on);
+        const Boundary<VEC> first_last(p.dS_T, rows.last, rows.n, D, ch, on);
         Vec<VEC> H = fill<VEC>(0.f);   // the state that enters the tile
         if (on && (int64_t)i * LINREC_CHUNK < end) H = load_f32<VEC>(states + i * D + ch);
-
-        Piece<T, VEC> x[kRows], dy[kRows];
-        Gate<GATE, VEC> a[kRows];
-        if (PATH == kStaged) {
-            copies_done();
-            __syncwarp();
-        }
-        const int left = on ? rows.live : 0;
-        take_rows<PATH, T, VEC>(x, sx, p.x, t0 * D + ch, D, left, lane);
-        take_rows<PATH, T, VEC>(dy, sy, p.dy, t0 * D + ch, D, left, lane);
-        take_gate<PATH, GATE, VEC>(a, sg, p.gate, t0, D, ch, p.H, p.d, left, lane);
+        Gate<GATE, VEC> a[R];
+        take_gate<R, GATE, VEC>(a, p, t0, D, c0, full, left, on, lane);
+        expand_gate<R, GATE, VEC>(a);
+        copies_done();
         auto input = [&](int r) {
-            if constexpr (COMP) return mul(a[r].na(), x[r].get());
-            else return x[r].get();
+            const Vec<VEC> q = staged<T, VEC>(x, r, lane);
+            if constexpr (COMP) return mul(a[r].na(), q);
+            else return q;
         };
-        auto boundary = [&](const float* src, int r) {   // S0 or dS_T of row r's sequence
-            Vec<VEC> h0 = fill<VEC>(0.f);
-            const int n = __shfl_sync(0xffffffffu, rows.n, r);
-            if (src && on) h0 = load_f32<VEC>(src + n * D + ch);
-            return h0;
-        };
+        auto start = [&](int r) { return first_start.at(r, p.S0, rows.n, D, ch, on); };
+        auto behind = [&](int r) { return first_last.at(r, p.dS_T, rows.n, D, ch, on); };
 
         // maps of the warp's rows, both ways
         Vec<VEC> A = fill<VEC>(1.f), B = fill<VEC>(0.f), RB = fill<VEC>(0.f), RA = fill<VEC>(1.f);
         if (!edge) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
+            for (int r = 0; r < R; ++r) {
                 B = fma(a[r].a(), B, input(r));
                 A = mul(A, a[r].a());
             }
 #pragma unroll
-            for (int r = kRows - 1; r >= 0; --r) RB = mul(a[r].a(), add(dy[r].get(), RB));
+            for (int r = R - 1; r >= 0; --r)
+                RB = mul(a[r].a(), add(staged<T, VEC>(dy, r, lane), RB));
             RA = A;
         } else {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (rows.start >> r & 1) B = boundary(p.S0, r);
+            for (int r = 0; r < R; ++r) {
+                if (rows.start >> r & 1) B = start(r);
                 B = fma(a[r].a(), B, input(r));
                 A = mul(A, a[r].a());
             }
 #pragma unroll
-            for (int r = kRows - 1; r >= 0; --r) {
-                if (rows.last >> r & 1) RB = boundary(p.dS_T, r);
-                if (r < rows.live) {   // rows past the end hand on nothing
-                    RB = mul(a[r].a(), add(dy[r].get(), RB));
+            for (int r = R - 1; r >= 0; --r) {
+                if (rows.last >> r & 1) RB = behind(r);
+                if (r < left) {   // rows past the end hand on nothing
+                    RB = mul(a[r].a(), add(staged<T, VEC>(dy, r, lane), RB));
                     RA = mul(RA, a[r].a());
                 }
             }
         }
-        maps.put(0, warp, lane, A, B, rows.start);
-        rmaps.put(0, warp, lane, RA, RB, rows.last);
-        if (threadIdx.x == 0 && w.nt > 1) next_ticket = atomicAdd(w.ticket, 1u);
+        maps.put(warp, lane, A, B, rows.start);
+        rmaps.put(warp, lane, RA, RB, rows.last);
         __syncthreads();
-        tile = w.nt > 1 ? (int64_t)next_ticket : tile + gridDim.x;
-        if (tile < tiles) stage(tile);
 
-        if (warp == kWarps - 1) {
-            bool reset = false;
+        // a gradient enters the tile from behind, unless its last row ends a sequence
+        // (or lies past the last one); the last warp hands the tile's map on
+        const int64_t first = (int64_t)i * LINREC_CHUNK;
+        const bool needed = first + LINREC_CHUNK < end &&
+                            !(rmaps.reset[kWarps - 1] >> (R - 1) & 1);
+        const bool wanted = i > 0 && first < end;
+        bool reset = false;
+        if (warp == kWarps - 1 && wanted) {
             A = fill<VEC>(1.f);
             B = fill<VEC>(0.f);
 #pragma unroll
             for (int j = kWarps - 1; j >= 0; --j) {
-                reset |= rmaps.reset[0][j] != 0;
-                B = rmaps.step(0, j, lane, B);
-                A = mul(A, rmaps.A[0][j][lane]);
+                reset |= rmaps.reset[j] != 0;
+                B = rmaps.step(j, lane, B);
+                A = mul(A, rmaps.A[j][lane]);
             }
-            // the tile's last row goes on in the next tile; a tile comes before
-            const bool needed = t0 + kRows < end && !(rows.last >> (kRows - 1) & 1);
-            const bool wanted = i > 0 && (int64_t)i * LINREC_CHUNK < end;
-            Vec<VEC> R = fill<VEC>(0.f);
-            if (wanted) publish<VEC>(w, i, c, ch, lane, reset ? kInclusive : kAggregate, A, B);
-            if (needed) {
-                R = look_back<VEC>(w, i, c, +1, ch, lane);
-                if (wanted && !reset)
-                    publish<VEC>(w, i, c, ch, lane, kInclusive, A, fma(A, R, B));
-            }
-            carry[lane] = R;
+            if (reset) A = fill<VEC>(0.f);
+            publish<VEC>(w, i, ch, known(A), B);
         }
-        __syncthreads();
-
-        // what the gate multiplies at each row: the state before it, less x for the complement
-        Vec<VEC> f[kRows];
-        for (int j = 0; j < warp; ++j) H = maps.step(0, j, lane, H);
-        auto less_x = [&](const Vec<VEC>& prev, int r) {
-            if constexpr (!COMP) return prev;
-            Vec<VEC> q = x[r].get();
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) q.v[v] = prev.v[v] - q.v[v];
-            return q;
-        };
-        if (!edge) {
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                f[r] = less_x(H, r);
-                H = fma(a[r].a(), H, input(r));
-            }
-        } else {
-#pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                if (rows.start >> r & 1) H = boundary(p.S0, r);
-                f[r] = less_x(H, r);
-                H = fma(a[r].a(), H, input(r));
-            }
-        }
-        Vec<VEC> R = carry[lane];
-        for (int j = kWarps - 1; j > warp; --j) R = rmaps.step(0, j, lane, R);
-        __syncthreads();   // the maps are read: the next tile may write them
-        float* dx = p.dx + t0 * D + ch;
-        // row r's gradients from R, the gradient that comes from behind
-        auto row = [&](int r, bool out) {
-            const Vec<VEC> g = add(dy[r].get(), R);
+        // what the gate multiplies at each row, before the wait: the state before the
+        // row, less x for the complement
+        for (int j = 0; j < warp; ++j) H = maps.step(j, lane, H);
+        auto put_f = [&](int r) {
+            Vec<VEC> q = H;
             if constexpr (COMP) {
-                if (out) store(dx + r * D, mul(a[r].na(), g));
-            } else {
-                if (out) store(dx + r * D, g);
+                const Vec<VEC> xr = staged<T, VEC>(x, r, lane);
+#pragma unroll
+                for (int v = 0; v < VEC; ++v) q.v[v] = H.v[v] - xr.v[v];
             }
-            f[r] = mul(g, f[r]);
-            R = mul(a[r].a(), g);
-            if constexpr (GATE == KDA_GATE_CHANNEL_LOG_BF16) f[r] = mul(a[r].a(), f[r]);
-            if (GATE != KDA_GATE_HEAD_F32 || head_mode == kHeadWide)
-                if (out) store(dgate + (t0 + r) * D + ch, f[r]);
+            store(f + r * 32 * VEC + lane * VEC, q);
+            H = fma(a[r].a(), H, input(r));
         };
         if (!edge) {
 #pragma unroll
-            for (int r = kRows - 1; r >= 0; --r) row(r, on);
+            for (int r = 0; r < R; ++r) put_f(r);
         } else {
 #pragma unroll
-            for (int r = kRows - 1; r >= 0; --r) {
-                if (rows.last >> r & 1) R = boundary(p.dS_T, r);
-                if (r < rows.live) row(r, on);
+            for (int r = 0; r < R; ++r) {
+                if (rows.start >> r & 1) H = start(r);
+                put_f(r);
+            }
+        }
+        Vec<VEC> G = fill<VEC>(0.f);   // the gradient that comes from behind
+        if (needed) {
+            G = look_back<VEC>(w, i, +1, live_tiles, ch, warp, lane, records);
+            if (warp == kWarps - 1 && wanted && !reset) {
+#pragma unroll
+                for (int v = 0; v < VEC; ++v)
+                    if (A.v[v] != 0.f) B.v[v] = fmaf(A.v[v], G.v[v], B.v[v]);
+                publish<VEC>(w, i, ch, fill<VEC>(0.f), B);
+            }
+        }
+        if (threadIdx.x == 0 && w.nt > 1) next_ticket = take_ticket(w);   // as in the forward kernel
+
+        for (int j = kWarps - 1; j > warp; --j) G = rmaps.step(j, lane, G);
+        float* dx = p.dx + (t0 * D + c0);
+        float* dg = dgate + (t0 * D + c0);
+        const bool sum_lanes = GATE == KDA_GATE_HEAD_F32 && head_mode == kHeadRow;
+        // row r's gradients
+        auto row = [&](int r, bool out) {
+            const Vec<VEC> g = add(staged<T, VEC>(dy, r, lane), G);
+            if constexpr (COMP) {
+                if (out) store(dx + r * D + lane * VEC, mul(a[r].na(), g));
+            } else {
+                if (out) store(dx + r * D + lane * VEC, g);
+            }
+            Vec<VEC> da = mul(g, staged<float, VEC>(f, r, lane));
+            G = mul(a[r].a(), g);
+            if constexpr (GATE == KDA_GATE_CHANNEL_LOG_BF16) da = mul(a[r].a(), da);
+            if (sum_lanes) store(f + r * 32 * VEC + lane * VEC, da);
+            else if (out) store(dg + r * D + lane * VEC, da);
+        };
+        if (!edge) {
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) row(r, true);
+        } else {
+#pragma unroll
+            for (int r = R - 1; r >= 0; --r) {
+                if (rows.last >> r & 1) G = behind(r);
+                if (r < left) row(r, on);
                 if (rows.start >> r & 1) {
                     const int n = __shfl_sync(0xffffffffu, rows.n, r);
-                    if (p.dS0 && on) store(p.dS0 + n * D + ch, R);
+                    if (p.dS0 && on) store(p.dS0 + n * D + ch, G);
                 }
             }
         }
-        if constexpr (GATE == KDA_GATE_HEAD_F32) {
-            if (head_mode == kHeadRow) {
-                // lanes that share a head (or one of its 64-channel parts) add up
-                const int part = p.d < 32 * VEC ? p.d : 32 * VEC, width = part / VEC;
+        if (sum_lanes) {
+            // lanes that share a head (or one of its 64-channel parts) add up
+            const int part = p.d < 32 * VEC ? p.d : 32 * VEC, width = part / VEC;
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
-                    float s = on && r < rows.live ? f[r].v[0] + (VEC == 2 ? f[r].v[VEC - 1] : 0.f)
-                                                  : 0.f;
-                    for (int o = width >> 1; o > 0; o >>= 1)
-                        s += __shfl_xor_sync(0xffffffffu, s, o);
-                    // [T][H][parts]: the part's index is the channel over its width
-                    if (on && r < rows.live && (lane & (width - 1)) == 0)
-                        dgate[(t0 + r) * (D / part) + ch / part] = s;
-                }
+            for (int r = 0; r < R; ++r) {
+                const Vec<VEC> da = staged<float, VEC>(f, r, lane);
+                float s = on && r < left ? da.v[0] + (VEC == 2 ? da.v[VEC - 1] : 0.f) : 0.f;
+                for (int o = width >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+                // [T][H][parts]: the part's index is the channel over its width
+                if (on && r < left && (lane & (width - 1)) == 0)
+                    dgate[(t0 + r) * (D / part) + ch / part] = s;
             }
         }
+        __syncthreads();
+        tile = w.nt > 1 ? (int64_t)next_ticket : tile + gridDim.x;
     }
 }
 
@@ -935,36 +1009,32 @@ int lane_channels(int64_t D) { return D % 2 == 0 ? 2 : 1; }
 
 struct TileLayout {
     int64_t nt, ct, Dp;
-    size_t head, agg, inc, end;
+    size_t end;
 };
-TileLayout tile_layout(int64_t T, int64_t D) {
+TileLayout tile_layout(int64_t T, int64_t D, int rows) {   // rows: tokens a warp
     TileLayout L;
+    const int64_t tile = kWarps * rows;
     const int64_t width = 32 * lane_channels(D);
-    L.nt = T > 0 ? (T + LINREC_CHUNK - 1) / LINREC_CHUNK : 1;
+    L.nt = T > 0 ? (T + tile - 1) / tile : 1;
     L.ct = (D + width - 1) / width;
     L.Dp = L.ct * width;
-    L.head = L.nt > 1 ? 16 + (size_t)L.nt * L.ct * sizeof(uint32_t) : 16;
-    L.agg = pad(L.head);
-    L.inc = L.agg + (L.nt > 1 ? pad((size_t)L.nt * L.Dp * sizeof(float2)) : 0);
-    L.end = L.inc + (L.nt > 1 ? pad((size_t)L.nt * L.Dp * sizeof(float)) : 0);
+    L.end = kRecords + (L.nt > 1 ? pad((size_t)L.nt * L.Dp * sizeof(uint64_t)) : 0);
     return L;
 }
 
-// Clears the head (keeping the status word of an earlier pass) and checks the
+// Fills the workspace (keeping the status word of an earlier pass) and checks the
 // offsets of large batches.
 cudaError_t start_tiles(const LinrecArgs& a, const TileLayout& L, char* ws, bool keep_status,
                         TileSpace& w, cudaStream_t stream) {
     w.status = reinterpret_cast<int32_t*>(ws);
     w.ticket = reinterpret_cast<uint32_t*>(ws + 4);
-    w.flag = reinterpret_cast<uint32_t*>(ws + 16);
-    w.agg = reinterpret_cast<float2*>(ws + L.agg);
-    w.inc = reinterpret_cast<float*>(ws + L.inc);
+    w.record = reinterpret_cast<uint64_t*>(ws + kRecords);
     w.nt = (int32_t)L.nt;
     w.ct = (int32_t)L.ct;
     w.Dp = L.Dp;
     if (L.nt > 1 || a.num_seqs > kSelfCheck) {
         const size_t from = keep_status ? 4 : 0;
-        const cudaError_t err = cudaMemsetAsync(ws + from, 0, L.head - from, stream);
+        const cudaError_t err = cudaMemsetAsync(ws + from, 0xff, L.end - from, stream);
         if (err != cudaSuccess) return err;
     }
     if (a.num_seqs > kSelfCheck && !keep_status) {
@@ -975,23 +1045,15 @@ cudaError_t start_tiles(const LinrecArgs& a, const TileLayout& L, char* ws, bool
     return cudaSuccess;
 }
 
-// Rows on a 16-byte grid take the staged path.  A head gate's two channels a lane
-// share a head there, so d is even.
-bool staged(const LinrecArgs& a) {
-    const int64_t D = (int64_t)a.H * a.d;
-    return D % 8 == 0 && (a.gate_format != KDA_GATE_HEAD_F32 || a.d % 2 == 0);
-}
-
-// f(T, gate, complement, channels a lane, path) with its arguments as types.
+// f(T, gate, complement, channels a lane) with its arguments as types.
 template <int N>
 using Int = std::integral_constant<int, N>;
 template <typename F>
 cudaError_t by_tile(const LinrecArgs& a, F&& f) {
     return by_type(a.dtype, a.gate_format, [&](auto* t, auto g) {
         auto pick = [&](auto comp) {
-            if (staged(a)) return f(t, g, comp, Int<2>(), Int<kStaged>());
-            if (lane_channels((int64_t)a.H * a.d) == 2) return f(t, g, comp, Int<2>(), Int<kDirect>());
-            return f(t, g, comp, Int<1>(), Int<kDirect>());
+            return lane_channels((int64_t)a.H * a.d) == 2 ? f(t, g, comp, Int<2>())
+                                                          : f(t, g, comp, Int<1>());
         };
         return a.complement ? pick(std::true_type()) : pick(std::false_type());
     });
@@ -1000,7 +1062,7 @@ cudaError_t by_tile(const LinrecArgs& a, F&& f) {
 template <typename K, typename... A>
 cudaError_t launch_tiles(K kernel, const TileLayout& L, int ctas, int smem, cudaStream_t stream,
                          const A&... args) {
-    if (smem > 0) {
+    if (smem > 32 * 1024) {   // above what every kernel may have with its static part
         const cudaError_t err =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
@@ -1011,17 +1073,16 @@ cudaError_t launch_tiles(K kernel, const TileLayout& L, int ctas, int smem, cuda
 }
 
 cudaError_t run_forward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
-    const TileLayout L = tile_layout(a.total_tokens, (int64_t)a.H * a.d);
+    const TileLayout L = tile_layout(a.total_tokens, (int64_t)a.H * a.d, kFwdRows);
     TileSpace w;
     cudaError_t err = start_tiles(a, L, ws, false, w, stream);
     if (err != cudaSuccess) return err;
-    return by_tile(a, [&](auto* t, auto g, auto comp, auto vec, auto path) {
+    return by_tile(a, [&](auto* t, auto g, auto comp, auto vec) {
         using T = std::remove_pointer_t<decltype(t)>;
-        constexpr int G = decltype(g)::value, P = decltype(path)::value;
+        constexpr int V = decltype(vec)::value;
         constexpr bool C = decltype(comp)::value;
-        const int smem = P == kStaged ? kWarps * (staged_bytes<sizeof(T)>() + gate_bytes<G>()) : 0;
-        return launch_tiles(linrec_fwd_kernel<T, G, C, decltype(vec)::value, P>, L,
-                            fwd_ctas<T, G, C, P>(), smem, stream, a, w);
+        return launch_tiles(linrec_fwd_kernel<T, decltype(g)::value, C, V>, L, 2,
+                            kWarps * FwdRows<T, C, V>::kBytes, stream, a, w);
     });
 }
 
@@ -1044,7 +1105,7 @@ int32_t head_parts(int32_t d, int gate_format, int64_t D) {
 }  // namespace
 
 size_t linrec_prefill_bytes(int32_t num_seqs, int64_t total_tokens, int64_t D) {
-    return tile_layout(total_tokens, D).end + pad((size_t)num_seqs * D * sizeof(float));
+    return tile_layout(total_tokens, D, kFwdRows).end + pad((size_t)num_seqs * D * sizeof(float));
 }
 
 // Workspace of the backward pass: the tiles, the states when the caller has
@@ -1052,7 +1113,8 @@ size_t linrec_prefill_bytes(int32_t num_seqs, int64_t total_tokens, int64_t D) {
 size_t linrec_backward_bytes(int32_t, int64_t total_tokens, int32_t H, int32_t d,
                              int gate_format, bool with_states) {
     const int64_t D = (int64_t)H * d;
-    const TileLayout L = tile_layout(total_tokens, D);
+    // (the forward scan's tiles need less room than the backward one's)
+    const TileLayout L = tile_layout(total_tokens, D, kBwdRows);
     size_t b = L.end;
     if (!with_states && total_tokens > 0) b += pad((size_t)L.nt * D * sizeof(float));
     const int32_t parts = head_parts(d, gate_format, D);
@@ -1066,7 +1128,7 @@ cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t st
     // have written S_T, so it reads a copy
     const int64_t D = (int64_t)a.H * a.d;
     LinrecArgs b = a;
-    float* copy = reinterpret_cast<float*>(ws + tile_layout(a.total_tokens, D).end);
+    float* copy = reinterpret_cast<float*>(ws + tile_layout(a.total_tokens, D, kFwdRows).end);
     const cudaError_t err = cudaMemcpyAsync(copy, a.S0, (size_t)a.num_seqs * D * sizeof(float),
                                             cudaMemcpyDeviceToDevice, stream);
     if (err != cudaSuccess) return err;
@@ -1076,7 +1138,7 @@ cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t st
 
 cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
     const int64_t D = (int64_t)a.H * a.d;
-    const TileLayout L = tile_layout(a.total_tokens, D);
+    const TileLayout L = tile_layout(a.total_tokens, D, kBwdRows);
     size_t at = L.end;
     const float* states = a.states;
     cudaError_t err;
@@ -1095,13 +1157,12 @@ cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t s
     const int mode = head_mode(a.d, a.gate_format, D);
     const int32_t parts = head_parts(a.d, a.gate_format, D);
     float* dgate = parts > 1 ? reinterpret_cast<float*>(ws + at) : a.dgate;
-    err = by_tile(a, [&](auto* t, auto g, auto comp, auto vec, auto path) {
+    err = by_tile(a, [&](auto* t, auto g, auto comp, auto vec) {
         using T = std::remove_pointer_t<decltype(t)>;
-        constexpr int G = decltype(g)::value, P = decltype(path)::value;
-        const int smem = P == kStaged ? kWarps * (2 * staged_bytes<sizeof(T)>() + gate_bytes<G>()) : 0;
-        return launch_tiles(
-            linrec_bwd_kernel<T, G, decltype(comp)::value, decltype(vec)::value, P>, L, 2, smem,
-            stream, a, w, states, dgate, mode);
+        constexpr int V = decltype(vec)::value;
+        return launch_tiles(linrec_bwd_kernel<T, decltype(g)::value, decltype(comp)::value, V>, L,
+                            BwdRows<T, V>::kCtas, kWarps * BwdRows<T, V>::kBytes, stream, a, w,
+                            states, dgate, mode);
     });
     if (err != cudaSuccess || parts == 1 || a.total_tokens == 0) return err;
     const int64_t blocks = (a.total_tokens * a.H + kWarps - 1) / kWarps;
