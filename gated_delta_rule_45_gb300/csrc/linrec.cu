@@ -17,9 +17,9 @@
 //
 // Between tiles: each publishes its (A, B) as one 8-byte record a channel, and once
 // the state that leaves it is known, that state as the map (0, h).  A tile reads
-// the records of the eight tiles before it (a warp each), as far back as it takes
-// to meet a map with A = 0, and applies them in token order: the arithmetic is
-// the same wherever that is, so results do not depend on timing.  A record is one
+// the records of the eight tiles before it (a warp each) and applies them in token
+// order from a map with A = 0 on: the arithmetic is the same whichever that is, so
+// results do not depend on timing.  A record is one
 // atomic word that is valid as soon as it is not the pattern the workspace was
 // filled with, so neither side needs a fence (with flags and fences a tile took
 // 13.7 us instead of 4.4).  Tiles are handed out in time order by a ticket, so a
@@ -401,6 +401,16 @@ __device__ __forceinline__ void clear_status(const TileSpace& w, int N) {
     else atomicCAS(reinterpret_cast<uint32_t*>(w.status), ~0u, (uint32_t)KDA_OK);
 }
 
+// True when every row of the tile is an inner token of one sequence: no boundary in it.
+__device__ __forceinline__ bool inner_tile(const Offsets& o, const int32_t* cu, int N, int64_t first,
+                                           int tile, int64_t end) {
+    if (first + tile >= end) return false;
+    const int n = sequence_of(o, cu, N, (int32_t)first);
+    const int32_t lo = o.stride == 1 ? o.sample[n] : cu[n];
+    const int32_t hi = o.stride == 1 ? o.sample[n + 1] : cu[n + 1];
+    return lo < first && hi > first + tile;
+}
+
 // dst[n] = src[n] (zeros without src) for the sequences without tokens.
 __device__ void copy_empty(const int32_t* cu, int N, int64_t D, const float* src, float* dst) {
     if (!dst || dst == src) return;
@@ -464,41 +474,44 @@ __device__ __forceinline__ void publish(const TileSpace& w, int i, int64_t ch,
     r.write(w.record + (int64_t)i * w.Dp + ch);
 }
 
+// True once a wait that began at t0 (0: now) is over its limit, here or in another CTA.
+__device__ __noinline__ bool expired(const TileSpace& w, uint64_t& t0) {
+    const uint64_t t = now_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitNs) atomicExch(w.status, (int32_t)KDA_ERR_DEVICE_TIMEOUT);
+    return *reinterpret_cast<volatile int32_t*>(w.status) == KDA_ERR_DEVICE_TIMEOUT;
+}
+
 // The state that enters tile i, for the lane's VEC channels from ch: warp j waits
 // for the record of the tile j + 1 steps before (step = -1: towards lower indices,
-// +1: higher), then every warp applies the eight from the farthest to the nearest;
-// a map with A = 0 is where the walk can end.  Tiles from `tiles` on hold no
-// sequence and publish nothing.  All warps call it together.  When a
-// wait runs out, here or elsewhere, the status word says so and the walk ends.
+// +1: higher), then every warp applies the eight from the farthest to the nearest.
+// A map with A = 0 is where the walk starts; while none of the eight is one, the
+// eight are read again (few channels and many tokens: with the walk going on past
+// them 170000 tokens of one channel took 1.7 ms instead of FEW us).  Tiles from
+// `tiles` on hold no sequence and publish nothing.  All warps call it together.  When
+// a wait runs out, here or elsewhere, the status word says so and the result is 0.
 template <int VEC>
 __device__ Vec<VEC> look_back(const TileSpace& w, int i, int step, int64_t tiles, int64_t ch,
                               int warp, int lane, Record<VEC> (*records)[32]) {
-    for (int far = 0;; far += kWarps) {
-        if (far) __syncthreads();   // the records before are read
-        const int64_t idx = i + (int64_t)step * (far + warp + 1);
+    const int64_t idx = i + (int64_t)step * (warp + 1);
+    const bool there = idx >= 0 && idx < tiles;
+    const uint64_t* p = w.record + (there ? idx * w.Dp + ch : 0);
+    uint64_t t0 = 0;
+    for (uint32_t round = 0;; ++round) {
         Record<VEC> r;
         r.set(fill<VEC>(0.f), fill<VEC>(0.f));
-        bool stop = false;
-        if (idx >= 0 && idx < tiles) {
-            const uint64_t* p = w.record + idx * w.Dp + ch;
-            uint64_t t0 = 0;
+        bool stop = (round & 63) == 63 && expired(w, t0);
+        if (there) {
             r.read(p);
-            for (uint32_t round = 1; !r.ready(); ++round) {
-                if ((round & 63) == 0) {
-                    const uint64_t t = now_ns();
-                    if (t0 == 0) t0 = t;
-                    if (t - t0 > kWaitNs) atomicExch(w.status, (int32_t)KDA_ERR_DEVICE_TIMEOUT);
-                    if (*reinterpret_cast<volatile int32_t*>(w.status) == KDA_ERR_DEVICE_TIMEOUT) {
-                        stop = true;
-                        break;
-                    }
-                }
+            for (uint32_t spin = 1; !stop && !r.ready(); ++spin) {
+                stop = (spin & 63) == 0 && expired(w, t0);
                 r.read(p);
             }
         }
+        __syncwarp();
         records[warp][lane] = r;
         if (__syncthreads_or(stop)) return fill<VEC>(0.f);
-        bool open = false;   // a channel whose walk goes on past these eight
+        bool open = false;   // a channel whose walk has no start among the eight
         Vec<VEC> H = fill<VEC>(0.f);
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
@@ -512,21 +525,8 @@ __device__ Vec<VEC> look_back(const TileSpace& w, int i, int step, int64_t tiles
             }
             open |= !met;
         }
-        if (!__any_sync(0xffffffffu, open)) {   // the same answer in every warp
-            if (far == 0) return H;
-            // the farther records once more, all known by now, in token order
-            H = fill<VEC>(0.f);
-            for (int j = far + kWarps; j >= 1; --j) {
-                const int64_t k = i + (int64_t)step * j;
-                if (k < 0 || k >= tiles) continue;
-                Record<VEC> q;
-                q.read(w.record + k * w.Dp + ch);
-#pragma unroll
-                for (int v = 0; v < VEC; ++v)
-                    H.v[v] = q.A(v) == 0.f ? q.B(v) : fmaf(q.A(v), H.v[v], q.B(v));
-            }
-            return H;
-        }
+        if (!__any_sync(0xffffffffu, open)) return H;   // the same answer in every warp
+        __syncthreads();   // all have read the records
     }
 }
 
@@ -562,29 +562,28 @@ __device__ __forceinline__ int64_t first_tile(const TileSpace& w, uint32_t* shar
     return *shared;
 }
 
-// Values that replace the carried one at a boundary row (S0 at a first token, dS_T at a
-// last one): that of the first boundary among the warp's rows is loaded with the
-// tile, those of more (sequences shorter than the warp's rows) when they are met.
+// The value that replaces the carried one at a boundary row (S0 at a first token, dS_T
+// at a last one), and the store of a state there.  Calls, not inlined: they stand in
+// loops unrolled over the rows, whose code would otherwise outgrow the instruction
+// cache (with 128-token sequences a fifth of the time went to instruction fetches).
 template <int VEC>
-struct Boundary {
-    Vec<VEC> value;
-    int row;
-    __device__ __forceinline__ Boundary(const float* src, uint32_t mask, int n, int64_t D, int ch,
-                                        bool on) {
-        row = __ffs(mask) - 1;
-        value = fill<VEC>(0.f);
-        if (row >= 0) value = load(src, row, n, D, ch, on);
-    }
-    __device__ __forceinline__ static Vec<VEC> load(const float* src, int r, int n, int64_t D,
-                                                    int ch, bool on) {
-        const int64_t seq = __shfl_sync(0xffffffffu, n, r);
-        return src && on ? load_f32<VEC>(src + seq * D + ch) : fill<VEC>(0.f);
-    }
-    __device__ __forceinline__ Vec<VEC> at(int r, const float* src, int n, int64_t D, int ch,
-                                           bool on) const {
-        return r == row ? value : load(src, r, n, D, ch, on);
-    }
-};
+__device__ __noinline__ Vec<VEC> boundary_value(const float* src, int n, int r, int64_t D, int ch) {
+    const int64_t seq = __shfl_sync(0xffffffffu, n, r);
+    return src && ch < D ? load_f32<VEC>(src + seq * D + ch) : fill<VEC>(0.f);
+}
+// That of the first boundary among a warp's rows, loaded along with the tile.
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> first_boundary(const float* src, uint32_t mask, int n,
+                                                   int64_t D, int ch) {
+    const int64_t seq = __shfl_sync(0xffffffffu, n, mask ? __ffs(mask) - 1 : 0);
+    return mask && src && ch < D ? load_f32<VEC>(src + seq * D + ch) : fill<VEC>(0.f);
+}
+template <int VEC>
+__device__ __noinline__ void boundary_store(float* dst, int n, int r, int64_t D, int ch,
+                                            Vec<VEC> h) {
+    const int64_t seq = __shfl_sync(0xffffffffu, n, r);
+    if (dst && ch < D) store(dst + seq * D + ch, h);
+}
 
 // Rows of x in shared memory; of the complement the inputs u, in fp32.
 template <typename T, bool COMP, int VEC>
@@ -634,9 +633,13 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
         const bool full = left == R && c0 + 32 * VEC <= D;
 
         stage_rows<R, T, VEC>(x, p.x, t0 * D + c0, D, full && D % 8 == 0, left, on, lane);
-        const Rows rows = rows_of<R>(off, cu, N, t0, end, lane);
-        const bool edge = (rows.start | rows.last) != 0 || !full;
-        const Boundary<VEC> first_start(p.S0, rows.start, rows.n, D, ch, on);
+        // all of the CTA's warps take the plain path or the one with boundaries together:
+        // each is unrolled, and the instruction cache holds one of them
+        const bool edge = c0 + 32 * VEC > D ||
+                          !inner_tile(off, cu, N, (int64_t)i * kTile, kTile, end);
+        Rows rows = {};
+        if (edge) rows = rows_of<R>(off, cu, N, t0, end, lane);
+        const Vec<VEC> start0 = first_boundary<VEC>(p.S0, rows.start, rows.n, D, ch);
         Gate<GATE, VEC> a[R];
         take_gate<R, GATE, VEC>(a, p, t0, D, c0, full, left, on, lane);
         expand_gate<R, GATE, VEC>(a);
@@ -644,7 +647,9 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
         if constexpr (COMP) complement_rows<R, T, GATE, VEC>(u, x, a, lane);
         auto input = [&](int r) { return staged<U, VEC>(u, r, lane); };
         // the state that replaces the carried one at a sequence's first token
-        auto start = [&](int r) { return first_start.at(r, p.S0, rows.n, D, ch, on); };
+        auto start = [&](int r) {
+            return r == __ffs(rows.start) - 1 ? start0 : boundary_value<VEC>(p.S0, rows.n, r, D, ch);
+        };
 
         Vec<VEC> A = fill<VEC>(1.f), B = fill<VEC>(0.f);
         if (!edge) {
@@ -711,15 +716,13 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
                 }
             }
         } else {
+            const int stored = on && y ? left : 0;
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 if (rows.start >> r & 1) h = start(r);
                 h = fma(a[r].a(), h, input(r));
-                if (on && y && r < left) store(y + r * D + lane * VEC, h);
-                if (rows.last >> r & 1) {
-                    const int n = __shfl_sync(0xffffffffu, rows.n, r);
-                    if (p.S_T && on) store(p.S_T + n * D + ch, h);
-                }
+                if (r < stored) store(y + r * D + lane * VEC, h);
+                if (rows.last >> r & 1) boundary_store<VEC>(p.S_T, rows.n, r, D, ch, h);
             }
         }
         __syncthreads();   // maps, records and the ticket: this tile is done with them
@@ -734,18 +737,16 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
 //     that neither divide 64 nor are a multiple of it)
 enum : int { kNoHead = 0, kHeadRow = 1, kHeadWide = 2 };
 
-// Per warp: rows of x and dy as stored, and of f in fp32 (see below).  Three CTAs an SM
-// with bf16 inputs, two with fp32 ones.
+// Per warp: rows of x and dy as stored, and of f in fp32 (see below).
 template <typename T, int VEC>
 struct BwdRows {
     static constexpr int R = kBwdRows;
     static constexpr int kRaw = R * 32 * VEC * (int)sizeof(T), kF = R * 32 * VEC * 4;
     static constexpr int kBytes = 2 * kRaw + kF;
-    static constexpr int kCtas = sizeof(T) == 2 ? 3 : 2;
-};
+    };
 
 template <typename T, int GATE, bool COMP, int VEC>
-__global__ void __launch_bounds__(kThreads, BwdRows<T, VEC>::kCtas)
+__global__ void __launch_bounds__(kThreads, 2)
 linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict__ states,
                   float* dgate, int head_mode) {
     constexpr int R = kBwdRows;
@@ -786,10 +787,12 @@ linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict
 
         stage_rows<R, T, VEC>(x, p.x, t0 * D + c0, D, full && D % 8 == 0, left, on, lane);
         stage_rows<R, T, VEC>(dy, p.dy, t0 * D + c0, D, full && D % 8 == 0, left, on, lane);
-        const Rows rows = rows_of<R>(off, cu, N, t0, end, lane);
-        const bool edge = (rows.start | rows.last) != 0 || !full;
-        const Boundary<VEC> first_start(p.S0, rows.start, rows.n, D, ch, on);
-        const Boundary<VEC> first_last(p.dS_T, rows.last, rows.n, D, ch, on);
+        const bool edge = c0 + 32 * VEC > D ||   // as in the forward kernel
+                          !inner_tile(off, cu, N, (int64_t)i * LINREC_CHUNK, LINREC_CHUNK, end);
+        Rows rows = {};
+        if (edge) rows = rows_of<R>(off, cu, N, t0, end, lane);
+        const Vec<VEC> start0 = first_boundary<VEC>(p.S0, rows.start, rows.n, D, ch);
+        const Vec<VEC> last0 = first_boundary<VEC>(p.dS_T, rows.last, rows.n, D, ch);
         Vec<VEC> H = fill<VEC>(0.f);   // the state that enters the tile
         if (on && (int64_t)i * LINREC_CHUNK < end) H = load_f32<VEC>(states + i * D + ch);
         Gate<GATE, VEC> a[R];
@@ -801,8 +804,12 @@ linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict
             if constexpr (COMP) return mul(a[r].na(), q);
             else return q;
         };
-        auto start = [&](int r) { return first_start.at(r, p.S0, rows.n, D, ch, on); };
-        auto behind = [&](int r) { return first_last.at(r, p.dS_T, rows.n, D, ch, on); };
+        auto start = [&](int r) {
+            return r == __ffs(rows.start) - 1 ? start0 : boundary_value<VEC>(p.S0, rows.n, r, D, ch);
+        };
+        auto behind = [&](int r) {
+            return r == __ffs(rows.last) - 1 ? last0 : boundary_value<VEC>(p.dS_T, rows.n, r, D, ch);
+        };
 
         // maps of the warp's rows, both ways
         Vec<VEC> A = fill<VEC>(1.f), B = fill<VEC>(0.f), RB = fill<VEC>(0.f), RA = fill<VEC>(1.f);
@@ -916,10 +923,7 @@ linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict
             for (int r = R - 1; r >= 0; --r) {
                 if (rows.last >> r & 1) G = behind(r);
                 if (r < left) row(r, on);
-                if (rows.start >> r & 1) {
-                    const int n = __shfl_sync(0xffffffffu, rows.n, r);
-                    if (p.dS0 && on) store(p.dS0 + n * D + ch, G);
-                }
+                if (rows.start >> r & 1) boundary_store<VEC>(p.dS0, rows.n, r, D, ch, G);
             }
         }
         if (sum_lanes) {
@@ -1161,7 +1165,7 @@ cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t s
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(vec)::value;
         return launch_tiles(linrec_bwd_kernel<T, decltype(g)::value, decltype(comp)::value, V>, L,
-                            BwdRows<T, V>::kCtas, kWarps * BwdRows<T, V>::kBytes, stream, a, w,
+                            2, kWarps * BwdRows<T, V>::kBytes, stream, a, w,
                             states, dgate, mode);
     });
     if (err != cudaSuccess || parts == 1 || a.total_tokens == 0) return err;
