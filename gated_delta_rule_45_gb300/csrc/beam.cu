@@ -3,16 +3,18 @@
 //
 // Selection.  The value of candidate (beam k, token v) is
 // score_k + x_kv - log sum_w exp(x_kw); within a beam the order is that of the
-// logits.  One pass over the logits, cut into pieces of at most 64 values a thread:
-// each CTA leaves, for its piece, the maximum, the sum of exponentials relative to it
-// and its num_out largest logits, sorted.  A second kernel, one CTA a request, joins
-// the sums in 64 bits and picks the num_out best of all pieces' candidates by their
-// values in 64 bits (candidates of different beams can lie closer than fp32 resolves).
+// logits.  One pass over the logits, cut into pieces: each CTA leaves, for its piece,
+// the maximum, the sum of exponentials relative to it and its num_out largest logits,
+// sorted.  A second kernel, one CTA a request, joins the sums in 64 bits and picks the
+// num_out best of all pieces' candidates by their values in 64 bits (candidates of
+// different beams can lie closer than fp32 resolves).
 //
-// Both pick by threshold.  Keys order value and index together, so no two are equal.
-// With t the num_out-th largest of the threads' own maxima, exactly num_out threads
-// hold keys >= t, all of the num_out largest keys are among theirs, and their list is
-// short (num_out times a thread's share at the very most); it is ranked by counting.
+// Both pick by threshold: a bound that at least num_out threads' own maxima reach
+// leaves a short list of candidates, which is ranked by counting.  Keys order value and
+// index together, so no two are equal.  Rows of equal or masked logits, where the bound
+// would leave a long list, go through the exact num_out-th largest of the threads'
+// maximum keys: exactly num_out threads hold keys from there on, so the list is
+// num_out times a thread's share at the most.
 //
 // Bound: HBM (each logit is read once); at 64 x 8 x 128000 bf16 logits SELECT.
 #include "kda_internal.h"
@@ -25,7 +27,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kShare = 64;   // most values a thread looks at
+constexpr int kList = 1024;  // logits the fast pass may list
+constexpr int kCtas = 8;     // an SM, resident or waiting
 
 // 16 bytes of logits.
 template <typename T>
@@ -55,6 +58,31 @@ struct Logits<__nv_bfloat16> {
         w = i & 1 ? (w & 0xffffu) | (b & 0xffff0000u) : (w & 0xffff0000u) | b >> 16;
     }
 };
+
+// Exponentials are taken as 2^(x log2 e - c) with c = M log2 e rounded once, M the
+// piece's maximum: one multiply-add and one special-function instruction a logit.  The
+// piece's sum is then made relative to e^M, with what the rounding of c left out.
+constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.92596299e-8f;
+__device__ __forceinline__ float exp2_ftz(float x) {   // below the normal numbers: 0
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
+    return e;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+// acc + (2^(a log2 e - c), 2^(b log2 e - c)), both halves at once
+__device__ __forceinline__ uint64_t add_exp2(uint64_t acc, float a, float b, uint64_t log2e2,
+                                             uint64_t c2) {
+    uint64_t t;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pack2(a, b)), "l"(log2e2), "l"(c2));
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(t));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(acc), "l"(pack2(exp2_ftz(x), exp2_ftz(y))));
+    return t;
+}
 
 // 16 bytes from bit `shift` (16 .. 112) of a and the vector after it.
 __device__ __forceinline__ uint4 shifted(const uint4 a, const uint4 b, int shift) {
@@ -109,198 +137,379 @@ __device__ __forceinline__ bool above(const ValueKey& a, const ValueKey& b) {
 __device__ __forceinline__ bool exists(uint64_t a) { return a != 0; }
 __device__ __forceinline__ bool exists(const ValueKey& a) { return a.index != 0; }
 
-// The num-th largest of the threads' best keys, Key{} when fewer threads have one.
-// Returns whether this thread's best is among the num largest.
-template <int THREADS, typename Key>
-__device__ bool threshold(Key* best, Key* limit, const Key& mine, int num) {
-    best[threadIdx.x] = mine;
-    if (threadIdx.x == 0) *limit = Key{};
-    __syncthreads();
-    int rank = 0;   // a thread without a key ranks behind all that have one
-    if (__any_sync(0xffffffffu, exists(mine))) {
-#pragma unroll 8
-        for (int j = 0; j < THREADS; ++j) rank += above(best[j], mine);
+// Upper bits of a key: larger or equal for a larger key, 0 only for none.
+__device__ __forceinline__ uint32_t coarse(uint64_t a) { return (uint32_t)(a >> 32); }
+__device__ __forceinline__ uint32_t coarse(const ValueKey& a) { return (uint32_t)(a.value >> 32); }
+
+// The r-th largest of a warp's values (0: none), equal ones counted one by one.
+__device__ __forceinline__ uint32_t warp_nth(uint32_t c, int r, int lane) {
+    uint32_t top = 0;
+    for (int i = 0; i < r; ++i) {
+        top = __reduce_max_sync(0xffffffffu, c);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, c == top)) - 1) c = 0;
     }
-    if (exists(mine) && rank == num - 1) *limit = mine;
-    __syncthreads();
-    return exists(mine) && rank < num;
+    return top;
 }
 
-// One piece of one row.  pieces: of a row; span: 16-byte vectors of a piece.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-beam_piece_kernel(const BeamSelectArgs p, int pieces, int span, uint64_t* __restrict__ keys,
-                  float2* __restrict__ sums) {
-    constexpr int N = Logits<T>::N;
-    extern __shared__ __align__(16) uint64_t list[];   // num_out x kShare
-    __shared__ uint64_t best_of[kThreads];
-    __shared__ uint64_t limit;
-    __shared__ float2 part[kWarps];
-    __shared__ int count;
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = blockIdx.x / pieces, piece = blockIdx.x % pieces;
-    const int num = p.num_out;
-    uint64_t* out = keys + (int64_t)blockIdx.x * num;
+// The num-th largest of the threads' best keys (Key{} when fewer threads have one) goes
+// to `limit`; returns whether this thread's best is among the num largest.  A first
+// bound, from every warp's own largest, leaves few keys to rank by counting.
+template <int THREADS, typename Key>
+struct Threshold {
+    Key best[THREADS];
+    Key limit;
+    uint32_t bound[THREADS / 32];
+    int count;
 
-    // Rows need not start on a 16-byte boundary.  Which tokens a thread takes does not
-    // depend on where the row starts, so equal rows have equal sums and tie exactly.
-    const T* r = static_cast<const T*>(p.logits) + row * p.ld;
-    const int shift = (int)(reinterpret_cast<uintptr_t>(r) & 15) * 8;   // bits
-    const int lo = piece * span * N, hi = min(lo + span * N, p.V);      // tokens
-
-    const float score = tame(p.scores[row]);
-    const bool finished = p.finished && p.finished[row];
-    if (finished || score == -INFINITY) {
-        // nothing to read: `eos` of a finished beam, then the lowest tokens at -inf
-        const bool has = finished && score != -INFINITY && p.eos >= lo && p.eos < hi;
-        for (int j = tid; j < num; j += kThreads) {
-            int v = lo + j;
-            uint64_t key = 0;
-            if (has) {
-                if (j == 0) key = logit_key(0.f, p.eos);
-                else if (--v >= p.eos) ++v;   // the tokens without eos
-            }
-            if (!key && v < hi) key = logit_key(-INFINITY, v);
-            out[j] = key;
+    __device__ bool find(const Key& mine, int num) {
+        constexpr int kW = THREADS / 32;
+        const int lane = threadIdx.x & 31;
+        const uint32_t c = exists(mine) ? coarse(mine) : 0;
+        const uint32_t nth = warp_nth(c, (num + kW - 1) / kW, lane);
+        if (lane == 0) bound[threadIdx.x >> 5] = nth;
+        if (threadIdx.x == 0) {
+            limit = Key{};
+            count = 0;
         }
-        if (tid == 0) sums[blockIdx.x] = has ? make_float2(0.f, 1.f) : make_float2(-INFINITY, 0.f);
-        return;
+        __syncthreads();
+        uint32_t least = bound[0];
+#pragma unroll
+        for (int j = 1; j < kW; ++j) least = min(least, bound[j]);
+        const bool in = exists(mine) && c >= least;
+        if (in) best[atomicAdd(&count, 1)] = mine;
+        __syncthreads();
+        int rank = 0;
+        if (in) {
+            const int have = count;
+            for (int j = 0; j < have; ++j) rank += above(best[j], mine);
+            if (rank == num - 1) limit = mine;
+        }
+        __syncthreads();
+        return in && rank < num;
     }
+};
 
+// Sorts the `have` keys of a list by counting; rank r < num goes to put(r, key).
+template <typename Key, typename F>
+__device__ __forceinline__ void rank_list(const Key* list, int have, int num, F&& put) {
+    for (int i = threadIdx.x; i < have; i += blockDim.x) {
+        const Key key = list[i];
+        int rank = 0;
+        for (int j = 0; j < have; ++j) rank += above(list[j], key);
+        if (rank < num) put(rank, key);
+    }
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+__device__ __forceinline__ float warp_sum(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Largest of a vector's values, NaN left out; -inf of none.
+__device__ __forceinline__ float largest(const Logits<float>& q) {
+    return fmaxf(fmaxf(q.get(0), q.get(1)), fmaxf(q.get(2), q.get(3)));
+}
+__device__ __forceinline__ float largest(const Logits<__nv_bfloat16>& q) {
+    const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&q.u);
+    const __nv_bfloat162 m = __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3]));
+    return fmaxf(fmaxf(__low2float(m), __high2float(m)), -INFINITY);
+}
+
+// A piece of a row as its CTA sees it: `vectors` of N values a thread.
+template <typename T>
+struct Piece {
+    static constexpr int N = Logits<T>::N;
+    const T* r;       // the row
+    int lo, hi;       // tokens [lo, hi)
+    int V, shift;     // shift: bits the row starts past a 16-byte boundary
+    int vectors;
+
+    // Which tokens a thread takes does not depend on where the row starts, so equal rows
+    // have equal sums and tie exactly.
+    __device__ __forceinline__ Piece(const BeamSelectArgs& p, int row, int piece, int each) {
+        r = static_cast<const T*>(p.logits) + row * p.ld;
+        V = p.V;
+        shift = (int)(reinterpret_cast<uintptr_t>(r) & 15) * 8;
+        vectors = each;
+        lo = piece * each * kThreads * N;
+        hi = min(lo + each * kThreads * N, V);
+    }
+    __device__ __forceinline__ int token(int j) const {
+        return lo + (j * kThreads + (int)threadIdx.x) * N;
+    }
     // A thread's j-th N values, -inf past the row's end.  Off the boundary they come from
     // the two aligned vectors they lie in (the next values of the row have to be there).
-    auto load = [&](int j) {
+    __device__ __forceinline__ Logits<T> load(int j) const {
         Logits<T> q;
-        const int v = lo + (j * kThreads + tid) * N;
-        if (v + (shift ? 2 * N : N) <= p.V) {
+        const int v = token(j);
+        if (v + (shift ? 2 * N : N) <= V) {
             const uint4* w = reinterpret_cast<const uint4*>(
                 reinterpret_cast<uintptr_t>(r + v) & ~(uintptr_t)15);
             q.u = __ldg(w);
             if (shift) q.u = shifted(q.u, __ldg(w + 1), shift);
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) q.set(i, v + i < p.V ? Elem<T>::load(r + v + i) : -INFINITY);
+            for (int i = 0; i < N; ++i) q.set(i, v + i < V ? Elem<T>::load(r + v + i) : -INFINITY);
         }
         return q;
-    };
-    const int mine = (span + kThreads - 1) / kThreads;   // vectors a thread
-
-    float m = -INFINITY, s = 0.f;   // running maximum and sum of exponentials
-    uint64_t best = 0;
-    // clean: values are known to be no NaN and no +inf
-    auto look = [&](const Logits<T>& q, int j, bool clean) {
-        const int v = lo + (j * kThreads + tid) * N;
-        float x[N], top = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            x[i] = clean ? q.get(i) : tame(q.get(i));
-            top = fmaxf(top, x[i]);
-        }
-        if (top > m || best == 0) {   // a new best: its first place
-            s *= m == -INFINITY ? 0.f : __expf(m - top);
-            m = top;
-            int at = -1;
-#pragma unroll
-            for (int i = N - 1; i >= 0; --i)
-                if (x[i] == top && v + i < hi) at = i;
-            if (at >= 0) best = logit_key(top, v + at);
-        }
-        if (m != -INFINITY) {
-            float e = 0.f;
-#pragma unroll
-            for (int i = 0; i < N; ++i) e += __expf(x[i] - m);
-            s += e;
-        }
-    };
-    for (int j0 = 0; j0 < mine; j0 += 4) {
-        Logits<T> q[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j0 + j < mine) q[j] = load(j0 + j);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (j0 + j < mine) look(q[j], j0 + j, true);
     }
-    // a NaN or +inf among them, or (where m is -inf) perhaps a NaN: again, replaced
-    if (!(s < INFINITY) || m == -INFINITY) {
-        m = -INFINITY;
-        s = 0.f;
-        best = 0;
-        for (int j = 0; j < mine; ++j) look(load(j), j, false);
-    }
-
-    // the piece's maximum and sum
-    float M = m;
+    // Vectors j0 .. j0 + U - 1 (those past the piece: -inf).
+    template <int U>
+    __device__ __forceinline__ void load_some(Logits<T> (&q)[U], int j0) const {
+        if (shift == 0 && lo + (j0 + U) * kThreads * N <= hi) {
+            const uint4* w = reinterpret_cast<const uint4*>(r + token(j0));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float S = m == -INFINITY ? 0.f : s * __expf(m - M);
+            for (int j = 0; j < U; ++j) q[j].u = __ldg(w + j * kThreads);
+        } else {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) S += __shfl_xor_sync(0xffffffffu, S, o);
-    if (lane == 0) part[warp] = make_float2(M, S);
-    if (tid == 0) count = 0;
-    const bool among = threshold<kThreads>(best_of, &limit, best, num);
-    if (tid == 0) {
-        float top = -INFINITY, sum = 0.f;
-        for (int j = 0; j < kWarps; ++j) top = fmaxf(top, part[j].x);
-        for (int j = 0; j < kWarps; ++j)
-            if (part[j].y > 0.f) sum += part[j].y * __expf(part[j].x - top);
-        sums[blockIdx.x] = make_float2(top, sum);
-    }
-    // the keys from the limit on, then their ranks
-    if (among) {
-        const uint64_t from = limit;
-        for (int j = 0; j < mine; ++j) {
-            const Logits<T> q = load(j);
-            const int v = lo + (j * kThreads + tid) * N;
+            for (int j = 0; j < U; ++j) {
+                if (j0 + j < vectors) {
+                    q[j] = load(j0 + j);
+                } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const uint64_t key = logit_key(tame(q.get(i)), v + i);
-                if (v + i < hi && key >= from) list[atomicAdd(&count, 1)] = key;
+                    for (int i = 0; i < N; ++i) q[j].set(i, -INFINITY);
+                }
             }
         }
     }
+};
+
+// Pieces whose fast pass gave up: a NaN or +inf, nothing above -inf, values far above the
+// first ones, or so many equal logits that the list ran over.  Values are replaced as
+// documented and the threads' maxima carry their tokens: of a step of U vectors a thread,
+// at most num_out x U N keys are listed, after the num_out best of the steps before.
+template <typename T, int U>
+__device__ __noinline__ void careful_piece(const Piece<T>& w, int num, uint64_t* list,
+                                           uint64_t* out, float2* sum_out) {
+    constexpr int N = Logits<T>::N;
+    __shared__ Threshold<kThreads, uint64_t> pick;
+    __shared__ uint64_t kept[BEAM_MAX_SELECT];
+    __shared__ float part[kWarps];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    float M = -INFINITY, S = 0.f;
+    int held = 0;
+    for (int j0 = 0; j0 < w.vectors; j0 += U) {
+        const int j1 = min(j0 + U, w.vectors);
+        float m = -INFINITY;
+        uint64_t best = 0;
+        for (int j = j0; j < j1; ++j) {
+            const Logits<T> q = w.load(j);
+            const int v = w.token(j);
+            for (int i = 0; i < N; ++i) {
+                if (v + i >= w.hi) break;
+                const float x = tame(q.get(i));
+                m = fmaxf(m, x);
+                best = max(best, logit_key(x, v + i));
+            }
+        }
+        m = warp_max(m);
+        if (lane == 0) part[warp] = m;
+        if (tid == 0) count = held;
+        if (tid < held) list[tid] = kept[tid];
+        const bool among = pick.find(best, num);
+        float top = M;
+        for (int j = 0; j < kWarps; ++j) top = fmaxf(top, part[j]);
+        float s = 0.f;
+        const uint64_t from = pick.limit;
+        for (int j = j0; j < j1; ++j) {
+            const Logits<T> q = w.load(j);
+            const int v = w.token(j);
+            for (int i = 0; i < N; ++i) {
+                if (v + i >= w.hi) break;
+                const float x = tame(q.get(i));
+                if (top != -INFINITY) s += exp2_ftz((x - top) * kLog2e);
+                if (among && logit_key(x, v + i) >= from)
+                    list[atomicAdd(&count, 1)] = logit_key(x, v + i);
+            }
+        }
+        s = warp_sum(s);
+        __syncthreads();   // the parts are read, the list is complete
+        if (lane == 0) part[warp] = s;
+        const int have = count;
+        rank_list(list, have, num, [&](int rank, uint64_t key) { kept[rank] = key; });
+        held = min(have, num);
+        __syncthreads();
+        if (M != -INFINITY) S *= exp2_ftz((M - top) * kLog2e);
+        for (int j = 0; j < kWarps; ++j) S += part[j];
+        M = top;
+        __syncthreads();
+    }
+    if (tid == 0) *sum_out = make_float2(M, S);
+    for (int i = tid; i < num; i += kThreads) out[i] = i < held ? kept[i] : 0;
+}
+
+// One piece of one row.  Its first U vectors a thread give the reference of the
+// exponentials and, ranked, the num_out best so far: the bound for all that follows.
+// The rest then streams by without a barrier, few of its logits reaching the bound.
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads, 5)
+beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __restrict__ keys,
+                  float2* __restrict__ sums) {
+    constexpr int N = Logits<T>::N;
+    extern __shared__ __align__(16) uint64_t list[];   // num_out (U N + 1), at least kList
+    __shared__ uint32_t bound[kWarps];
+    __shared__ float2 part[kWarps];
+    __shared__ float limit;
+    __shared__ int count;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / pieces;
+    const int num = p.num_out;
+    uint64_t* out = keys + (int64_t)blockIdx.x * num;
+    const Piece<T> w(p, row, blockIdx.x - row * pieces, each);
+    const float score = tame(p.scores[row]);
+    const bool finished = p.finished && p.finished[row];
+    if (finished || score == -INFINITY) {
+        // nothing to read: `eos` of a finished beam, then the lowest tokens at -inf
+        const bool has = finished && score != -INFINITY && p.eos >= w.lo && p.eos < w.hi;
+        for (int j = tid; j < num; j += kThreads) {
+            int v = w.lo + j;
+            uint64_t key = 0;
+            if (has) {
+                if (j == 0) key = logit_key(0.f, p.eos);
+                else if (--v >= p.eos) ++v;   // the tokens without eos
+            }
+            if (!key && v < w.hi) key = logit_key(-INFINITY, v);
+            out[j] = key;
+        }
+        if (tid == 0) sums[blockIdx.x] = has ? make_float2(0.f, 1.f) : make_float2(-INFINITY, 0.f);
+        return;
+    }
+
+    Logits<T> q[U];
+    w.load_some(q, 0);
+    // their maximum, and a bound that at least num_out threads reach
+    float m = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < U; ++j) m = fmaxf(m, largest(q[j]));
+    const int warps = min((w.hi - w.lo) / (32 * N), kWarps);   // whose threads all have values
+    const uint32_t nth = warp < warps ? warp_nth(ordered(m), (num + warps - 1) / warps, lane) : 0;
+    m = warp_max(m);
+    if (lane == 0) {
+        part[warp].x = m;
+        bound[warp] = nth;
+    }
+    if (tid == 0) {
+        count = 0;
+        limit = -INFINITY;
+    }
+    __syncthreads();
+    uint32_t least = warps > 0 ? bound[0] : 0;
+    float M = part[0].x;
+#pragma unroll
+    for (int j = 1; j < kWarps; ++j) {
+        if (j < warps) least = min(least, bound[j]);
+        M = fmaxf(M, part[j].x);
+    }
+    const float c = M * kLog2e;
+    const uint64_t log2e2 = pack2(kLog2e, kLog2e), c2 = pack2(-c, -c);
+    uint64_t acc[2] = {0, 0};
+    // the sum of exponentials; the vectors with a logit at or above the bound are read
+    // again, in a loop that is short code (unrolled over the registers a third of the
+    // time went to instruction fetches), and those logits listed
+    auto look = [&](int j0, float from) {
+        uint32_t hits = 0;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+#pragma unroll
+            for (int i = 0; i < N; i += 2)
+                acc[i / 2 & 1] = add_exp2(acc[i / 2 & 1], q[j].get(i), q[j].get(i + 1), log2e2, c2);
+            hits |= (largest(q[j]) >= from ? 1u : 0u) << j;
+        }
+        for (; hits; hits &= hits - 1) {
+            const int j = j0 + __ffs(hits) - 1, v = w.token(j);
+            if (j >= w.vectors) break;
+            const Logits<T> x = w.load(j);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (x.get(i) >= from && v + i < w.hi) {
+                    const int place = atomicAdd(&count, 1);
+                    if (place < kList) list[place] = logit_key(x.get(i), v + i);
+                }
+            }
+        }
+    };
+    look(0, least ? unordered(least) : -INFINITY);
+    if (each > U) {
+        // the num_out-th best so far: at least num_out logits of the piece reach it
+        __syncthreads();
+        const int have = min(count, kList);
+        rank_list(list, have, num, [&](int rank, uint64_t key) {
+            if (rank == num - 1) limit = unordered((uint32_t)(key >> 32));
+        });
+        __syncthreads();
+        for (int j0 = U; j0 < each; j0 += U) {
+            w.load_some(q, j0);
+            look(j0, limit);
+        }
+    }
+    float s, s1, s2, s3;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(s), "=f"(s1) : "l"(acc[0]));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(s2), "=f"(s3) : "l"(acc[1]));
+    s = warp_sum((s + s1) + (s2 + s3));
+    if (lane == 0) part[warp].y = s;
     __syncthreads();
     const int have = count;
-    for (int i = tid; i < have; i += kThreads) {
-        const uint64_t key = list[i];
-        int rank = 0;
-        for (int j = 0; j < have; ++j) rank += list[j] > key;
-        if (rank < num) out[rank] = key;
+    s = 0.f;
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) s += part[j].y;
+    if (!(s > 0.f && s < INFINITY) || have > kList) {   // the same in all threads
+        __syncthreads();
+        careful_piece<T, U>(w, num, list, out, sums + blockIdx.x);
+        return;
     }
+    if (tid == 0)
+        sums[blockIdx.x] = make_float2(M, s * exp2_ftz(fmaf(M, kLog2e, -c) + M * kLog2eRest));
+    rank_list(list, have, num, [&](int rank, uint64_t key) { out[rank] = key; });
     for (int i = have + tid; i < num; i += kThreads) out[i] = 0;
+}
+
+// ln t for t > 0 to about 2^-25, as two addends of which the first is exact: t = 2^e f,
+// e ln 2 in two parts and ln f of an f near 1.  (The 64-bit functions took half of the
+// joining kernel's time: this card's 64-bit rate is low.)
+__device__ __forceinline__ double log_of_sum(float t) {
+    int e = (int)(__float_as_uint(t) >> 23) - 127;
+    float f = __uint_as_float((__float_as_uint(t) & 0x7fffffu) | 0x3f800000u);   // [1, 2)
+    if (f > 1.4142135f) {
+        f *= 0.5f;
+        ++e;
+    }
+    // ln 2 = 0.693145751953125 (17 bits, so times e it is exact) + the rest
+    return (double)(e * 0.693145751953125f) + (double)(fmaf((float)e, 1.42860677e-6f, logf(f)));
 }
 
 // One request: joins its rows' pieces.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS)
-beam_join_kernel(const BeamSelectArgs p, int pieces, const uint64_t* __restrict__ keys,
-                 const float2* __restrict__ sums) {
+beam_join_kernel(const BeamSelectArgs p, int pieces, uint32_t per_beam_inv,
+                 const uint64_t* __restrict__ keys, const float2* __restrict__ sums) {
     extern __shared__ __align__(16) ValueKey candidates[];   // num_out x a thread's share
-    __shared__ ValueKey best_of[THREADS];
-    __shared__ ValueKey limit;
-    __shared__ double lse[BEAM_MAX_BEAMS];
-    __shared__ double score[BEAM_MAX_BEAMS];
+    __shared__ Threshold<THREADS, ValueKey> pick;
+    __shared__ double lse[BEAM_MAX_BEAMS], score[BEAM_MAX_BEAMS];
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x, num = p.num_out;
     if (tid == 0) count = 0;
+    if (tid < p.K) score[tid] = (double)tame(p.scores[(int64_t)b * p.K + tid]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // a row's maximum, then its pieces' sums relative to it; a warp a row
     for (int k = warp; k < p.K; k += THREADS / 32) {
         const float2* q = sums + ((int64_t)b * p.K + k) * pieces;
         float M = -INFINITY;
         for (int j = lane; j < pieces; j += 32) M = fmaxf(M, q[j].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        double s = 0.0;
+        M = warp_max(M);
+        float s = 0.f;
         for (int j = lane; j < pieces; j += 32)
-            if (q[j].y > 0.f) s += (double)q[j].y * exp((double)q[j].x - (double)M);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) {
-            lse[k] = s > 0.0 ? (double)M + log(s) : 0.0;
-            score[k] = (double)tame(p.scores[(int64_t)b * p.K + k]);
-        }
+            if (q[j].y > 0.f) s = fmaf(q[j].y, expf(q[j].x - M), s);
+        s = warp_sum(s);
+        if (lane == 0) lse[k] = s > 0.f ? (double)M + log_of_sum(s) : 0.0;
     }
     __syncthreads();
 
@@ -310,7 +519,7 @@ beam_join_kernel(const BeamSelectArgs p, int pieces, const uint64_t* __restrict_
         const uint64_t key = mine[i];
         ValueKey q{0, 0};
         if (key) {
-            const int k = i / per_beam;
+            const int k = per_beam == 1 ? i : (int)__umulhi((uint32_t)i, per_beam_inv);
             const float x = unordered((uint32_t)(key >> 32));
             const uint32_t v = 0xffffffffu - (uint32_t)key;
             const double val = x == -INFINITY || score[k] == -INFINITY
@@ -320,49 +529,44 @@ beam_join_kernel(const BeamSelectArgs p, int pieces, const uint64_t* __restrict_
         }
         return q;
     };
+    // neighbouring candidates, of one beam and good or bad together, go to different warps:
+    // the first bound is the worst warp's, and would be loose otherwise
+    const int first = lane * (THREADS / 32) + warp;
     ValueKey best{0, 0};
-    for (int i = tid; i < all; i += THREADS) {
+    for (int i = first; i < all; i += THREADS) {
         const ValueKey q = value(i);
         if (above(q, best)) best = q;
     }
-    if (threshold<THREADS>(best_of, &limit, best, num)) {
-        const ValueKey from = limit;
-        for (int i = tid; i < all; i += THREADS) {
+    if (pick.find(best, num)) {
+        const ValueKey from = pick.limit;
+        for (int i = first; i < all; i += THREADS) {
             const ValueKey q = value(i);
             if (exists(q) && !above(from, q)) candidates[atomicAdd(&count, 1)] = q;
         }
     }
     __syncthreads();
-    const int have = count;
-    for (int i = tid; i < have; i += THREADS) {
-        const ValueKey key = candidates[i];
-        int rank = 0;
-        for (int j = 0; j < have; ++j) rank += above(candidates[j], key);
-        if (rank < num) {
-            const uint32_t at = 0xffffffffu - (uint32_t)key.index;
-            const int64_t o = (int64_t)b * num + rank;
-            p.out_scores[o] = (float)unordered(key.value);
-            p.out_parents[o] = b * p.K + (int)(at / (uint32_t)p.V);
-            p.out_tokens[o] = (int)(at % (uint32_t)p.V);
-        }
-    }
+    rank_list(candidates, count, num, [&](int rank, const ValueKey& key) {
+        const uint32_t at = 0xffffffffu - (uint32_t)key.index;
+        const int64_t o = (int64_t)b * num + rank;
+        p.out_scores[o] = (float)unordered(key.value);
+        p.out_parents[o] = b * p.K + (int)(at / (uint32_t)p.V);
+        p.out_tokens[o] = (int)(at % (uint32_t)p.V);
+    });
 }
 
 struct Pieces {
-    int pieces, span;   // of a row; 16-byte vectors of one
+    int pieces, each;   // of a row; 16-byte vectors a thread
 };
-// A thread takes up to kShare values; fewer when that would leave SMs without a CTA
-// (four CTAs an SM keep enough loads in flight).
+// Enough pieces for kCtas CTAs an SM, none shorter than one vector a thread.
 Pieces split_row(int64_t rows, int32_t V, kda_dtype dtype) {
     const int N = dtype == KDA_BF16 ? 8 : 4;
-    const int64_t vectors = (V + N - 1) / N;
-    const int64_t most = kShare / N;                // vectors a thread
-    const int64_t ctas = 4 * (int64_t)(sm_count() > 0 ? sm_count() : 148);
-    int64_t each = (vectors * rows + ctas * kThreads - 1) / (ctas * kThreads);
-    each = each < 1 ? 1 : each > most ? most : each;
+    const int64_t blocks = ((int64_t)(V + N - 1) / N + kThreads - 1) / kThreads;   // one vector a thread
+    const int64_t ctas = kCtas * (int64_t)(sm_count() > 0 ? sm_count() : 148);
+    int64_t pieces = rows > 0 ? (ctas + rows - 1) / rows : 1;
+    pieces = pieces < blocks ? pieces : blocks;
     Pieces s;
-    s.span = (int)(each * kThreads);
-    s.pieces = (int)((vectors + s.span - 1) / s.span);
+    s.each = (int)((blocks + pieces - 1) / pieces);
+    s.pieces = (int)((blocks + s.each - 1) / s.each);
     return s;
 }
 
@@ -372,6 +576,25 @@ int join_share(const Pieces& s, int K, int num_out, int threads) {
 }
 
 size_t pad(size_t b) { return (b + 255) & ~(size_t)255; }
+
+template <typename T, int U>
+cudaError_t launch_pieces(const BeamSelectArgs& a, const Pieces& s, uint64_t* keys, float2* sums,
+                          cudaStream_t stream) {
+    if constexpr (U > 1) {
+        if (s.each <= U / 2) return launch_pieces<T, U / 2>(a, s, keys, sums, stream);
+    }
+    const size_t most = (size_t)a.num_out * (U * Logits<T>::N + 1);   // of a careful step
+    const size_t smem = (most > kList ? most : kList) * sizeof(uint64_t);
+    if (smem > 16 * 1024) {
+        const cudaError_t err =
+            cudaFuncSetAttribute(beam_piece_kernel<T, U>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (err != cudaSuccess) return err;
+    }
+    const unsigned grid = (unsigned)((int64_t)a.B * a.K * s.pieces);
+    beam_piece_kernel<T, U><<<grid, kThreads, smem, stream>>>(a, s.pieces, s.each, keys, sums);
+    return cudaGetLastError();
+}
 
 template <int THREADS>
 cudaError_t launch_join(const BeamSelectArgs& a, const Pieces& s, const uint64_t* keys,
@@ -395,7 +618,9 @@ cudaError_t launch_join(const BeamSelectArgs& a, const Pieces& s, const uint64_t
     c.stream = stream;
     c.attrs = &early;
     c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, beam_join_kernel<THREADS>, a, s.pieces, keys, sums);
+    // i / (pieces num_out) as a product: exact for i below 2^32 over the divisor
+    const uint32_t inv = (uint32_t)(((1ull << 32) + s.pieces * a.num_out - 1) / (s.pieces * a.num_out));
+    return cudaLaunchKernelEx(&c, beam_join_kernel<THREADS>, a, s.pieces, inv, keys, sums);
 }
 
 // ---------------------------------------------------------------- reordering
@@ -514,14 +739,9 @@ cudaError_t launch_beam_select(const BeamSelectArgs& a, char* ws, cudaStream_t s
     const Pieces s = split_row(rows, a.V, a.dtype);
     uint64_t* keys = reinterpret_cast<uint64_t*>(ws);
     float2* sums = reinterpret_cast<float2*>(ws + pad((size_t)rows * s.pieces * a.num_out * 8));
-    const unsigned grid = (unsigned)(rows * s.pieces);
-    const int share = s.span / kThreads * (a.dtype == KDA_BF16 ? 8 : 4);
-    const size_t smem = (size_t)a.num_out * share * sizeof(uint64_t);
-    if (a.dtype == KDA_BF16)
-        beam_piece_kernel<__nv_bfloat16><<<grid, kThreads, smem, stream>>>(a, s.pieces, s.span, keys, sums);
-    else
-        beam_piece_kernel<float><<<grid, kThreads, smem, stream>>>(a, s.pieces, s.span, keys, sums);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = a.dtype == KDA_BF16
+                                ? launch_pieces<__nv_bfloat16, 8>(a, s, keys, sums, stream)
+                                : launch_pieces<float, 8>(a, s, keys, sums, stream);
     if (err != cudaSuccess) return err;
     // 16 candidates a thread at most where 256 threads will do
     if (join_share(s, a.K, a.num_out, kThreads) <= 16)
