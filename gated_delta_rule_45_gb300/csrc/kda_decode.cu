@@ -51,6 +51,8 @@ __device__ __forceinline__ float gate_of(const void* alpha, int bh, size_t vi) {
 // parents[b] of S_in, a zero state for an entry outside [0, num_rows), and
 // written to row b of S.  Beams that share a parent read the same bytes; the
 // rest of the step is the same, so moving the states costs nothing of its own.
+// 32 requests of 8 beams, 32 heads of 128 x 128: 141 us for 0.90 GB (6.4 TB/s; 160 us
+// with loads that stay in L1, although beams share parents).
 template <int DK, typename T, int GATE, bool PARENTS>
 __global__ void __launch_bounds__(kDecodeWarps * 32)
 kda_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
@@ -99,8 +101,8 @@ kda_decode_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __r
             const float4* src = reinterpret_cast<const float4*>(src_bh + (size_t)r * DK);
 #pragma unroll
             for (int j = 0; j < Sh::VEC; ++j) {
-                if (!PARENTS) s[u][j] = __ldcs(src + j * Sh::LPR + sub);
-                else s[u][j] = live ? __ldg(src + j * Sh::LPR + sub) : make_float4(0.f, 0.f, 0.f, 0.f);
+                if (!PARENTS || live) s[u][j] = __ldcs(src + j * Sh::LPR + sub);
+                else s[u][j] = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
     }

@@ -486,9 +486,9 @@ __device__ __noinline__ bool expired(const TileSpace& w, uint64_t& t0) {
 // for the record of the tile j + 1 steps before (step = -1: towards lower indices,
 // +1: higher), then every warp applies the eight from the farthest to the nearest.
 // A map with A = 0 is where the walk starts; while none of the eight is one, the
-// eight are read again (few channels and many tokens: with the walk going on past
-// them 170000 tokens of one channel took 1.7 ms instead of FEW us).  Tiles from
-// `tiles` on hold no sequence and publish nothing.  All warps call it together.  When
+// eight are read again (with few channels a tile has hundreds of others before it that
+// are still unresolved, and a walk over all of them costs more than waiting for the
+// nearest).  Tiles from `tiles` on hold no sequence and publish nothing.  All warps call it together.  When
 // a wait runs out, here or elsewhere, the status word says so and the result is 0.
 template <int VEC>
 __device__ Vec<VEC> look_back(const TileSpace& w, int i, int step, int64_t tiles, int64_t ch,
@@ -970,27 +970,69 @@ __global__ void linrec_check_kernel(const int32_t* cu, int32_t N, int64_t T, int
         *status = KDA_ERR_DEVICE_INPUT;
 }
 
-template <typename T, int GATE>
-__global__ void __launch_bounds__(kThreads) linrec_step_kernel(const LinrecStepArgs p) {
+// One token a row: W neighbouring channels a thread, four where the head width allows
+// (16-byte accesses of the state and the fp32 gate), else one.  A streaming pass, bound by
+// HBM and, at a few megabytes, by its launch.
+template <typename T, int GATE, int W>
+__global__ void __launch_bounds__(kThreads) linrec_step_kernel(const LinrecStepArgs p, int blocks) {
     const int D = p.H * p.d;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= (int64_t)p.B * D) return;
-    const int b = (int)(i / D), c = (int)(i % D);
+    const int b = blockIdx.x / blocks;
+    const int c = ((blockIdx.x - b * blocks) * kThreads + threadIdx.x) * W;
+    if (c >= D) return;
     const int row = p.parents ? p.parents[b] : b;
-    const float h = row >= 0 && row < p.num_rows ? p.S[(int64_t)row * D + c] : 0.f;
-    float a, na;
-    if (GATE == KDA_GATE_CHANNEL_LOG_BF16) {
-        const float la = __bfloat162float(static_cast<const __nv_bfloat16*>(p.gate)[i]);
-        a = expf(la);
-        na = -expm1f(la);
+    const int64_t at = (int64_t)b * D + c;
+    const bool live = row >= 0 && row < p.num_rows;
+    const float* S = p.S + (live ? (int64_t)row * D + c : 0);
+    float h[W], a[W], na[W], x[W];
+    if constexpr (W == 4) {
+        const float4 s = live ? __ldcs(reinterpret_cast<const float4*>(S))
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        h[0] = s.x; h[1] = s.y; h[2] = s.z; h[3] = s.w;
     } else {
-        a = static_cast<const float*>(p.gate)[GATE == KDA_GATE_HEAD_F32 ? i / p.d : i];
-        na = 1.f - a;
+        h[0] = live ? *S : 0.f;
     }
-    const float xv = Elem<T>::load(static_cast<const T*>(p.x) + i);
-    const float out = fmaf(a, h, p.complement ? na * xv : xv);
-    p.S_out[i] = out;
-    Elem<T>::store(static_cast<T*>(p.y) + i, out);
+    auto load = [&](const auto* q, float (&out)[W]) {
+        using E = std::remove_cv_t<std::remove_pointer_t<decltype(q)>>;
+        if constexpr (W == 1) {
+            out[0] = Elem<E>::load(q);
+        } else if constexpr (sizeof(E) == 4) {
+            const float4 u = __ldcs(reinterpret_cast<const float4*>(q));
+            out[0] = u.x; out[1] = u.y; out[2] = u.z; out[3] = u.w;
+        } else {
+            const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
+            out[0] = __uint_as_float(u.x << 16); out[1] = __uint_as_float(u.x & 0xffff0000u);
+            out[2] = __uint_as_float(u.y << 16); out[3] = __uint_as_float(u.y & 0xffff0000u);
+        }
+    };
+    load(static_cast<const T*>(p.x) + at, x);
+    if (GATE == KDA_GATE_CHANNEL_LOG_BF16) {
+        load(static_cast<const __nv_bfloat16*>(p.gate) + at, a);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+            na[i] = -expm1f(a[i]);
+            a[i] = expf(a[i]);
+        }
+    } else {
+        if (GATE == KDA_GATE_HEAD_F32) {
+#pragma unroll
+            for (int i = 0; i < W; ++i) a[i] = static_cast<const float*>(p.gate)[b * (int64_t)p.H + c / p.d];
+        } else {
+            load(static_cast<const float*>(p.gate) + at, a);
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) na[i] = 1.f - a[i];
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) h[i] = fmaf(a[i], h[i], p.complement ? na[i] * x[i] : x[i]);
+    T* y = static_cast<T*>(p.y) + at;
+    if constexpr (W == 4) {
+        *reinterpret_cast<float4*>(p.S_out + at) = make_float4(h[0], h[1], h[2], h[3]);
+        store(y, Vec<2>{h[0], h[1]});
+        store(y + 2, Vec<2>{h[2], h[3]});
+    } else {
+        p.S_out[at] = h[0];
+        Elem<T>::store(y, h[0]);
+    }
 }
 
 template <typename F>
@@ -1177,11 +1219,15 @@ cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t s
 }
 
 cudaError_t launch_linrec_step(const LinrecStepArgs& a, cudaStream_t stream) {
-    const int64_t n = (int64_t)a.B * a.H * a.d;
+    const int D = a.H * a.d;
+    const bool wide = a.d % 4 == 0;
+    const int blocks = (D / (wide ? 4 : 1) + kThreads - 1) / kThreads;
+    if ((int64_t)a.B * blocks > INT32_MAX) return cudaErrorInvalidValue;
     return by_type(a.dtype, a.gate_format, [&](auto* t, auto g) {
         using T = std::remove_pointer_t<decltype(t)>;
-        linrec_step_kernel<T, decltype(g)::value>
-            <<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a);
+        constexpr int G = decltype(g)::value;
+        auto kernel = wide ? linrec_step_kernel<T, G, 4> : linrec_step_kernel<T, G, 1>;
+        kernel<<<(unsigned)(a.B * blocks), kThreads, 0, stream>>>(a, blocks);
         return cudaGetLastError();
     });
 }

@@ -19,7 +19,6 @@ gated linear recurrence of ``include/linrec.h``, and ``beam_select``,
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -595,23 +594,33 @@ def _check(what: str, t, dtype, shape) -> None:
 
 def _place(stream, *ts) -> int:
     """Raw stream to launch on; every tensor must be contiguous on the current device."""
-    dev = torch.cuda.current_device() if ts[0].is_cuda else -1
+    dev = ts[0].get_device()
     for t in ts:
-        if t is not None and (not t.is_cuda or not t.is_contiguous()):
-            raise ValueError("all tensors must be contiguous CUDA tensors")
-        if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors must be on the current CUDA device")
+        if t is not None and (t.get_device() != dev or dev < 0 or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+    return _stream_on(dev, stream)
+
+
+def _stream_on(dev: int, stream) -> int:
+    """Raw handle of `stream`, or of the current one, which must be the current device's.
+    (The small calls are bound by this module: torch.cuda.current_stream() alone would
+    take as long as the launch.)"""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("the tensors must be on the current CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream.device_index != dev:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device_index != dev:
         raise ValueError("the stream must belong to the current CUDA device")
     return stream.cuda_stream
 
 
-def _alloc(stream):
-    """Context in which memory is allocated for work on `stream`: the caching
-    allocator hands a block freed there only to later work of the same stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _empty(stream, shape, dtype, device):
+    """torch.empty for work on `stream`: the caching allocator hands a block that is freed
+    again only to later work of the stream it was allocated on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _p(t):
@@ -635,6 +644,16 @@ def linrec_workspace_size(num_seqs: int, total_tokens: int, H: int, d: int) -> i
     return load().linrec_prefill_workspace_size(num_seqs, total_tokens, H, d)
 
 
+def _linrec_inputs(x, a, S0, cu_seqlens, gate: str):
+    """Checked sizes (T, N, H, d, dtype code, gate code) of a packed batch."""
+    H, d, code, gcode = _linrec_args(x, a, gate, "T")
+    N = cu_seqlens.numel() - 1
+    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
+    if S0 is not None:
+        _check("S0", S0, torch.float32, (N, H, d))
+    return x.shape[0], N, H, d, code, gcode
+
+
 def linrec_prefill_into(x, a, S0, cu_seqlens, y, S_T, workspace, *, states=None,
                         gate: str = "channel", complement: bool = False, stream=None) -> None:
     """Enqueue linrec_prefill into preallocated outputs: h_t = a_t h_{t-1} + u_t per
@@ -647,13 +666,9 @@ def linrec_prefill_into(x, a, S0, cu_seqlens, y, S_T, workspace, *, states=None,
     [ceil(T / LINREC_CHUNK), H, d] fp32 or None, kept for ``linrec_backward``;
     workspace: uint8, at least ``linrec_workspace_size`` bytes.
     """
-    H, d, code, gcode = _linrec_args(x, a, gate, "T")
-    T, N = x.shape[0], cu_seqlens.numel() - 1
-    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
+    T, N, H, d, code, gcode = _linrec_inputs(x, a, S0, cu_seqlens, gate)
     _check("y", y, x.dtype, x.shape)
     _check("S_T", S_T, torch.float32, (N, H, d))
-    if S0 is not None:
-        _check("S0", S0, torch.float32, (N, H, d))
     if states is not None:
         _check("states", states, torch.float32, (-(-T // LINREC_CHUNK), H, d))
     raw = _place(stream, x, a, S0, cu_seqlens, y, S_T, states, workspace)
@@ -669,19 +684,22 @@ def linrec_prefill(x, a, S0, cu_seqlens, *, gate: str = "channel", complement: b
     """Allocate outputs with PyTorch and run linrec_prefill; returns (y, S_T), or with
     `save_states` (y, S_T, states) for ``linrec_backward``.  y of tokens past
     cu_seqlens[-1] is not written."""
-    H, d, _, _ = _linrec_args(x, a, gate, "T")
-    T, N, dev = x.shape[0], cu_seqlens.numel() - 1, x.device
-    nbytes = linrec_workspace_size(N, T, H, d)
+    T, N, H, d, code, gcode = _linrec_inputs(x, a, S0, cu_seqlens, gate)
+    raw = _place(stream, x, a, S0, cu_seqlens)
+    lib, dev = load(), x.device
+    nbytes = lib.linrec_prefill_workspace_size(N, T, H, d)
     if nbytes == 0:
         raise KdaError(ERR_UNSUPPORTED, "linrec_prefill")
-    with _alloc(stream):
-        y = torch.empty_like(x)
-        S_T = torch.empty((N, H, d), dtype=torch.float32, device=dev)
-        states = torch.empty((-(-T // LINREC_CHUNK), H, d), dtype=torch.float32,
-                             device=dev) if save_states else None
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    linrec_prefill_into(x, a, S0, cu_seqlens, y, S_T, ws, states=states, gate=gate,
-                        complement=complement, stream=stream)
+    y = _empty(stream, x.shape, x.dtype, dev)
+    S_T = _empty(stream, (N, H, d), torch.float32, dev)
+    states = _empty(stream, (-(-T // LINREC_CHUNK), H, d), torch.float32, dev) \
+        if save_states else None
+    ws = _empty(stream, nbytes, torch.uint8, dev)
+    st = lib.linrec_prefill(x.data_ptr(), a.data_ptr(), gcode, _p(S0), cu_seqlens.data_ptr(), N,
+                            T, H, d, code, int(complement), y.data_ptr(), S_T.data_ptr(),
+                            _p(states), ws.data_ptr(), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "linrec_prefill")
     if check_device_status:
         device_status(ws, stream=stream)
     return (y, S_T, states) if save_states else (y, S_T)
@@ -704,12 +722,10 @@ def linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, workspace, *, st
     to log a for "log_bf16") and optionally "dS0" [N, H, d]; workspace: uint8, at
     least ``linrec_backward_workspace_size`` bytes.
     """
-    H, d, code, gcode = _linrec_args(x, a, gate, "T")
-    T, N = x.shape[0], cu_seqlens.numel() - 1
+    T, N, H, d, code, gcode = _linrec_inputs(x, a, S0, cu_seqlens, gate)
     dx, dgate, dS0 = grads["dx"], grads["dgate"], grads.get("dS0")
-    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
     _check("dy", dy, x.dtype, x.shape)
-    for what, t in (("S0", S0), ("dS_T", dS_T), ("dS0", dS0)):
+    for what, t in (("dS_T", dS_T), ("dS0", dS0)):
         if t is not None:
             _check(what, t, torch.float32, (N, H, d))
     if states is not None:
@@ -729,16 +745,15 @@ def linrec_backward(x, a, S0, cu_seqlens, dy, dS_T=None, *, states=None, gate: s
                     complement: bool = False, stream=None, check_device_status: bool = False):
     """Allocate fp32 gradients with PyTorch and run linrec_backward; returns a dict with
     dx, dgate and dS0.  Rows of tokens past cu_seqlens[-1] are not written."""
-    H, d, _, _ = _linrec_args(x, a, gate, "T")
-    T, N, dev = x.shape[0], cu_seqlens.numel() - 1, x.device
+    T, N, H, d, _, _ = _linrec_inputs(x, a, S0, cu_seqlens, gate)
+    dev = x.device
     nbytes = linrec_backward_workspace_size(N, T, H, d, gate=gate, with_states=states is not None)
     if nbytes == 0:
         raise KdaError(ERR_UNSUPPORTED, "linrec_backward")
-    with _alloc(stream):
-        grads = {"dx": torch.empty(x.shape, dtype=torch.float32, device=dev),
-                 "dgate": torch.empty(a.shape, dtype=torch.float32, device=dev),
-                 "dS0": torch.empty((N, H, d), dtype=torch.float32, device=dev)}
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    grads = {"dx": _empty(stream, x.shape, torch.float32, dev),
+             "dgate": _empty(stream, a.shape, torch.float32, dev),
+             "dS0": _empty(stream, (N, H, d), torch.float32, dev)}
+    ws = _empty(stream, nbytes, torch.uint8, dev)
     linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, ws, states=states, gate=gate,
                          complement=complement, stream=stream)
     if check_device_status:
@@ -767,12 +782,11 @@ def linrec_decode_step(x, a, S, y=None, *, parents=None, S_out=None, gate: str =
         S_out = S
     else:
         _check("S_out", S_out, torch.float32, (B, H, d))
+    raw = _place(stream, x, a, S, parents, S_out, y)
     if y is None:
-        with _alloc(stream):
-            y = torch.empty_like(x)
+        y = _empty(stream, x.shape, x.dtype, x.device)
     else:
         _check("y", y, x.dtype, x.shape)
-    raw = _place(stream, x, a, S, parents, S_out, y)
     st = load().linrec_decode_step(_p(x), _p(a), gcode, _p(S), S.shape[0], _p(parents), B, H, d,
                                    code, int(complement), _p(y), _p(S_out), raw)
     if st != OK:
@@ -798,12 +812,11 @@ def decode_step_parents(q, k, v, alpha, beta, S_in, parents, S_out, o=None, *,
     _check("S_in", S_in, torch.float32, (S_in.shape[0], H, d_v, d_k))
     _check("S_out", S_out, torch.float32, (B, H, d_v, d_k))
     _check("parents", parents, torch.int32, (B,))
+    raw = _place(stream, q, k, v, alpha, beta, S_in, parents, S_out, o)
     if o is None:
-        with _alloc(stream):
-            o = torch.empty_like(v)
+        o = _empty(stream, v.shape, v.dtype, v.device)
     else:
         _check("o", o, q.dtype, v.shape)
-    raw = _place(stream, q, k, v, alpha, beta, S_in, parents, S_out, o)
     st = load().kda_decode_step_parents(_p(q), _p(k), _p(v), _p(alpha), gcode, _p(beta),
                                         _p(S_in), S_in.shape[0], _p(parents), _p(S_out), B, H,
                                         d_k, d_v, code, _p(o), raw)
@@ -830,7 +843,8 @@ def beam_select(logits, scores, num_out: int, *, finished=None, eos: int = 0, ou
     B, K = scores.shape
     V = logits.shape[1]
     _check("scores", scores, torch.float32, (B, K))
-    _check("logits", logits, logits.dtype, (B * K, V))
+    if logits.shape[0] != B * K:
+        raise ValueError(f"logits must have {B * K} rows, got {tuple(logits.shape)}")
     if finished is not None:
         if finished.dtype == torch.bool:
             finished = finished.view(torch.uint8)
@@ -838,26 +852,24 @@ def beam_select(logits, scores, num_out: int, *, finished=None, eos: int = 0, ou
     ld = logits.stride(0) if B * K > 1 else V
     if V > 1 and logits.stride(1) != 1:
         raise ValueError("each row of logits must be contiguous")
-    lib = load()
+    lib, dev = load(), scores.device
     nbytes = lib.beam_select_workspace_size(B, K, V, num_out)
     if nbytes == 0:
         raise KdaError(ERR_UNSUPPORTED if 1 <= num_out <= K * V else ERR_INVALID_ARG,
                        "beam_select")
-    with _alloc(stream):
-        if out is None:
-            buf = torch.empty((3, B, num_out), dtype=torch.int32, device=scores.device) \
-                if B * num_out % 4 == 0 else None
-            out = (buf[0].view(torch.float32), buf[1], buf[2]) if buf is not None else \
-                tuple(torch.empty((B, num_out), dtype=t, device=scores.device)
-                      for t in (torch.float32, torch.int32, torch.int32))
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=scores.device)
-    for what, t, dt in zip(("out scores", "out parents", "out tokens"), out,
-                           (torch.float32, torch.int32, torch.int32)):
-        _check(what, t, dt, (B, num_out))
-    if not logits.is_cuda or logits.get_device() != scores.get_device():
-        raise ValueError("all tensors must be contiguous CUDA tensors on one device")
-    raw = _place(stream, scores, finished, *out, workspace)
+    if logits.get_device() != scores.get_device():
+        raise ValueError("all tensors must be CUDA tensors on one device")
+    raw = _place(stream, scores, finished, workspace, *(out or ()))
+    if out is None:
+        out = (_empty(stream, (B, num_out), torch.float32, dev),
+               _empty(stream, (B, num_out), torch.int32, dev),
+               _empty(stream, (B, num_out), torch.int32, dev))
+    else:
+        for what, t, dt in zip(("out scores", "out parents", "out tokens"), out,
+                               (torch.float32, torch.int32, torch.int32)):
+            _check(what, t, dt, (B, num_out))
+    if workspace is None:
+        workspace = _empty(stream, nbytes, torch.uint8, dev)
     st = lib.beam_select(_p(logits), ld, _p(scores), _p(finished), B, K, V, num_out, eos, code,
                          _p(out[0]), _p(out[1]), _p(out[2]), _p(workspace),
                          workspace.numel() * workspace.element_size(), raw)
