@@ -176,8 +176,21 @@ struct Gate {
         return r;
     }
 };
-// log a in bf16: exp by the accurate function, since a state multiplies up to
-// thousands of gates; 1 - a from expm1, since 1 - exp would lose it near 1.
+// a = e^(log a) as 2^(log a log2 e + s) 2^-s, three instructions where the full function
+// takes nine (625 -> 562 us for 131072 x 4096).  The special-function unit cuts its
+// argument off after 24 fractional bits, which by itself leaves gates near 1, of which a
+// state multiplies hundreds, 2e-8 too small on average; s moves their argument to where
+// the multiply-add has rounded it to those bits already.  s is one of the values whose
+// 2^-s is a float to 1e-12.  Measured over all bf16 inputs down to log a = -1: at most
+// 1.6e-7 of the gate, 1e-8 or less on average (the full function: 1.1e-7 and 1.5e-8).
+// Below the normal numbers the gate is 0.
+__device__ __forceinline__ float gate_exp(float la) {
+    float a;
+    asm("ex2.approx.ftz.f32 %0, %1;"
+        : "=f"(a) : "f"(fmaf(la, 1.4426950408889634f, 0x1.8ca934p-1f)));
+    return a * 0x1.2b4368p-1f;
+}
+// log a in bf16; 1 - a from expm1, since 1 - exp would lose it near 1.
 template <int VEC>
 struct Gate<KDA_GATE_CHANNEL_LOG_BF16, VEC> {
     Piece<__nv_bfloat16, VEC> raw;
@@ -293,7 +306,7 @@ __device__ __forceinline__ void expand_gate(Gate<GATE, VEC> (&a)[R]) {
         for (int r = 0; r < R; ++r) {
             const Vec<VEC> la = a[r].raw.get();
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) a[r].f.v[v] = expf(la.v[v]);
+            for (int v = 0; v < VEC; ++v) a[r].f.v[v] = gate_exp(la.v[v]);
         }
     }
 }
@@ -326,7 +339,8 @@ struct Offsets {
 };
 
 // True when the offsets are valid.  Up to kSelfCheck sequences are checked here
-// (every CTA for itself), more by linrec_check_kernel before the launch.
+// (every CTA for itself), more by linrec_check_kernel before the launch.  Waits for that
+// one and for the fill of the workspace: nothing of it is touched before.
 __device__ bool read_offsets(Offsets& o, const int32_t* cu, int N, int64_t T,
                              const int32_t* status) {
     bool bad = false;
@@ -339,9 +353,11 @@ __device__ bool read_offsets(Offsets& o, const int32_t* cu, int N, int64_t T,
             bad |= i == 0 ? c != 0 : c < cu[i - 1];
             if (i == N) bad |= (int64_t)c > T;
         }
+        asm volatile("griddepcontrol.wait;" ::: "memory");
     } else {
         for (int j = threadIdx.x; j < count; j += kThreads)
             o.sample[j] = cu[min((int64_t)j * stride, (int64_t)N)];
+        asm volatile("griddepcontrol.wait;" ::: "memory");
         bad = *reinterpret_cast<const volatile int32_t*>(status) == KDA_ERR_DEVICE_INPUT;
     }
     if (threadIdx.x == 0) {
@@ -614,12 +630,13 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
     T* x = reinterpret_cast<T*>(row_area + warp * Area::kBytes + Area::kAt);
 
     const int64_t tiles = (int64_t)w.nt * w.ct;
-    int64_t tile = first_tile(w, &next_ticket);
-    if (!read_offsets(off, cu, N, p.total_tokens, w.status)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) *w.status = KDA_ERR_DEVICE_INPUT;
-        return;
+    const bool valid = read_offsets(off, cu, N, p.total_tokens, w.status);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (valid) clear_status(w, N);
+        else *w.status = KDA_ERR_DEVICE_INPUT;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) clear_status(w, N);
+    if (!valid) return;
+    int64_t tile = first_tile(w, &next_ticket);
     const int64_t end = cu[N], live_tiles = (end + kTile - 1) / kTile;
     copy_empty(cu, N, D, p.S0, p.S_T);
 
@@ -767,12 +784,13 @@ linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict
     float* f = reinterpret_cast<float*>(row_area + warp * Area::kBytes + 2 * Area::kRaw);
 
     const int64_t tiles = (int64_t)w.nt * w.ct;
-    int64_t tile = first_tile(w, &next_ticket);
-    if (!read_offsets(off, cu, N, p.total_tokens, w.status)) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) *w.status = KDA_ERR_DEVICE_INPUT;
-        return;
+    const bool valid = read_offsets(off, cu, N, p.total_tokens, w.status);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        if (valid) clear_status(w, N);
+        else *w.status = KDA_ERR_DEVICE_INPUT;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) clear_status(w, N);
+    if (!valid) return;
+    int64_t tile = first_tile(w, &next_ticket);
     const int64_t end = cu[N], live_tiles = (end + LINREC_CHUNK - 1) / LINREC_CHUNK;
     copy_empty(cu, N, D, p.dS_T, p.dS0);
 
@@ -961,6 +979,22 @@ linrec_head_sum_kernel(const float* __restrict__ part, const int32_t* cu, int32_
     }
 }
 
+// Fills the workspace with 0xff bytes, but for the status word when `keep`.
+__global__ void __launch_bounds__(kThreads)
+linrec_fill_kernel(char* ws, size_t bytes, bool keep) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    const uint4 ones = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (size_t i = blockIdx.x * (size_t)kThreads + threadIdx.x; i < bytes / 16;
+         i += (size_t)gridDim.x * kThreads) {
+        if (i == 0 && keep) {
+            uint32_t* w = reinterpret_cast<uint32_t*>(ws);
+            w[1] = w[2] = w[3] = ~0u;
+        } else {
+            reinterpret_cast<uint4*>(ws)[i] = ones;
+        }
+    }
+}
+
 // Offsets of more sequences than a CTA checks by itself.
 __global__ void linrec_check_kernel(const int32_t* cu, int32_t N, int64_t T, int32_t* status) {
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -1010,7 +1044,7 @@ __global__ void __launch_bounds__(kThreads) linrec_step_kernel(const LinrecStepA
 #pragma unroll
         for (int i = 0; i < W; ++i) {
             na[i] = -expm1f(a[i]);
-            a[i] = expf(a[i]);
+            a[i] = gate_exp(a[i]);
         }
     } else {
         if (GATE == KDA_GATE_HEAD_F32) {
@@ -1068,6 +1102,9 @@ TileLayout tile_layout(int64_t T, int64_t D, int rows) {   // rows: tokens a war
     return L;
 }
 
+// Whether the tiles need a workspace filled beforehand.
+bool filled(const LinrecArgs& a, const TileLayout& L) { return L.nt > 1 || a.num_seqs > kSelfCheck; }
+
 // Fills the workspace (keeping the status word of an earlier pass) and checks the
 // offsets of large batches.
 cudaError_t start_tiles(const LinrecArgs& a, const TileLayout& L, char* ws, bool keep_status,
@@ -1078,9 +1115,12 @@ cudaError_t start_tiles(const LinrecArgs& a, const TileLayout& L, char* ws, bool
     w.nt = (int32_t)L.nt;
     w.ct = (int32_t)L.ct;
     w.Dp = L.Dp;
-    if (L.nt > 1 || a.num_seqs > kSelfCheck) {
-        const size_t from = keep_status ? 4 : 0;
-        const cudaError_t err = cudaMemsetAsync(ws + from, 0xff, L.end - from, stream);
+    if (filled(a, L)) {
+        const size_t blocks = (L.end / 16 + kThreads - 1) / kThreads;
+        const size_t most = 4 * (size_t)(sm_count() > 0 ? sm_count() : 1);
+        linrec_fill_kernel<<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, stream>>>(
+            ws, L.end, keep_status);
+        const cudaError_t err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }
     if (a.num_seqs > kSelfCheck && !keep_status) {
@@ -1105,17 +1145,26 @@ cudaError_t by_tile(const LinrecArgs& a, F&& f) {
     });
 }
 
-template <typename K, typename... A>
-cudaError_t launch_tiles(K kernel, const TileLayout& L, int ctas, int smem, cudaStream_t stream,
-                         const A&... args) {
+// After a fill the kernel starts while that still runs: it reads its offsets meanwhile
+// and waits before its first ticket (3 us less a call than after a memset).
+template <typename K>
+cudaError_t configure_tiles(K kernel, const TileLayout& L, bool early, int smem, cudaStream_t stream,
+                         cudaLaunchConfig_t& c, cudaLaunchAttribute& attr) {
     if (smem > 32 * 1024) {   // above what every kernel may have with its static part
         const cudaError_t err =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
     }
-    const int64_t tiles = L.nt * L.ct, most = (int64_t)ctas * sm_count();
-    kernel<<<(unsigned)(tiles < most ? tiles : most > 0 ? most : 1), kThreads, smem, stream>>>(args...);
-    return cudaGetLastError();
+    const int64_t tiles = L.nt * L.ct, most = 2 * (int64_t)sm_count();
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    c.gridDim = dim3((unsigned)(tiles < most ? tiles : most > 0 ? most : 1));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = stream;
+    c.attrs = &attr;
+    c.numAttrs = early ? 1 : 0;
+    return cudaSuccess;
 }
 
 cudaError_t run_forward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
@@ -1127,8 +1176,12 @@ cudaError_t run_forward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(vec)::value;
         constexpr bool C = decltype(comp)::value;
-        return launch_tiles(linrec_fwd_kernel<T, decltype(g)::value, C, V>, L, 2,
-                            kWarps * FwdRows<T, C, V>::kBytes, stream, a, w);
+        auto kernel = linrec_fwd_kernel<T, decltype(g)::value, C, V>;
+        cudaLaunchConfig_t c = {};
+        cudaLaunchAttribute attr;
+        const cudaError_t set = configure_tiles(kernel, L, filled(a, L),
+                                             kWarps * FwdRows<T, C, V>::kBytes, stream, c, attr);
+        return set == cudaSuccess ? cudaLaunchKernelEx(&c, kernel, a, w) : set;
     });
 }
 
@@ -1206,9 +1259,12 @@ cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t s
     err = by_tile(a, [&](auto* t, auto g, auto comp, auto vec) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int V = decltype(vec)::value;
-        return launch_tiles(linrec_bwd_kernel<T, decltype(g)::value, decltype(comp)::value, V>, L,
-                            2, kWarps * BwdRows<T, V>::kBytes, stream, a, w,
-                            states, dgate, mode);
+        auto kernel = linrec_bwd_kernel<T, decltype(g)::value, decltype(comp)::value, V>;
+        cudaLaunchConfig_t c = {};
+        cudaLaunchAttribute attr;
+        const cudaError_t set = configure_tiles(kernel, L, filled(a, L),
+                                             kWarps * BwdRows<T, V>::kBytes, stream, c, attr);
+        return set == cudaSuccess ? cudaLaunchKernelEx(&c, kernel, a, w, states, dgate, mode) : set;
     });
     if (err != cudaSuccess || parts == 1 || a.total_tokens == 0) return err;
     const int64_t blocks = (a.total_tokens * a.H + kWarps - 1) / kWarps;
