@@ -533,7 +533,10 @@ static kda_status linrec_check(int64_t rows, int32_t num_seqs, int32_t H, int32_
     if (input != LINREC_PLAIN && input != LINREC_COMPLEMENT) return KDA_ERR_INVALID_ARG;
     if (d > 65536 || (int64_t)H * d > (1 << 20) || rows > (int64_t)INT32_MAX - LINREC_CHUNK)
         return KDA_ERR_UNSUPPORTED;
-    if ((int64_t)num_seqs * H * d >= (int64_t)1 << 40) return KDA_ERR_UNSUPPORTED;
+    // tiles and rows are counted in 32 bits
+    if (num_seqs > (1 << 30) || (int64_t)num_seqs * H * d >= (int64_t)1 << 40 ||
+        rows * H * d >= (int64_t)1 << 45)
+        return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }
 

@@ -42,8 +42,8 @@ typedef enum {
 #define LINREC_CHUNK 128
 
 /*
- * Bytes of device workspace linrec_prefill needs: about total_tokens x H x d / 10
- * bytes.  Returns 0 for a size it does not support.
+ * Bytes of device workspace linrec_prefill needs: about total_tokens x H x d / 32
+ * + num_seqs x H x d x 4.  Returns 0 for a size it does not support.
  * Contents need no initialisation and are overwritten by every call.
  */
 size_t linrec_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t H,
@@ -70,8 +70,9 @@ size_t linrec_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, int
  *
  * kda_prefill_device_status(workspace) reports device-detected errors
  * (KDA_ERR_DEVICE_INPUT; KDA_ERR_DEVICE_TIMEOUT if a wait of the time-axis
- * scan ran out).  Supported: H >= 1, 1 <= d <= 65536, H x d <= 2^20,
- * total_tokens <= 2^31 - 1 - 128, num_seqs x H x d < 2^40.  Any d, odd ones too.
+ * scan ran out).  Supported: H >= 1, 1 <= d <= 65536, H x d <= 2^20 (odd widths
+ * too), total_tokens <= 2^31 - 1 - 128, total_tokens x H x d < 2^45, num_seqs <= 2^30,
+ * num_seqs x H x d < 2^40.
  */
 kda_status linrec_prefill(const void* x, const void* gate, kda_gate_format gate_format,
                           const float* S0, const int32_t* cu_seqlens, int32_t num_seqs,

@@ -44,7 +44,7 @@ def _prefill(lib, **kw):
 @pytest.mark.parametrize("kw,expect", [
     (dict(N=-1), 1), (dict(T=-1), 1), (dict(H=0), 1), (dict(d=0), 1), (dict(dtype=4), 1),
     (dict(fmt=3), 1), (dict(input=2), 1), (dict(d=70000), 2), (dict(H=2048, d=1024), 2),
-    (dict(T=2 ** 31 - 1), 2),
+    (dict(T=2 ** 31 - 1), 2), (dict(N=2 ** 30 + 1), 2), (dict(T=2 ** 30, d=65536), 2),
     (dict(cu=None), 1), (dict(ws=None), 1), (dict(S_T=None), 1), (dict(x=None), 1),
     (dict(gate=None), 1), (dict(y=None), 1), (dict(ws_bytes=8), 1),
     (dict(x=1 * M + 4), 1), (dict(states=7 * M + 8), 1),
