@@ -28,7 +28,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kList = 1024;  // logits the fast pass may list
-constexpr int kCtas = 8;     // an SM, resident or waiting
+constexpr int kJoin = 16;    // candidates a thread of the joining kernel, with 256 threads
+constexpr int kParts = 8;    // most vectors a thread of a piece's first part
+constexpr int kCtas = 4;     // an SM
 
 // 16 bytes of logits.
 template <typename T>
@@ -557,15 +559,23 @@ beam_join_kernel(const BeamSelectArgs p, int pieces, uint32_t per_beam_inv,
 struct Pieces {
     int pieces, each;   // of a row; 16-byte vectors a thread
 };
-// Enough pieces for kCtas CTAs an SM, none shorter than one vector a thread.
-Pieces split_row(int64_t rows, int32_t V, kda_dtype dtype) {
+// Pieces for kCtas CTAs an SM, none shorter than one vector a thread: more pieces leave
+// more candidates to join (4 x 8 x 128000 fp32 logits: 28 us with 3 CTAs an SM, 39 with
+// 8, 82 with 16; 64 x 8 x 128000 bf16: 50, 52, 60).  Nor so long that the logits above
+// the bound of a piece's first part, num_out a part on average, outgrow its list
+// (64 x 8 x 250000 in one piece a row: 410 us, in two 126).
+Pieces split_row(int64_t rows, int32_t K, int32_t V, int32_t num_out, kda_dtype dtype) {
     const int N = dtype == KDA_BF16 ? 8 : 4;
     const int64_t blocks = ((int64_t)(V + N - 1) / N + kThreads - 1) / kThreads;   // one vector a thread
     const int64_t ctas = kCtas * (int64_t)(sm_count() > 0 ? sm_count() : 148);
+    const int64_t longest = kParts * kList / 4 / num_out;
     int64_t pieces = rows > 0 ? (ctas + rows - 1) / rows : 1;
     pieces = pieces < blocks ? pieces : blocks;
+    const int64_t joined = kJoin * kThreads / (K * num_out);   // 32 beams, 64 of 260000: 136 us without
+    if (pieces > joined) pieces = joined > 1 ? joined : 1;
     Pieces s;
     s.each = (int)((blocks + pieces - 1) / pieces);
+    if (s.each > longest) s.each = (int)longest;
     s.pieces = (int)((blocks + s.each - 1) / s.each);
     return s;
 }
@@ -726,7 +736,7 @@ size_t beam_select_bytes(int32_t B, int32_t K, int32_t V, int32_t num_out) {
     const int64_t rows = (int64_t)B * K;
     size_t most = 256;
     for (kda_dtype t : {KDA_BF16, KDA_FP32}) {
-        const Pieces s = split_row(rows, V, t);
+        const Pieces s = split_row(rows, K, V, num_out, t);
         const size_t n = (size_t)rows * s.pieces;
         const size_t b = pad(n * num_out * sizeof(uint64_t)) + pad(n * sizeof(float2));
         most = b > most ? b : most;
@@ -736,15 +746,14 @@ size_t beam_select_bytes(int32_t B, int32_t K, int32_t V, int32_t num_out) {
 
 cudaError_t launch_beam_select(const BeamSelectArgs& a, char* ws, cudaStream_t stream) {
     const int64_t rows = (int64_t)a.B * a.K;
-    const Pieces s = split_row(rows, a.V, a.dtype);
+    const Pieces s = split_row(rows, a.K, a.V, a.num_out, a.dtype);
     uint64_t* keys = reinterpret_cast<uint64_t*>(ws);
     float2* sums = reinterpret_cast<float2*>(ws + pad((size_t)rows * s.pieces * a.num_out * 8));
     const cudaError_t err = a.dtype == KDA_BF16
-                                ? launch_pieces<__nv_bfloat16, 8>(a, s, keys, sums, stream)
-                                : launch_pieces<float, 8>(a, s, keys, sums, stream);
+                                ? launch_pieces<__nv_bfloat16, kParts>(a, s, keys, sums, stream)
+                                : launch_pieces<float, kParts>(a, s, keys, sums, stream);
     if (err != cudaSuccess) return err;
-    // 16 candidates a thread at most where 256 threads will do
-    if (join_share(s, a.K, a.num_out, kThreads) <= 16)
+    if (join_share(s, a.K, a.num_out, kThreads) <= kJoin)
         return launch_join<kThreads>(a, s, keys, sums, stream);
     return launch_join<1024>(a, s, keys, sums, stream);
 }
