@@ -31,8 +31,8 @@ size_t beam_select_workspace_size(int32_t B, int32_t K, int32_t V, int32_t num_o
  *
  *     scores[b][k] + logits[b K + k][v] - log sum_w exp(logits[b K + k][w]),
  *
- * formed in 64 bits from the fp32 or bf16 logits (the sum of exponentials in
- * 32 bits within a piece of the row); a finished beam has one candidate, token
+ * formed in 64 bits from the fp32 or bf16 logits and a logarithm of the sum
+ * good to about 1e-7 (equal rows get equal ones); a finished beam has one candidate, token
  * `eos` at scores[b][k], and its logits are not read.  Candidates are ordered
  * by value, larger first, equal values by k V + v, smaller first.
  *
