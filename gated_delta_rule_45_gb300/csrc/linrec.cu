@@ -3,12 +3,12 @@
 //
 // Mathematics.  Every channel is a chain of affine maps h -> a h + u, and maps
 // compose: over a run of tokens h_out = A h_in + B with A the product of the
-// gates and B the run's result from zero.  A tile of 128 tokens x 64 channels
-// lives in the registers of one CTA: each of its eight warps holds 16 tokens
-// (two channels a lane), forms its (A, B), and once the state that enters the
-// tile is known every warp starts from its own entry state and walks its
-// tokens again in registers.  So x and the gate are read from memory once and
-// y is written once.
+// gates and B the run's result from zero.  A tile of 256 tokens (backward 128) x 64
+// channels belongs to one CTA: each of its eight warps takes 32 (16) tokens, two
+// channels a lane, with the gates in registers and the rows in shared memory, forms
+// its (A, B), and once the state that enters the tile is known every warp starts from
+// its own entry state and walks its tokens again.  So x and the gate are read from
+// memory once and y is written once.
 //
 // The packed token axis is cut into tiles regardless of sequences.  At a
 // sequence's first token the carried state is replaced by S0 (replaced, not
@@ -34,7 +34,9 @@
 // us for 3.2 GB (5.8 TB/s), of 64 ragged ones, 266240 x 4096, 1343 us for 8.7 GB (6.5);
 // backward of 8 x 4096 x 4096 380 us for 2.1 GB (5.7).  32 tokens a warp and two CTAs an SM
 // hold 192 KB of inputs on an SM, which covers the waits for the tiles before; 16 tokens
-// and three CTAs took 10 % longer.
+// and three CTAs took 10 % longer.  With one gate a head there are fewer bytes for the same
+// instructions, and those bound it: 8 x 4096 x 4096 forward 142 us for 0.54 GB (3.8 TB/s),
+// backward 346 us for 1.1 GB (3.1).
 #include "kda_internal.h"
 
 #include <type_traits>
@@ -190,6 +192,13 @@ struct Gate {
         return r;
     }
 };
+// One gate a head: a lane's channels share it (see lane_channels).
+template <int VEC>
+struct Gate<KDA_GATE_HEAD_F32, VEC> {
+    float f;
+    __device__ __forceinline__ Vec<VEC> a() const { return fill<VEC>(f); }
+    __device__ __forceinline__ Vec<VEC> na() const { return fill<VEC>(1.f - f); }
+};
 // a = e^(log a) as 2^(log a log2 e + s) 2^-s, three instructions where the full function
 // takes nine (625 -> 562 us for 131072 x 4096).  The special-function unit cuts its
 // argument off after 24 fractional bits, which by itself leaves gates near 1, of which a
@@ -280,17 +289,10 @@ __device__ __forceinline__ void take_gate(Gate<GATE, VEC> (&a)[R], const LinrecA
                                           int64_t t0, int64_t D, int c0, bool full, int left,
                                           bool on, int lane) {
     if constexpr (GATE == KDA_GATE_HEAD_F32) {
-        const int ch = c0 + lane * VEC, last = (int)D - 1;
-        const int h0 = min(ch, last) / p.d, h1 = min(ch + VEC - 1, last) / p.d;
-        const float* g = static_cast<const float*>(p.gate) + t0 * p.H;
+        const float* g = static_cast<const float*>(p.gate) + t0 * p.H +
+                         min(c0 + lane * VEC, (int)D - 1) / p.d;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            a[r].f = fill<VEC>(0.f);
-            if (full || r < left) {
-                a[r].f.v[0] = g[r * p.H + h0];
-                a[r].f.v[VEC - 1] = VEC == 2 && h1 != h0 ? g[r * p.H + h1] : a[r].f.v[0];
-            }
-        }
+        for (int r = 0; r < R; ++r) a[r].f = full || r < left ? g[r * p.H] : 0.f;
     } else {
         using G = std::conditional_t<GATE == KDA_GATE_CHANNEL_LOG_BF16, __nv_bfloat16, float>;
         const G* g = static_cast<const G*>(p.gate) + t0 * D + c0;
@@ -624,8 +626,13 @@ struct FwdRows {
     static constexpr int kAt = COMP ? kBytes - R * 32 * VEC * (int)sizeof(T) : 0;
 };
 
+// CTAs an SM: gates of one value a row leave registers, and bf16 rows shared memory, for
+// three (8 x 4096 tokens of 4096 channels: 142 us, with two 151).
+template <typename T, int GATE, bool COMP>
+constexpr int kFwdCtas = GATE == KDA_GATE_HEAD_F32 && sizeof(T) == 2 && !COMP ? 3 : 2;
+
 template <typename T, int GATE, bool COMP, int VEC>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, (kFwdCtas<T, GATE, COMP>))
 linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
     constexpr int R = kFwdRows, kTile = kWarps * R;
     using Area = FwdRows<T, COMP, VEC>;
@@ -786,6 +793,7 @@ linrec_fwd_kernel(const LinrecArgs p, const TileSpace w) {
 //   kHeadWide: every channel's term goes to a buffer, summed afterwards (widths
 //     that neither divide 64 nor are a multiple of it)
 enum : int { kNoHead = 0, kHeadRow = 1, kHeadWide = 2 };
+constexpr int kFewParts = 8;   // summed by one thread
 
 // Per warp: rows of x and dy as stored, and of f in fp32 (see below).
 template <typename T, int VEC>
@@ -1010,16 +1018,41 @@ linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict
             }
         }
         if (sum_lanes) {
-            // lanes that share a head (or one of its 64-channel parts) add up
+            // lanes that share a head (or one of its 64-channel parts) add up; [T][H][parts]:
+            // the part's index is the channel over its width
             const int part = p.d < 32 * VEC ? p.d : 32 * VEC, width = part / VEC;
+            const int64_t out = t0 * (D / part) + ch / part;
+            float s[R];
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const Vec<VEC> da = staged<float, VEC>(f, r, lane);
-                float s = on && r < left ? da.v[0] + (VEC == 2 ? da.v[VEC - 1] : 0.f) : 0.f;
-                for (int o = width >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-                // [T][H][parts]: the part's index is the channel over its width
-                if (on && r < left && (lane & (width - 1)) == 0)
-                    dgate[(t0 + r) * (D / part) + ch / part] = s;
+                s[r] = on && r < left ? da.v[0] + (VEC == 2 ? da.v[VEC - 1] : 0.f) : 0.f;
+            }
+            if (width == 32 && R == 16) {
+                // all lanes: each exchange halves the rows a lane carries, so that lanes 2 r
+                // and 2 r + 1 end with row r
+#pragma unroll
+                for (int o = 16, n = R / 2; o > 1; o >>= 1, n >>= 1) {
+                    const bool upper = lane & o;
+#pragma unroll
+                    for (int r = 0; r < n; ++r) {
+                        const float give = upper ? s[r] : s[r + n];
+                        s[r] = (upper ? s[r + n] : s[r]) + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+                }
+                s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+                if ((lane & 1) == 0 && lane / 2 < left) dgate[out + lane / 2 * (D / part)] = s[0];
+            } else {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    if (o < width) {
+#pragma unroll
+                        for (int r = 0; r < R; ++r) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+                    if (on && r < left && (lane & (width - 1)) == 0) dgate[out + r * (D / part)] = s[r];
             }
         }
         __syncthreads();
@@ -1027,13 +1060,23 @@ linrec_bwd_kernel(const LinrecArgs p, const TileSpace w, const float* __restrict
     }
 }
 
-// dgate[t][h] = the sum of the head's `parts` terms, one warp each.
+// dgate[t][h] = the sum of the head's `parts` terms: a thread each for few terms, in order,
+// a warp each for many.
 __global__ void __launch_bounds__(kThreads)
 linrec_head_sum_kernel(const float* __restrict__ part, const int32_t* cu, int32_t N, int32_t H,
                        int32_t parts, float* __restrict__ dgate, const int32_t* status) {
     if (N == 0 || *status == KDA_ERR_DEVICE_INPUT) return;
-    const int lane = threadIdx.x & 31;
     const int64_t rows = (int64_t)cu[N] * H;
+    if (parts <= kFewParts) {
+        for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < rows;
+             i += (int64_t)gridDim.x * kThreads) {
+            float s = 0.f;
+            for (int j = 0; j < parts; ++j) s += part[i * parts + j];
+            dgate[i] = s;
+        }
+        return;
+    }
+    const int lane = threadIdx.x & 31;
     for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < rows;
          i += (int64_t)gridDim.x * kWarps) {
         float s = 0.f;
@@ -1149,17 +1192,22 @@ cudaError_t by_type(kda_dtype dtype, int gate, F&& f) {
 
 size_t pad(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// Two channels a lane need rows on a 4-byte (bf16) grid: an even row width.
+// Two channels a lane need rows on a 4-byte (bf16) grid, an even row width, and with a
+// head gate heads of an even width.
 int lane_channels(int64_t D) { return D % 2 == 0 ? 2 : 1; }
+int lane_channels(int64_t D, int32_t d, int gate_format) {
+    return gate_format == KDA_GATE_HEAD_F32 && d % 2 != 0 ? 1 : lane_channels(D);
+}
 
 struct TileLayout {
     int64_t nt, ct, Dp;
     size_t end;
 };
-TileLayout tile_layout(int64_t T, int64_t D, int rows) {   // rows: tokens a warp
+// rows: tokens a warp; lanes: channels a lane (the wider tiles need the larger workspace).
+TileLayout tile_layout(int64_t T, int64_t D, int rows, int lanes) {
     TileLayout L;
     const int64_t tile = kWarps * rows;
-    const int64_t width = 32 * lane_channels(D);
+    const int64_t width = 32 * lanes;
     L.nt = T > 0 ? (T + tile - 1) / tile : 1;
     L.ct = (D + width - 1) / width;
     L.Dp = L.ct * width;
@@ -1203,8 +1251,9 @@ template <typename F>
 cudaError_t by_tile(const LinrecArgs& a, F&& f) {
     return by_type(a.dtype, a.gate_format, [&](auto* t, auto g) {
         auto pick = [&](auto comp) {
-            return lane_channels((int64_t)a.H * a.d) == 2 ? f(t, g, comp, Int<2>())
-                                                          : f(t, g, comp, Int<1>());
+            return lane_channels((int64_t)a.H * a.d, a.d, a.gate_format) == 2
+                       ? f(t, g, comp, Int<2>())
+                       : f(t, g, comp, Int<1>());
         };
         return a.complement ? pick(std::true_type()) : pick(std::false_type());
     });
@@ -1213,14 +1262,15 @@ cudaError_t by_tile(const LinrecArgs& a, F&& f) {
 // After a fill the kernel starts while that still runs: it reads its offsets meanwhile
 // and waits before its first ticket (3 us less a call than after a memset).
 template <typename K>
-cudaError_t configure_tiles(K kernel, const TileLayout& L, bool early, int smem, cudaStream_t stream,
-                         cudaLaunchConfig_t& c, cudaLaunchAttribute& attr) {
+cudaError_t configure_tiles(K kernel, const TileLayout& L, int ctas, bool early, int smem,
+                            cudaStream_t stream, cudaLaunchConfig_t& c,
+                            cudaLaunchAttribute& attr) {
     if (smem > 32 * 1024) {   // above what every kernel may have with its static part
         const cudaError_t err =
             cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
     }
-    const int64_t tiles = L.nt * L.ct, most = 2 * (int64_t)sm_count();
+    const int64_t tiles = L.nt * L.ct, most = ctas * (int64_t)sm_count();
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     c.gridDim = dim3((unsigned)(tiles < most ? tiles : most > 0 ? most : 1));
@@ -1233,7 +1283,8 @@ cudaError_t configure_tiles(K kernel, const TileLayout& L, bool early, int smem,
 }
 
 cudaError_t run_forward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
-    const TileLayout L = tile_layout(a.total_tokens, (int64_t)a.H * a.d, kFwdRows);
+    const TileLayout L = tile_layout(a.total_tokens, (int64_t)a.H * a.d, kFwdRows,
+                                     lane_channels((int64_t)a.H * a.d, a.d, a.gate_format));
     TileSpace w;
     cudaError_t err = start_tiles(a, L, ws, false, w, stream);
     if (err != cudaSuccess) return err;
@@ -1244,15 +1295,16 @@ cudaError_t run_forward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
         auto kernel = linrec_fwd_kernel<T, decltype(g)::value, C, V>;
         cudaLaunchConfig_t c = {};
         cudaLaunchAttribute attr;
-        const cudaError_t set = configure_tiles(kernel, L, filled(a, L),
-                                             kWarps * FwdRows<T, C, V>::kBytes, stream, c, attr);
+        const cudaError_t set =
+            configure_tiles(kernel, L, kFwdCtas<T, decltype(g)::value, C>, filled(a, L),
+                            kWarps * FwdRows<T, C, V>::kBytes, stream, c, attr);
         return set == cudaSuccess ? cudaLaunchKernelEx(&c, kernel, a, w) : set;
     });
 }
 
 int head_mode(int32_t d, int gate_format, int64_t D) {
     if (gate_format != KDA_GATE_HEAD_F32) return kNoHead;
-    const int lanes = lane_channels(D);
+    const int lanes = lane_channels(D, d, gate_format);
     const int width = 32 * lanes;
     if (d >= lanes && (d % width == 0 || width % d == 0)) return kHeadRow;
     return kHeadWide;
@@ -1260,7 +1312,10 @@ int head_mode(int32_t d, int gate_format, int64_t D) {
 // Partial sums a head's gate gradient is left in (1: none are).
 int32_t head_parts(int32_t d, int gate_format, int64_t D) {
     switch (head_mode(d, gate_format, D)) {
-        case kHeadRow: return d > 32 * lane_channels(D) ? d / (32 * lane_channels(D)) : 1;
+        case kHeadRow: {
+            const int32_t width = 32 * lane_channels(D, d, gate_format);
+            return d > width ? d / width : 1;
+        }
         case kHeadWide: return d;
         default: return 1;
     }
@@ -1269,7 +1324,8 @@ int32_t head_parts(int32_t d, int gate_format, int64_t D) {
 }  // namespace
 
 size_t linrec_prefill_bytes(int32_t num_seqs, int64_t total_tokens, int64_t D) {
-    return tile_layout(total_tokens, D, kFwdRows).end + pad((size_t)num_seqs * D * sizeof(float));
+    return tile_layout(total_tokens, D, kFwdRows, lane_channels(D)).end +
+           pad((size_t)num_seqs * D * sizeof(float));
 }
 
 // Workspace of the backward pass: the tiles, the states when the caller has
@@ -1278,7 +1334,7 @@ size_t linrec_backward_bytes(int32_t, int64_t total_tokens, int32_t H, int32_t d
                              int gate_format, bool with_states) {
     const int64_t D = (int64_t)H * d;
     // (the forward scan's tiles need less room than the backward one's)
-    const TileLayout L = tile_layout(total_tokens, D, kBwdRows);
+    const TileLayout L = tile_layout(total_tokens, D, kBwdRows, lane_channels(D));
     size_t b = L.end;
     if (!with_states && total_tokens > 0) b += pad((size_t)L.nt * D * sizeof(float));
     const int32_t parts = head_parts(d, gate_format, D);
@@ -1292,7 +1348,8 @@ cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t st
     // have written S_T, so it reads a copy
     const int64_t D = (int64_t)a.H * a.d;
     LinrecArgs b = a;
-    float* copy = reinterpret_cast<float*>(ws + tile_layout(a.total_tokens, D, kFwdRows).end);
+    float* copy = reinterpret_cast<float*>(
+        ws + tile_layout(a.total_tokens, D, kFwdRows, lane_channels(D)).end);
     const cudaError_t err = cudaMemcpyAsync(copy, a.S0, (size_t)a.num_seqs * D * sizeof(float),
                                             cudaMemcpyDeviceToDevice, stream);
     if (err != cudaSuccess) return err;
@@ -1302,8 +1359,9 @@ cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t st
 
 cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t stream) {
     const int64_t D = (int64_t)a.H * a.d;
-    const TileLayout L = tile_layout(a.total_tokens, D, kBwdRows);
-    size_t at = L.end;
+    const TileLayout L = tile_layout(a.total_tokens, D, kBwdRows,
+                                     lane_channels(D, a.d, a.gate_format));
+    size_t at = tile_layout(a.total_tokens, D, kBwdRows, lane_channels(D)).end;
     const float* states = a.states;
     cudaError_t err;
     const bool rerun = !states && a.total_tokens > 0;
@@ -1327,12 +1385,13 @@ cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t s
         auto kernel = linrec_bwd_kernel<T, decltype(g)::value, decltype(comp)::value, V>;
         cudaLaunchConfig_t c = {};
         cudaLaunchAttribute attr;
-        const cudaError_t set = configure_tiles(kernel, L, filled(a, L),
+        const cudaError_t set = configure_tiles(kernel, L, 2, filled(a, L),
                                              kWarps * BwdRows<T, V>::kBytes, stream, c, attr);
         return set == cudaSuccess ? cudaLaunchKernelEx(&c, kernel, a, w, states, dgate, mode) : set;
     });
     if (err != cudaSuccess || parts == 1 || a.total_tokens == 0) return err;
-    const int64_t blocks = (a.total_tokens * a.H + kWarps - 1) / kWarps;
+    const int64_t each = parts <= kFewParts ? kThreads : kWarps;   // rows a block
+    const int64_t blocks = (a.total_tokens * a.H + each - 1) / each;
     const int64_t most = 16 * (int64_t)sm_count();
     linrec_head_sum_kernel<<<(unsigned)(blocks < most ? blocks : most), kThreads, 0, stream>>>(
         dgate, a.cu_seqlens, a.num_seqs, a.H, parts, a.dgate, w.status);

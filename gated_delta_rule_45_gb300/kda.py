@@ -632,11 +632,12 @@ def _linrec_args(x, a, gate: str, rows: str):
     code = _DTYPE_CODES.get(x.dtype)
     if code is None:
         raise TypeError(f"the storage dtype must be bfloat16 or float32, got {x.dtype}")
-    if x.dim() != 3:
-        raise ValueError(f"x must be [{rows}, H, d], got {tuple(x.shape)}")
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x must be [{rows}, H, d], got {tuple(shape)}")
     gcode, adt, arank = _GATES[gate]
-    _check(f"the gate (layout {gate!r})", a, adt, x.shape[:arank])
-    return x.shape[1], x.shape[2], code, gcode
+    _check("the gate", a, adt, shape[:arank])
+    return shape[1], shape[2], code, gcode
 
 
 def linrec_workspace_size(num_seqs: int, total_tokens: int, H: int, d: int) -> int:
@@ -712,6 +713,14 @@ def linrec_backward_workspace_size(num_seqs: int, total_tokens: int, H: int, d: 
                                                  int(with_states))
 
 
+def _check_cotangents(x, dy, dS_T, states, T, N, H, d):
+    _check("dy", dy, x.dtype, x.shape)
+    if dS_T is not None:
+        _check("dS_T", dS_T, torch.float32, (N, H, d))
+    if states is not None:
+        _check("states", states, torch.float32, (-(-T // LINREC_CHUNK), H, d))
+
+
 def linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, workspace, *, states=None,
                          gate: str = "channel", complement: bool = False, stream=None) -> None:
     """Enqueue linrec_backward into preallocated fp32 gradients.
@@ -724,12 +733,9 @@ def linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, workspace, *, st
     """
     T, N, H, d, code, gcode = _linrec_inputs(x, a, S0, cu_seqlens, gate)
     dx, dgate, dS0 = grads["dx"], grads["dgate"], grads.get("dS0")
-    _check("dy", dy, x.dtype, x.shape)
-    for what, t in (("dS_T", dS_T), ("dS0", dS0)):
-        if t is not None:
-            _check(what, t, torch.float32, (N, H, d))
-    if states is not None:
-        _check("states", states, torch.float32, (-(-T // LINREC_CHUNK), H, d))
+    _check_cotangents(x, dy, dS_T, states, T, N, H, d)
+    if dS0 is not None:
+        _check("dS0", dS0, torch.float32, (N, H, d))
     _check("dx", dx, torch.float32, x.shape)
     _check("dgate", dgate, torch.float32, a.shape)
     raw = _place(stream, x, a, S0, cu_seqlens, dy, dS_T, states, dx, dgate, dS0, workspace)
@@ -745,17 +751,23 @@ def linrec_backward(x, a, S0, cu_seqlens, dy, dS_T=None, *, states=None, gate: s
                     complement: bool = False, stream=None, check_device_status: bool = False):
     """Allocate fp32 gradients with PyTorch and run linrec_backward; returns a dict with
     dx, dgate and dS0.  Rows of tokens past cu_seqlens[-1] are not written."""
-    T, N, H, d, _, _ = _linrec_inputs(x, a, S0, cu_seqlens, gate)
-    dev = x.device
-    nbytes = linrec_backward_workspace_size(N, T, H, d, gate=gate, with_states=states is not None)
+    T, N, H, d, code, gcode = _linrec_inputs(x, a, S0, cu_seqlens, gate)
+    _check_cotangents(x, dy, dS_T, states, T, N, H, d)
+    raw = _place(stream, x, a, S0, cu_seqlens, dy, dS_T, states)
+    lib, dev = load(), x.device
+    nbytes = lib.linrec_backward_workspace_size(N, T, H, d, gcode, int(states is not None))
     if nbytes == 0:
         raise KdaError(ERR_UNSUPPORTED, "linrec_backward")
     grads = {"dx": _empty(stream, x.shape, torch.float32, dev),
              "dgate": _empty(stream, a.shape, torch.float32, dev),
              "dS0": _empty(stream, (N, H, d), torch.float32, dev)}
     ws = _empty(stream, nbytes, torch.uint8, dev)
-    linrec_backward_into(x, a, S0, cu_seqlens, dy, dS_T, grads, ws, states=states, gate=gate,
-                         complement=complement, stream=stream)
+    st = lib.linrec_backward(x.data_ptr(), a.data_ptr(), gcode, _p(S0), cu_seqlens.data_ptr(), N,
+                             T, H, d, code, int(complement), dy.data_ptr(), _p(dS_T), _p(states),
+                             grads["dx"].data_ptr(), grads["dgate"].data_ptr(),
+                             grads["dS0"].data_ptr(), ws.data_ptr(), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "linrec_backward")
     if check_device_status:
         device_status(ws, stream=stream)
     return grads

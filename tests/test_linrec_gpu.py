@@ -128,6 +128,20 @@ def test_widths(H, d, gate):
         _check_backward(c, dev, out[2], gate, True)
 
 
+@pytest.mark.parametrize("H,d", [(2, 1), (64, 1), (6, 5), (2, 640), (2, 128)])
+def test_head_gate_widths(H, d):
+    """Heads of an odd width in rows of an even one, where a lane takes one channel; more
+    partial sums a head than one thread adds up."""
+    c = _case([70, 0, 300, 31, 17], H, d, torch.bfloat16, "head", True, seed=H + d)
+    dev, out = _check_prefill(c, torch.bfloat16, "head", False)
+    got = _check_backward(c, dev, out[2], "head", False)
+    again = _check_backward(c, dev, None, "head", False)
+    end = c["cu_list"][-1]
+    for name in got:
+        rows = slice(None) if name == "dS0" else slice(0, end)
+        assert torch.equal(got[name][rows], again[name][rows])
+
+
 def test_many_sequences():
     """More sequences than a CTA checks by itself, most of them empty or one token."""
     r = np.random.RandomState(0)
