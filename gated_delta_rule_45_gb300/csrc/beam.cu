@@ -16,8 +16,9 @@
 // maximum keys: exactly num_out threads hold keys from there on, so the list is
 // num_out times a thread's share at the most.
 //
-// Bound: HBM (each logit is read once, 19 us for 64 x 8 x 128000 bf16); measured 46 us:
-// 37 for the pieces, half of it the dependent phases of their first parts, 9 to join.
+// Bound: HBM (each logit is read once, 19 us for 64 x 8 x 128000 bf16, 16 of them);
+// measured 37 us: 30 for the pieces, whose warps issue in three cycles of five, and 7 to
+// join.  For the best one alone it is 29 us: the rest is the listing.
 #include "kda_internal.h"
 
 #include <cfloat>
@@ -31,7 +32,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kList = 1024;  // logits the fast pass may list
 constexpr int kJoin = 16;    // candidates a thread of the joining kernel, with 256 threads
 constexpr int kParts = 8;    // most vectors a thread of a piece's first part
-constexpr int kCtas = 4;     // an SM
+constexpr int kCtas = 3;     // an SM
 
 // 16 bytes of logits.
 template <typename T>
@@ -155,8 +156,8 @@ __device__ __forceinline__ uint32_t warp_nth(uint32_t c, int r, int lane) {
 }
 
 // The num-th largest of the threads' best keys (Key{} when fewer threads have one) goes
-// to `limit`; returns whether this thread's best is among the num largest.  A first
-// bound, from every warp's own largest, leaves few keys to rank by counting.
+// to `limit`; returns whether this thread's best is among the num largest, and then its
+// rank.  A first bound, from every warp's own largest, leaves few keys to rank by counting.
 template <int THREADS, typename Key>
 struct Threshold {
     Key best[THREADS];
@@ -164,7 +165,7 @@ struct Threshold {
     uint32_t bound[THREADS / 32];
     int count;
 
-    __device__ bool find(const Key& mine, int num) {
+    __device__ bool find(const Key& mine, int num, int& rank) {
         constexpr int kW = THREADS / 32;
         const int lane = threadIdx.x & 31;
         const uint32_t c = exists(mine) ? coarse(mine) : 0;
@@ -181,7 +182,7 @@ struct Threshold {
         const bool in = exists(mine) && c >= least;
         if (in) best[atomicAdd(&count, 1)] = mine;
         __syncthreads();
-        int rank = 0;
+        rank = 0;
         if (in) {
             const int have = count;
             for (int j = 0; j < have; ++j) rank += above(best[j], mine);
@@ -262,6 +263,17 @@ struct Piece {
         }
         return q;
     }
+    // All threads' vectors j0 .. j0 + n - 1, j0 > 0, on their way into L2 (called by one
+    // thread): whole 16 bytes inside the row.
+    __device__ __forceinline__ void prefetch(int j0, int n) const {
+        const int from = lo + j0 * kThreads * N, to = min(from + n * kThreads * N, hi);
+        if (from >= to) return;
+        const uintptr_t a = reinterpret_cast<uintptr_t>(r + from) & ~(uintptr_t)15;
+        const uintptr_t b = reinterpret_cast<uintptr_t>(r + to) & ~(uintptr_t)15;
+        if (a < b)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a),
+                         "r"((uint32_t)(b - a)));
+    }
     // Vectors j0 .. j0 + U - 1 (those past the piece: -inf).
     template <int U>
     __device__ __forceinline__ void load_some(Logits<T> (&q)[U], int j0) const {
@@ -316,7 +328,8 @@ __device__ __noinline__ void careful_piece(const Piece<T>& w, int num, uint64_t*
         if (lane == 0) part[warp] = m;
         if (tid == 0) count = held;
         if (tid < held) list[tid] = kept[tid];
-        const bool among = pick.find(best, num);
+        int rank;
+        const bool among = pick.find(best, num, rank);
         float top = M;
         for (int j = 0; j < kWarps; ++j) top = fmaxf(top, part[j]);
         float s = 0.f;
@@ -350,9 +363,12 @@ __device__ __noinline__ void careful_piece(const Piece<T>& w, int num, uint64_t*
 
 // One piece of one row.  Its first U vectors a thread give the reference of the
 // exponentials and, ranked, the num_out best so far: the bound for all that follows.
-// The rest then streams by without a barrier, few of its logits reaching the bound.
+// The rest then streams by without a barrier, few of its logits reaching the bound; the
+// next part is on its way into L2 while one is worked on (64 x 8 x 128000 bf16 39.2 us
+// instead of 41.2; two parts ahead 39.7).  Four CTAs an SM leave 64 registers: with five,
+// of 48, values spill (42.2).
 template <typename T, int U>
-__global__ void __launch_bounds__(kThreads, 5)
+__global__ void __launch_bounds__(kThreads, 4)
 beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __restrict__ keys,
                   float2* __restrict__ sums) {
     constexpr int N = Logits<T>::N;
@@ -388,6 +404,7 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
 
     Logits<T> q[U];
     w.load_some(q, 0);
+    if (tid == 0) w.prefetch(U, U);
     // their maximum, and a bound that at least num_out threads reach
     float m = -INFINITY;
 #pragma unroll
@@ -450,6 +467,7 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
         __syncthreads();
         for (int j0 = U; j0 < each; j0 += U) {
             w.load_some(q, j0);
+            if (tid == 0) w.prefetch(j0 + U, U);
             look(j0, limit);
         }
     }
@@ -502,24 +520,28 @@ beam_join_kernel(const BeamSelectArgs p, int pieces, uint32_t per_beam_inv,
     if (tid == 0) count = 0;
     if (tid < p.K) score[tid] = (double)tame(p.scores[(int64_t)b * p.K + tid]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per_beam = pieces * num, all = p.K * per_beam;
+    const uint64_t* mine = keys + (int64_t)b * all;
+    // neighbouring candidates, of one beam and good or bad together, go to different warps:
+    // the first bound is the worst warp's, and would be loose otherwise
+    const int first = lane * (THREADS / 32) + warp;
+    const uint64_t first_key = first < all ? mine[first] : 0;   // under way with the sums
     // a row's maximum, then its pieces' sums relative to it; a warp a row
     for (int k = warp; k < p.K; k += THREADS / 32) {
         const float2* q = sums + ((int64_t)b * p.K + k) * pieces;
-        float M = -INFINITY;
-        for (int j = lane; j < pieces; j += 32) M = fmaxf(M, q[j].x);
+        const float2 own = lane < pieces ? q[lane] : make_float2(-INFINITY, 0.f);
+        float M = own.x;
+        for (int j = lane + 32; j < pieces; j += 32) M = fmaxf(M, q[j].x);
         M = warp_max(M);
-        float s = 0.f;
-        for (int j = lane; j < pieces; j += 32)
+        float s = own.y > 0.f ? own.y * expf(own.x - M) : 0.f;
+        for (int j = lane + 32; j < pieces; j += 32)
             if (q[j].y > 0.f) s = fmaf(q[j].y, expf(q[j].x - M), s);
         s = warp_sum(s);
         if (lane == 0) lse[k] = s > 0.f ? (double)M + log_of_sum(s) : 0.0;
     }
     __syncthreads();
 
-    const int per_beam = pieces * num, all = p.K * per_beam;
-    const uint64_t* mine = keys + (int64_t)b * all;
-    auto value = [&](int i) {
-        const uint64_t key = mine[i];
+    auto value = [&](int i, uint64_t key) {
         ValueKey q{0, 0};
         if (key) {
             const int k = per_beam == 1 ? i : (int)__umulhi((uint32_t)i, per_beam_inv);
@@ -532,39 +554,44 @@ beam_join_kernel(const BeamSelectArgs p, int pieces, uint32_t per_beam_inv,
         }
         return q;
     };
-    // neighbouring candidates, of one beam and good or bad together, go to different warps:
-    // the first bound is the worst warp's, and would be loose otherwise
-    const int first = lane * (THREADS / 32) + warp;
-    ValueKey best{0, 0};
-    for (int i = first; i < all; i += THREADS) {
-        const ValueKey q = value(i);
-        if (above(q, best)) best = q;
-    }
-    if (pick.find(best, num)) {
-        const ValueKey from = pick.limit;
-        for (int i = first; i < all; i += THREADS) {
-            const ValueKey q = value(i);
-            if (exists(q) && !above(from, q)) candidates[atomicAdd(&count, 1)] = q;
-        }
-    }
-    __syncthreads();
-    rank_list(candidates, count, num, [&](int rank, const ValueKey& key) {
+    auto put = [&](int rank, const ValueKey& key) {
         const uint32_t at = 0xffffffffu - (uint32_t)key.index;
         const int64_t o = (int64_t)b * num + rank;
         p.out_scores[o] = (float)unordered(key.value);
         p.out_parents[o] = b * p.K + (int)(at / (uint32_t)p.V);
         p.out_tokens[o] = (int)(at % (uint32_t)p.V);
-    });
+    };
+    ValueKey best = value(first, first_key);
+    for (int i = first + THREADS; i < all; i += THREADS) {
+        const ValueKey q = value(i, mine[i]);
+        if (above(q, best)) best = q;
+    }
+    int rank;
+    const bool among = pick.find(best, num, rank);
+    if (all <= THREADS) {   // a candidate a thread: the ranks are final
+        if (among) put(rank, best);
+        return;
+    }
+    if (among) {
+        const ValueKey from = pick.limit;
+        for (int i = first; i < all; i += THREADS) {
+            const ValueKey q = value(i, i == first ? first_key : mine[i]);
+            if (exists(q) && !above(from, q)) candidates[atomicAdd(&count, 1)] = q;
+        }
+    }
+    __syncthreads();
+    rank_list(candidates, count, num, put);
 }
 
 struct Pieces {
     int pieces, each;   // of a row; 16-byte vectors a thread
 };
 // Pieces for kCtas CTAs an SM, none shorter than one vector a thread: more pieces leave
-// more candidates to join (4 x 8 x 128000 fp32 logits: 28 us with 3 CTAs an SM, 39 with
-// 8, 82 with 16; 64 x 8 x 128000 bf16: 50, 52, 60).  Nor so long that the logits above
-// the bound of a piece's first part, num_out a part on average, outgrow its list
-// (64 x 8 x 250000 in one piece a row: 410 us, in two 126).
+// more candidates to join, fewer leave SMs idle (16 x 8 x 128000 bf16 logits: 23.1 us with 2
+// CTAs an SM, 22.2 with 3, 27.9 with 4; 32 x 8 x 32000: 15.7, 15.7, 22.0; 64 x 8 x 128000:
+// 39, 39, 43).  Nor so long that the logits above the bound of a piece's first part,
+// num_out a part on average, outgrow its list (64 x 8 x 250000 in one piece a row: 410 us,
+// in two 110).
 Pieces split_row(int64_t rows, int32_t K, int32_t V, int32_t num_out, kda_dtype dtype) {
     const int N = dtype == KDA_BF16 ? 8 : 4;
     const int64_t blocks = ((int64_t)(V + N - 1) / N + kThreads - 1) / kThreads;   // one vector a thread
