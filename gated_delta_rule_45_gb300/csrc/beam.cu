@@ -64,9 +64,14 @@ struct Logits<__nv_bfloat16> {
 };
 
 // Exponentials are taken as 2^(x log2 e - c) with c = M log2 e rounded once, M the
-// piece's maximum: one multiply-add and one special-function instruction a logit.  The
-// piece's sum is then made relative to e^M, with what the rounding of c left out.
-constexpr float kLog2e = 1.4426950408889634f, kLog2eRest = 1.92596299e-8f;
+// maximum of the piece's first part: one multiply-add and one special-function instruction
+// a logit.  The term of x = M is then 2^r and not 1, r = M log2 e - c what the rounding
+// left out (6e-8 of c: at M = 1000, 6e-5), so the sum is divided by 2^r.  (log2 e is
+// itself rounded, by 2e-8 of x log2 e; in terms relative to e^M that is 2e-8 of x - M,
+// which does not show.)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMostRest = 0.5f;   // beyond (logits of 1e7 and more): the careful path
 __device__ __forceinline__ float exp2_ftz(float x) {   // below the normal numbers: 0
     float e;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
@@ -296,7 +301,7 @@ struct Piece {
 };
 
 // Pieces whose fast pass gave up: a NaN or +inf, nothing above -inf, values far above the
-// first ones, or so many equal logits that the list ran over.  Values are replaced as
+// first ones, logits of 1e7 and more, or so many equal logits that the list ran over.  Values are replaced as
 // documented and the threads' maxima carry their tokens: of a step of U vectors a thread,
 // at most num_out x U N keys are listed, after the num_out best of the steps before.
 template <typename T, int U>
@@ -481,13 +486,15 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
     s = 0.f;
 #pragma unroll
     for (int j = 0; j < kWarps; ++j) s += part[j].y;
-    if (!(s > 0.f && s < INFINITY) || have > kList) {   // the same in all threads
+    const float rest = fmaf(M, kLog2e, -c);
+    // the same in all threads; a NaN in either fails its comparison
+    if (!(s > 0.f && s < INFINITY) || !(fabsf(rest) <= kMostRest) || have > kList) {
         __syncthreads();
         careful_piece<T, U>(w, num, list, out, sums + blockIdx.x);
         return;
     }
-    if (tid == 0)
-        sums[blockIdx.x] = make_float2(M, s * exp2_ftz(fmaf(M, kLog2e, -c) + M * kLog2eRest));
+    // s 2^-rest, the factor's distance from 1 by itself: a factor near 1 would be rounded
+    if (tid == 0) sums[blockIdx.x] = make_float2(M, fmaf(s, expm1f(-rest * kLn2), s));
     rank_list(list, have, num, [&](int rank, uint64_t key) { out[rank] = key; });
     for (int i = have + tid; i < num; i += kThreads) out[i] = 0;
 }
