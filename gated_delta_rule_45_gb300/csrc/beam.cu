@@ -68,9 +68,14 @@ struct Logits<__nv_bfloat16> {
 // a logit.  The term of x = M is then 2^r and not 1, r = M log2 e - c what the rounding
 // left out (6e-8 of c: at M = 1000, 6e-5), so the sum is divided by 2^r.  (log2 e is
 // itself rounded, by 2e-8 of x log2 e; in terms relative to e^M that is 2e-8 of x - M,
-// which does not show.)
+// which does not show.)  A later logit far above M has a large argument, whose rounding
+// shows (6.6e-7 of the term up to 22 above, 2.6e-6 from 44 on, and at 88 sums overflow): a
+// piece whose sum says that some lie 22 above is summed again relative to the largest.
+// (Taking a new reference on the way would save that, but cost every piece 3 %: 41.5 us
+// for 40.3 at 64 x 8 x 128000 bf16.)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMostSum = 0x1p32f;   // the terms of a piece at M or below add to 2^20 at most
 constexpr float kMostRest = 0.5f;   // beyond (logits of 1e7 and more): the careful path
 __device__ __forceinline__ float exp2_ftz(float x) {   // below the normal numbers: 0
     float e;
@@ -82,15 +87,30 @@ __device__ __forceinline__ uint64_t pack2(float a, float b) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
     return r;
 }
-// acc + (2^(a log2 e - c), 2^(b log2 e - c)), both halves at once
-__device__ __forceinline__ uint64_t add_exp2(uint64_t acc, float a, float b, uint64_t log2e2,
-                                             uint64_t c2) {
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// (2^(a log2 e - c), 2^(b log2 e - c)), both halves at once
+__device__ __forceinline__ uint64_t both_exp2(float a, float b, uint64_t log2e2, uint64_t c2) {
     uint64_t t;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(t) : "l"(pack2(a, b)), "l"(log2e2), "l"(c2));
     float x, y;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(t));
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(acc), "l"(pack2(exp2_ftz(x), exp2_ftz(y))));
-    return t;
+    return pack2(exp2_ftz(x), exp2_ftz(y));
+}
+
+// The sum of n values (a power of two) in pairs: of equal ones without rounding.  Rows with
+// one logit many times over have equal terms, whose roundings do not cancel.
+template <int n>
+__device__ __forceinline__ float sum_pairs(float (&v)[n]) {
+#pragma unroll
+    for (int h = n / 2; h > 0; h /= 2) {
+#pragma unroll
+        for (int i = 0; i < h; ++i) v[i] += v[i + h];
+    }
+    return v[0];
 }
 
 // 16 bytes from bit `shift` (16 .. 112) of a and the vector after it.
@@ -300,8 +320,61 @@ struct Piece {
     }
 };
 
-// Pieces whose fast pass gave up: a NaN or +inf, nothing above -inf, values far above the
-// first ones, logits of 1e7 and more, or so many equal logits that the list ran over.  Values are replaced as
+// The sum of a part's exponentials, in a thread's two halves: few additions one after the
+// other (a vector's are in pairs).
+template <typename T, int U>
+__device__ __forceinline__ uint64_t part_sum(const Logits<T> (&q)[U], uint64_t log2e2,
+                                             uint64_t c2) {
+    constexpr int N = Logits<T>::N;
+    uint64_t sum = 0;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+        uint64_t pair[N / 4];
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            pair[i / 4] = add2(both_exp2(q[j].get(i), q[j].get(i + 1), log2e2, c2),
+                               both_exp2(q[j].get(i + 2), q[j].get(i + 3), log2e2, c2));
+        sum = add2(sum, N == 4 ? pair[0] : add2(pair[0], pair[N / 4 - 1]));
+    }
+    return sum;
+}
+// The sum of all threads' halves; a barrier.
+__device__ __forceinline__ float piece_sum(uint64_t acc, float (&total)[kWarps]) {
+    float s, s1;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(s), "=f"(s1) : "l"(acc));
+    s = warp_sum(s + s1);
+    if ((threadIdx.x & 31) == 0) total[threadIdx.x >> 5] = s;
+    __syncthreads();
+    float each[kWarps];
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) each[j] = total[j];
+    return sum_pairs(each);
+}
+
+// A piece whose logits lie far above those of its first part: the sum once more, relative to
+// the largest of the list.  Returns that and the sum.
+template <typename T, int U>
+__device__ __noinline__ float2 sum_again(const Piece<T>& w, const uint64_t* list, int have) {
+    __shared__ uint32_t largest_of[kWarps];
+    __shared__ float total[kWarps];
+    uint32_t m = 0;
+    for (int i = threadIdx.x; i < have; i += kThreads) m = max(m, (uint32_t)(list[i] >> 32));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) largest_of[threadIdx.x >> 5] = m;
+    __syncthreads();
+    for (int j = 0; j < kWarps; ++j) m = max(m, largest_of[j]);
+    const float M = unordered(m), c = M * kLog2e;
+    uint64_t acc = 0;
+    for (int j0 = 0; j0 < w.vectors; j0 += U) {
+        Logits<T> q[U];
+        w.load_some(q, j0);
+        acc = add2(acc, part_sum<T, U>(q, pack2(kLog2e, kLog2e), pack2(-c, -c)));
+    }
+    return make_float2(M, piece_sum(acc, total));
+}
+
+// Pieces whose fast pass gave up: a NaN or +inf, nothing above -inf in the first part, logits
+// of 1e7 and more, or so many equal logits that the list ran over.  Values are replaced as
 // documented and the threads' maxima carry their tokens: of a step of U vectors a thread,
 // at most num_out x U N keys are listed, after the num_out best of the steps before.
 template <typename T, int U>
@@ -342,13 +415,16 @@ __device__ __noinline__ void careful_piece(const Piece<T>& w, int num, uint64_t*
         for (int j = j0; j < j1; ++j) {
             const Logits<T> q = w.load(j);
             const int v = w.token(j);
+            float e[N];
             for (int i = 0; i < N; ++i) {
-                if (v + i >= w.hi) break;
+                e[i] = 0.f;
+                if (v + i >= w.hi) continue;
                 const float x = tame(q.get(i));
-                if (top != -INFINITY) s += exp2_ftz((x - top) * kLog2e);
+                if (top != -INFINITY) e[i] = exp2_ftz((x - top) * kLog2e);
                 if (among && logit_key(x, v + i) >= from)
                     list[atomicAdd(&count, 1)] = logit_key(x, v + i);
             }
+            s += sum_pairs(e);
         }
         s = warp_sum(s);
         __syncthreads();   // the parts are read, the list is complete
@@ -358,7 +434,9 @@ __device__ __noinline__ void careful_piece(const Piece<T>& w, int num, uint64_t*
         held = min(have, num);
         __syncthreads();
         if (M != -INFINITY) S *= exp2_ftz((M - top) * kLog2e);
-        for (int j = 0; j < kWarps; ++j) S += part[j];
+        float e[kWarps];
+        for (int j = 0; j < kWarps; ++j) e[j] = part[j];
+        S += sum_pairs(e);
         M = top;
         __syncthreads();
     }
@@ -379,7 +457,8 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
     constexpr int N = Logits<T>::N;
     extern __shared__ __align__(16) uint64_t list[];   // num_out (U N + 1), at least kList
     __shared__ uint32_t bound[kWarps];
-    __shared__ float2 part[kWarps];
+    __shared__ float part[kWarps];
+    __shared__ float total[kWarps];
     __shared__ float limit;
     __shared__ int count;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -418,7 +497,7 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
     const uint32_t nth = warp < warps ? warp_nth(ordered(m), (num + warps - 1) / warps, lane) : 0;
     m = warp_max(m);
     if (lane == 0) {
-        part[warp].x = m;
+        part[warp] = m;
         bound[warp] = nth;
     }
     if (tid == 0) {
@@ -427,27 +506,23 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
     }
     __syncthreads();
     uint32_t least = warps > 0 ? bound[0] : 0;
-    float M = part[0].x;
+    float M = part[0];
 #pragma unroll
     for (int j = 1; j < kWarps; ++j) {
         if (j < warps) least = min(least, bound[j]);
-        M = fmaxf(M, part[j].x);
+        M = fmaxf(M, part[j]);
     }
     const float c = M * kLog2e;
     const uint64_t log2e2 = pack2(kLog2e, kLog2e), c2 = pack2(-c, -c);
-    uint64_t acc[2] = {0, 0};
+    uint64_t acc = 0;
     // the sum of exponentials; the vectors with a logit at or above the bound are read
     // again, in a loop that is short code (unrolled over the registers a third of the
     // time went to instruction fetches), and those logits listed
     auto look = [&](int j0, float from) {
         uint32_t hits = 0;
+        acc = add2(acc, part_sum<T, U>(q, log2e2, c2));
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-#pragma unroll
-            for (int i = 0; i < N; i += 2)
-                acc[i / 2 & 1] = add_exp2(acc[i / 2 & 1], q[j].get(i), q[j].get(i + 1), log2e2, c2);
-            hits |= (largest(q[j]) >= from ? 1u : 0u) << j;
-        }
+        for (int j = 0; j < U; ++j) hits |= (largest(q[j]) >= from ? 1u : 0u) << j;
         for (; hits; hits &= hits - 1) {
             const int j = j0 + __ffs(hits) - 1, v = w.token(j);
             if (j >= w.vectors) break;
@@ -476,25 +551,23 @@ beam_piece_kernel(const BeamSelectArgs p, int pieces, int each, uint64_t* __rest
             look(j0, limit);
         }
     }
-    float s, s1, s2, s3;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(s), "=f"(s1) : "l"(acc[0]));
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(s2), "=f"(s3) : "l"(acc[1]));
-    s = warp_sum((s + s1) + (s2 + s3));
-    if (lane == 0) part[warp].y = s;
-    __syncthreads();
+    float s = piece_sum(acc, total);   // the list is complete, too
     const int have = count;
-    s = 0.f;
-#pragma unroll
-    for (int j = 0; j < kWarps; ++j) s += part[j].y;
-    const float rest = fmaf(M, kLog2e, -c);
+    if (s >= kMostSum && have <= kList) {
+        const float2 again = sum_again<T, U>(w, list, have);
+        M = again.x;
+        s = again.y;
+    }
+    const float rest = fmaf(M, kLog2e, -(M * kLog2e));
     // the same in all threads; a NaN in either fails its comparison
-    if (!(s > 0.f && s < INFINITY) || !(fabsf(rest) <= kMostRest) || have > kList) {
+    if (!(s > 0.f && s < kMostSum) || !(fabsf(rest) <= kMostRest) || have > kList) {
         __syncthreads();
         careful_piece<T, U>(w, num, list, out, sums + blockIdx.x);
         return;
     }
-    // s 2^-rest, the factor's distance from 1 by itself: a factor near 1 would be rounded
-    if (tid == 0) sums[blockIdx.x] = make_float2(M, fmaf(s, expm1f(-rest * kLn2), s));
+    // s 2^-rest, the factor's distance from 1 by itself: a factor near 1 would be rounded (by
+    // the last thread: the first ones rank the list)
+    if (tid == kThreads - 1) sums[blockIdx.x] = make_float2(M, fmaf(s, expm1f(-rest * kLn2), s));
     rank_list(list, have, num, [&](int rank, uint64_t key) { out[rank] = key; });
     for (int i = have + tid; i < num; i += kThreads) out[i] = 0;
 }

@@ -31,9 +31,11 @@ size_t beam_select_workspace_size(int32_t B, int32_t K, int32_t V, int32_t num_o
  *
  *     scores[b][k] + logits[b K + k][v] - log sum_w exp(logits[b K + k][w]),
  *
- * formed in 64 bits from the fp32 or bf16 logits and a logarithm of the sum
- * good to about 1e-7 (equal rows get equal ones); a finished beam has one candidate, token
- * `eos` at scores[b][k], and its logits are not read.  Candidates are ordered
+ * formed in 64 bits from the fp32 or bf16 logits and a logarithm of the sum of
+ * 32-bit exponentials relative to one near the row's largest: off by 1e-7 as a
+ * rule and by less than 3e-6 at worst, wherever the logits lie (equal rows get
+ * equal ones).  A finished beam has one candidate, token `eos` at
+ * scores[b][k], and its logits are not read.  Candidates are ordered
  * by value, larger first, equal values by k V + v, smaller first.
  *
  *   logits       [B K][ld] (dtype), the first V entries of each row used

@@ -24,8 +24,15 @@ F32_HALF = 2.0 ** -24
 REF = 4.0
 
 
-def _lse_err(x):
-    """Largest error of the log-sum-exp of each row [rows, V], as above: [rows, 1]."""
+def _lse_err(x, rising=False):
+    """Largest error of the log-sum-exp of each row [rows, V], as above: [rows, 1].  Where
+    later parts lie far above the first (`rising`), arguments are as large as 32, 22 below
+    or above the reference, or the sums are scaled to new references, each time by one more
+    exponential.  Those rows have equal terms, whose additions round alike in all threads:
+    the sums are in pairs (exact then), but for 8 vectors of a part, of which the 3rd, 5th
+    .. 8th addition round, by 2^-24 of 3/8, 5/8 .. 8/8 of the result (3.6), up to 8 parts
+    (as much) and two last factors: 10 x 2^-24 in all, 4 more."""
+    ref = 22.0 if rising else REF
     big = np.finfo(np.float32).max
     x = np.minimum(np.where(np.isnan(x), -np.inf, x), big)
     top = x.max(-1, keepdims=True)
@@ -34,8 +41,12 @@ def _lse_err(x):
     share = np.exp(-below)
     share /= share.sum(-1, keepdims=True)
     near = np.minimum(below, 200.0)
-    arg = (np.maximum(near, REF) / np.log(2)).astype(np.float32)
-    term = 2.0 ** -22 + np.log(2) * np.spacing(arg).astype(np.float64) / 2 + 1.34e-8 * near
+    far = np.maximum(near, ref)
+    arg = (far / np.log(2)).astype(np.float32)
+    term = 2.0 ** -22 + np.log(2) * np.spacing(arg).astype(np.float64) / 2 + 1.34e-8 * far
+    if rising:
+        term += (np.floor(near / 4) + 1) * 2.0 ** -22
+        term += 4 * F32_HALF
     return (share * term).sum(-1, keepdims=True) + 6 * F32_HALF
 
 
@@ -43,9 +54,9 @@ def _np(t):
     return t.detach().double().cpu().numpy()
 
 
-def _check(logits, scores, n):
-    err = _lse_err(_np(logits)).reshape(scores.shape).max(-1, keepdims=True)
-    assert err.max() < 1e-6
+def _check(logits, scores, n, rising=False):
+    err = _lse_err(_np(logits), rising).reshape(scores.shape).max(-1, keepdims=True)
+    assert err.max() < (3e-6 if rising else 1e-6)   # as the header states
     vals, par, tok = ref.select(_np(logits), _np(scores), n)
     s, p, t = kda.beam_select(logits.cuda(), scores.cuda(), n)
     torch.cuda.synchronize()
@@ -96,3 +107,42 @@ def test_order_of_beams_that_differ_by_a_constant(shift):
         sc = torch.tensor([[-0.25 - 2.0 ** -20, -0.25]])
         _check(torch.cat([z, z + shift]), sc, 32)
         _check(torch.cat([z + shift, z]), sc, 32)
+
+
+# Tokens far above the rest of their row, behind the part of it that is seen first.  The sums
+# stay relative to what is near the largest logit.
+FAR = [10.0, 20.0, 21.5, 27.0, 40.0, 80.0, 88.5, 120.0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("above", FAR)
+def test_tokens_far_above_the_first_ones(above, dtype):
+    """A row's fill of -100 and two allowed tokens, each in another piece of the row."""
+    rows, V = 256, 128000
+    z = torch.full((rows, V), -100.0)
+    z[:, 40000], z[:, 100000] = -100.0 + above, -100.0 + above
+    z[7, 100000] += 0.25
+    z[9, 3] = -100.0 + above           # one more, seen first
+    z[11, 40000:40400] = -100.0 + above
+    z[13, 5000:125000:97] += above / 2     # some in every part, on the way up
+    _check(z.to(dtype), torch.zeros(rows, 1), 4, rising=True)
+    if above < 100:
+        # logits that differ, so that few of them are listed; two sums of e^88.5 overflow
+        g = torch.Generator().manual_seed(int(above))
+        z = torch.minimum(z, z - torch.rand(rows, V, generator=g).round(decimals=2))
+        z[:, 40000], z[:, 100000] = -100.0 + above, -100.0 + above
+        _check(z.to(dtype), torch.zeros(rows, 1), 4, rising=True)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rising_rows(dtype):
+    """Logits that rise along the row, so that each part lies above the ones before, and a
+    few steps of it, from a fill as low as the type has."""
+    V = 100003
+    ramp = torch.linspace(-60, 60, V)
+    steps = torch.full((V,), torch.finfo(torch.float32).min)
+    steps[30000:] = -1e4
+    steps[70000:] = 5.0
+    steps[99000:] = 25.5
+    _check(torch.stack([ramp, -ramp, 3 * ramp, steps, steps.flip(0)]).to(dtype),
+           torch.zeros(5, 1), 16, rising=True)
