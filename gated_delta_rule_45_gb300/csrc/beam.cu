@@ -695,20 +695,38 @@ int join_share(const Pieces& s, int K, int num_out, int threads) {
 
 size_t pad(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// Allows a kernel `most` bytes of dynamic shared memory, its largest use by any call.  The
+// limit is the kernel's, for all host threads: with each call's own size, one call could
+// lower it between another's setting and its launch.
+template <typename K>
+cudaError_t allow_shared(K kernel, size_t most) {
+    if (most <= 16 * 1024) return cudaSuccess;   // with the static part below the default limit
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
+// Bytes of a piece's list: that of a careful step, at least the fast pass's.
+constexpr size_t list_bytes(int num_out, int values) {
+    const size_t most = (size_t)num_out * (values + 1);
+    return (most > kList ? most : kList) * sizeof(uint64_t);
+}
+// Bytes of the joining kernel's candidates at most.  kJoin a thread with 256 threads.  With
+// 1024 more than that come from pieces kept short (see split_row): of 2^20 fp32 logits, 32
+// pieces of 32 vectors a thread, 32 beams, 64 of them: 64 a thread.
+template <int THREADS>
+constexpr size_t kMostJoin = (THREADS == kThreads ? kJoin : 64) * BEAM_MAX_SELECT *
+                             sizeof(ValueKey);
+
 template <typename T, int U>
 cudaError_t launch_pieces(const BeamSelectArgs& a, const Pieces& s, uint64_t* keys, float2* sums,
                           cudaStream_t stream) {
     if constexpr (U > 1) {
         if (s.each <= U / 2) return launch_pieces<T, U / 2>(a, s, keys, sums, stream);
     }
-    const size_t most = (size_t)a.num_out * (U * Logits<T>::N + 1);   // of a careful step
-    const size_t smem = (most > kList ? most : kList) * sizeof(uint64_t);
-    if (smem > 16 * 1024) {
-        const cudaError_t err =
-            cudaFuncSetAttribute(beam_piece_kernel<T, U>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (err != cudaSuccess) return err;
-    }
+    constexpr int kValues = U * Logits<T>::N;
+    const cudaError_t err =
+        allow_shared(beam_piece_kernel<T, U>, list_bytes(BEAM_MAX_SELECT, kValues));
+    if (err != cudaSuccess) return err;
+    const size_t smem = list_bytes(a.num_out, kValues);
     const unsigned grid = (unsigned)((int64_t)a.B * a.K * s.pieces);
     beam_piece_kernel<T, U><<<grid, kThreads, smem, stream>>>(a, s.pieces, s.each, keys, sums);
     return cudaGetLastError();
@@ -719,12 +737,9 @@ cudaError_t launch_join(const BeamSelectArgs& a, const Pieces& s, const uint64_t
                         const float2* sums, cudaStream_t stream) {
     const size_t smem =
         (size_t)join_share(s, a.K, a.num_out, THREADS) * a.num_out * sizeof(ValueKey);
-    if (smem > 16 * 1024) {   // with the static part perhaps above the default limit
-        const cudaError_t err =
-            cudaFuncSetAttribute(beam_join_kernel<THREADS>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (err != cudaSuccess) return err;
-    }
+    if (smem > kMostJoin<THREADS>) return cudaErrorInvalidValue;
+    const cudaError_t err = allow_shared(beam_join_kernel<THREADS>, kMostJoin<THREADS>);
+    if (err != cudaSuccess) return err;
     // its launch overlaps the pieces' kernel; it waits for their results itself
     cudaLaunchAttribute early;
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
