@@ -19,7 +19,10 @@
  *
  * The state, the products of gates and every sum are fp32; y is rounded once
  * to dtype.  Gates are meant to lie in [0, 1] (log a <= 0); any finite gates
- * whose products over 128 tokens stay finite give the recurrence's result.
+ * whose products over LINREC_MAX_TILE tokens stay finite give the recurrence's
+ * result (beyond that, only a state of zero does: it stays zero).  Of a state
+ * that the gates of up to LINREC_MAX_TILE tokens multiply by less than 2^-126,
+ * what is left may count as 0.
  * Inputs and states are meant to be finite.  A sequence whose values are not
  * never reaches another sequence's outputs.  Results do not depend on timing:
  * the same call on the same inputs gives the same bits.
@@ -40,6 +43,9 @@ typedef enum {
 
 /* Tokens between two stored states of linrec_prefill (`states`). */
 #define LINREC_CHUNK 128
+
+/* Tokens whose gates' product is formed by itself, at most. */
+#define LINREC_MAX_TILE 256
 
 /*
  * Bytes of device workspace linrec_prefill needs: about total_tokens x H x d / 32
