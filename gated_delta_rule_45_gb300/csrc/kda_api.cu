@@ -661,8 +661,8 @@ kda_status linrec_decode_step(const void* x, const void* gate, kda_gate_format g
     if (num_rows < 0) return KDA_ERR_INVALID_ARG;
     const kda_status st = linrec_check(B, num_rows, H, d, dtype, gate_format, input);
     if (st != KDA_OK) return st;
+    if (B == 0) return KDA_OK;   // (`parents` of no sequences may be null)
     if (!parents && num_rows != B) return KDA_ERR_INVALID_ARG;
-    if (B == 0) return KDA_OK;
     if (!x || !gate || (num_rows > 0 && !S) || !y || !S_out) return KDA_ERR_INVALID_ARG;
     const void* ptrs[] = {x, gate, S, parents, y, S_out};
     for (const void* p : ptrs)
