@@ -265,6 +265,17 @@ kda_status kda_check_wait_timeout(void* workspace, size_t workspace_bytes, uint6
                : KDA_ERR_CUDA;
 }
 
+kda_status kda_check_scan_timeout(void* workspace, size_t workspace_bytes, uint64_t timeout_ns,
+                                  kda_stream_t stream) {
+    if (!workspace || !aligned16(workspace) || workspace_bytes < KDA_SCAN_CHECK_BYTES)
+        return KDA_ERR_INVALID_ARG;
+    if (timeout_ns < 1000 || timeout_ns > 1000000000ull) return KDA_ERR_INVALID_ARG;
+    return kda::launch_linrec_wait_check(static_cast<char*>(workspace), timeout_ns,
+                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? KDA_OK
+               : KDA_ERR_CUDA;
+}
+
 // Validation and launch behind kda_decode_step / kda_decode_step_gates.
 static kda_status decode_impl(const void* q, const void* k, const void* v, const void* alpha,
                               kda_gate_format gate, const float* beta, float* S, int32_t B,

@@ -253,6 +253,7 @@ size_t linrec_backward_bytes(int32_t num_seqs, int64_t total_tokens, int32_t H, 
                              int gate_format, bool with_states);
 cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t stream);
 cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t stream);
+cudaError_t launch_linrec_wait_check(char* ws, uint64_t timeout_ns, cudaStream_t stream);
 cudaError_t launch_linrec_step(const LinrecStepArgs& a, cudaStream_t stream);
 // Beam search (beam.cu).
 size_t beam_select_bytes(int32_t B, int32_t K, int32_t V, int32_t num_out);

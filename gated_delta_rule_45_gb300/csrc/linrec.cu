@@ -67,6 +67,7 @@ struct TileSpace {
     uint64_t* record;
     int32_t nt, ct;      // tiles along tokens and channels
     int64_t Dp;
+    uint64_t wait_ns;    // limit of a wait for another tile
 };
 constexpr size_t kRecords = 256;
 
@@ -516,7 +517,7 @@ __device__ __forceinline__ void publish(const TileSpace& w, int i, int64_t ch,
 __device__ __noinline__ bool expired(const TileSpace& w, uint64_t& t0) {
     const uint64_t t = now_ns();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitNs) atomicExch(w.status, (int32_t)KDA_ERR_DEVICE_TIMEOUT);
+    if (t - t0 > w.wait_ns) atomicExch(w.status, (int32_t)KDA_ERR_DEVICE_TIMEOUT);
     return *reinterpret_cast<volatile int32_t*>(w.status) == KDA_ERR_DEVICE_TIMEOUT;
 }
 
@@ -1118,6 +1119,20 @@ __global__ void linrec_check_kernel(const int32_t* cu, int32_t N, int64_t T, int
         *status = KDA_ERR_DEVICE_INPUT;
 }
 
+// A batch of one sequence of kCheckTiles tiles and one channel, in a workspace whose ticket
+// stands behind the first tile: nobody takes that, so the others' waits for its record run
+// out.  Behind the layout's end: x, gate, y [T], S_T, cu_seqlens.
+constexpr int kCheckTiles = 3, kCheckTokens = kCheckTiles * kWarps * kFwdRows;
+__global__ void __launch_bounds__(kThreads)
+linrec_check_case_kernel(char* ws, size_t end) {
+    for (size_t i = threadIdx.x; i < end / 4; i += kThreads)
+        reinterpret_cast<uint32_t*>(ws)[i] = i == 1 ? 0u : ~0u;
+    float* x = reinterpret_cast<float*>(ws + end);
+    for (int i = threadIdx.x; i < 3 * kCheckTokens + 4; i += kThreads) x[i] = 0.5f;
+    int32_t* cu = reinterpret_cast<int32_t*>(x + 3 * kCheckTokens + 4);
+    if (threadIdx.x < 2) cu[threadIdx.x] = threadIdx.x * kCheckTokens;
+}
+
 // One token a row: W neighbouring channels a thread, four where the head width allows
 // (16-byte accesses of the state and the fp32 gate), else one.  A streaming pass, bound by
 // HBM and, at a few megabytes, by its launch.
@@ -1224,16 +1239,21 @@ TileLayout tile_layout(int64_t T, int64_t D, int rows, int lanes) {
 // Whether the tiles need a workspace filled beforehand.
 bool filled(const LinrecArgs& a, const TileLayout& L) { return L.nt > 1 || a.num_seqs > kSelfCheck; }
 
-// Fills the workspace (keeping the status word of an earlier pass) and checks the
-// offsets of large batches.
-cudaError_t start_tiles(const LinrecArgs& a, const TileLayout& L, char* ws, bool keep_status,
-                        TileSpace& w, cudaStream_t stream) {
+void set_space(TileSpace& w, const TileLayout& L, char* ws) {
     w.status = reinterpret_cast<int32_t*>(ws);
     w.ticket = reinterpret_cast<uint32_t*>(ws + 4);
     w.record = reinterpret_cast<uint64_t*>(ws + kRecords);
     w.nt = (int32_t)L.nt;
     w.ct = (int32_t)L.ct;
     w.Dp = L.Dp;
+    w.wait_ns = kWaitNs;
+}
+
+// Fills the workspace (keeping the status word of an earlier pass) and checks the
+// offsets of large batches.
+cudaError_t start_tiles(const LinrecArgs& a, const TileLayout& L, char* ws, bool keep_status,
+                        TileSpace& w, cudaStream_t stream) {
+    set_space(w, L, ws);
     if (filled(a, L)) {
         const size_t blocks = (L.end / 16 + kThreads - 1) / kThreads;
         const size_t most = 4 * (size_t)(sm_count() > 0 ? sm_count() : 1);
@@ -1361,6 +1381,32 @@ cudaError_t launch_linrec_prefill(const LinrecArgs& a, char* ws, cudaStream_t st
     if (err != cudaSuccess) return err;
     b.S0 = copy;
     return run_forward(b, ws, stream);
+}
+
+cudaError_t launch_linrec_wait_check(char* ws, uint64_t timeout_ns, cudaStream_t stream) {
+    const TileLayout L = tile_layout(kCheckTokens, 1, kFwdRows, 1);
+    static_assert(kRecords + kCheckTiles * 32 * sizeof(uint64_t) + 256 +
+                  (3 * kCheckTokens + 8) * sizeof(float) <= KDA_SCAN_CHECK_BYTES, "its workspace");
+    linrec_check_case_kernel<<<1, kThreads, 0, stream>>>(ws, L.end);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    TileSpace w;
+    set_space(w, L, ws);
+    w.wait_ns = timeout_ns;
+    float* x = reinterpret_cast<float*>(ws + L.end);
+    LinrecArgs a = {};
+    a.x = x;
+    a.gate = x + kCheckTokens;
+    a.y = x + 2 * kCheckTokens;
+    a.S_T = x + 3 * kCheckTokens;
+    a.cu_seqlens = reinterpret_cast<const int32_t*>(x + 3 * kCheckTokens + 4);
+    a.total_tokens = kCheckTokens;
+    a.num_seqs = a.H = a.d = 1;
+    a.dtype = KDA_FP32;
+    a.gate_format = KDA_GATE_CHANNEL_F32;
+    linrec_fwd_kernel<float, KDA_GATE_CHANNEL_F32, false, 1>
+        <<<kCheckTiles - 1, kThreads, kWarps * FwdRows<float, false, 1>::kBytes, stream>>>(a, w);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_linrec_backward(const LinrecArgs& a, char* ws, cudaStream_t stream) {

@@ -81,6 +81,8 @@ def load(path: str | None = None):
     lib.kda_segment_combine.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp]
     lib.kda_check_wait_timeout.restype = ctypes.c_int
     lib.kda_check_wait_timeout.argtypes = [vp, sz, ctypes.c_uint64, vp]
+    lib.kda_check_scan_timeout.restype = ctypes.c_int
+    lib.kda_check_scan_timeout.argtypes = [vp, sz, ctypes.c_uint64, vp]
     lib.kda_prefill_device_status.restype = ctypes.c_int
     lib.kda_prefill_device_status.argtypes = [vp, vp]
     lib.kda_decode_step.restype = ctypes.c_int
@@ -344,6 +346,16 @@ def check_wait_timeout(workspace, timeout_ns: int, *, stream=None) -> None:
         raise KdaError(st, "kda_check_wait_timeout")
 
 
+def check_scan_timeout(workspace, timeout_ns: int, *, stream=None) -> None:
+    """Enqueue kda_check_scan_timeout: the same for the time-axis scan of the ``linrec_*``
+    calls; workspace: at least SCAN_CHECK_BYTES bytes, overwritten."""
+    _check_cuda(workspace)
+    st = load().kda_check_scan_timeout(_ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       int(timeout_ns), _stream_ptr(stream))
+    if st != OK:
+        raise KdaError(st, "kda_check_scan_timeout")
+
+
 def device_status(workspace, stream=None) -> None:
     """Synchronise `stream` and raise KdaError if the device rejected the last prefill's input."""
     st = load().kda_prefill_device_status(_ptr(workspace), _stream_ptr(stream))
@@ -577,6 +589,7 @@ def attnres_layer(blocks, q, *, partial=None, h_last=None, partial_out=None, blo
 
 _DTYPE_CODES = {torch.bfloat16: BF16, torch.float32: FP32}
 LINREC_CHUNK = 128
+SCAN_CHECK_BYTES = 16384
 BEAM_MAX_BEAMS, BEAM_MAX_SELECT = 32, 64
 
 

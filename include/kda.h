@@ -270,6 +270,24 @@ kda_status kda_segment_combine(const float* S_in, const float* g, const float* P
 kda_status kda_check_wait_timeout(void* workspace, size_t workspace_bytes, uint64_t timeout_ns,
                                   kda_stream_t stream);
 
+/* Bytes of workspace kda_check_scan_timeout needs. */
+#define KDA_SCAN_CHECK_BYTES 16384
+
+/*
+ * The same for the time-axis scan of linrec.h, whose tiles wait for those before
+ * them (2 s at most): runs its forward kernel on a small batch of its own with
+ * the limit `timeout_ns`, the first tile left out.  The tiles behind it wait,
+ * one of them gives up and records KDA_ERR_DEVICE_TIMEOUT, the rest stop at
+ * that, and the kernel returns.  Afterwards kda_prefill_device_status(workspace)
+ * returns KDA_ERR_DEVICE_TIMEOUT.
+ *
+ *   workspace   device memory of at least KDA_SCAN_CHECK_BYTES, 16-byte
+ *               aligned; overwritten
+ *   timeout_ns  1e3 .. 1e9 (otherwise KDA_ERR_INVALID_ARG)
+ */
+kda_status kda_check_scan_timeout(void* workspace, size_t workspace_bytes, uint64_t timeout_ns,
+                                  kda_stream_t stream);
+
 /* Largest num_seqs that kda_prefill_noalloc accepts. */
 #define KDA_NOALLOC_MAX_SEQS 65536
 

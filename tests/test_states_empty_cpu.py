@@ -45,3 +45,11 @@ def test_sizes_are_checked_all_the_same(lib):
     assert f(None, None, 0, None, -1, None, 0, 2, 64, 0, 0, None, None, None) == kda.ERR_INVALID_ARG
     assert f(None, None, 0, None, 0, None, 0, 0, 64, 0, 0, None, None, None) == kda.ERR_INVALID_ARG
     assert f(None, None, 7, None, 0, None, 0, 2, 64, 0, 0, None, None, None) == kda.ERR_INVALID_ARG
+
+
+def test_scan_timeout_check_rejects_on_host(lib):
+    f = lib.kda_check_scan_timeout
+    n = kda.SCAN_CHECK_BYTES
+    for args in ((None, n, 10 ** 6), (M + 8, n, 10 ** 6), (M, n - 1, 10 ** 6), (M, n, 999),
+                 (M, n, 10 ** 9 + 1)):
+        assert f(*args, None) == kda.ERR_INVALID_ARG
