@@ -442,8 +442,10 @@ cudaError_t launch_segment_combine(const float* S_in, const float* g, const floa
                                    const float* R, int32_t N, int32_t H, int32_t d_k,
                                    int32_t d_v, float* S_out, cudaStream_t stream) {
     const int smem = (d_k + kCombRows) * (d_k + 1) * (int)sizeof(float);
+    // the limit is the kernel's, for all host threads: that of the widest call (d_k 128)
+    constexpr int kMost = (128 + kCombRows) * (128 + 1) * (int)sizeof(float);
     cudaError_t err = cudaFuncSetAttribute(segment_combine_kernel,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (err != cudaSuccess) return err;
     const int64_t blocks = (int64_t)N * H * ((d_v + kCombRows - 1) / kCombRows);
     if (blocks == 0) return cudaSuccess;
