@@ -17,8 +17,8 @@
 // num_out times a thread's share at the most.
 //
 // Bound: HBM (each logit is read once, 19 us for 64 x 8 x 128000 bf16, 16 of them);
-// measured 37 us: 30 for the pieces, whose warps issue in three cycles of five, and 7 to
-// join.  For the best one alone it is 29 us: the rest is the listing.
+// measured 38 us: 31 for the pieces, whose warps issue in three cycles of five, and 7 to
+// join.  For the best one alone it is 30 us: the rest is the listing.
 #include "kda_internal.h"
 
 #include <cfloat>

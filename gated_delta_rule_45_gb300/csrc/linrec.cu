@@ -35,8 +35,8 @@
 // backward of 8 x 4096 x 4096 380 us for 2.1 GB (5.7).  32 tokens a warp and two CTAs an SM
 // hold 192 KB of inputs on an SM, which covers the waits for the tiles before; 16 tokens
 // and three CTAs took 10 % longer.  With one gate a head there are fewer bytes for the same
-// instructions, and those bound it: 8 x 4096 x 4096 forward 142 us for 0.54 GB (3.8 TB/s),
-// backward 346 us for 1.1 GB (3.1).
+// instructions: 8 x 4096 x 4096 forward 140 us for 0.54 GB (3.9 TB/s), backward 363 us for
+// 1.1 GB (3.0), issue slots 55 and 53 % busy, the rest waits.
 #include "kda_internal.h"
 
 #include <cfloat>
@@ -209,8 +209,9 @@ struct Gate<KDA_GATE_HEAD_F32, VEC> {
 // state multiplies hundreds, 2e-8 too small on average; s moves their argument to where
 // the multiply-add has rounded it to those bits already.  s is one of the values whose
 // 2^-s is a float to 1e-12.  Measured over all bf16 inputs down to log a = -1: at most
-// 1.6e-7 of the gate, 1e-8 or less on average (the full function: 1.1e-7 and 1.5e-8).
-// Below the normal numbers the gate is 0.
+// 1.6e-7 of the gate, 1e-8 or less on average (the full function: 1.1e-7 and 1.5e-8); a
+// log gate of 0 gives exactly 1, and none more than 1.  Below the normal numbers the gate
+// is 0.
 __device__ __forceinline__ float gate_exp(float la) {
     float a;
     asm("ex2.approx.ftz.f32 %0, %1;"
