@@ -1,0 +1,1153 @@
+// Selective state space scan (include/selscan.h): prefill, backward and decode step.
+//
+// Mathematics.  Per channel, h_t = exp(D_t A) h_{t-1} + D_t x_t B_t over the n values of its state
+// and y_t = C_t . h_t.  Unlike a gate that comes with the token, the decays are formed from one
+// step size and n rates: one exponential a (token, channel, value), 16 times as many as there
+// are inputs, for two multiply-adds each.
+//
+// Forward: a channel lies in L lanes of 8 values each (n padded to 8, 16, 32 or 64), its
+// rates and state in registers.  A CTA walks its tokens in tiles of 32: the step sizes and D x
+// are formed once a (token, channel) into shared memory, the state is carried through the
+// tile, and the sums over the state are finished (skip, gate, rounding) by another pass over
+// the tile in rows of 16 bytes.
+//
+// Work along the tokens: where the sequences alone fill the GPU a CTA walks a whole sequence.
+// Few long ones are cut into segments of the packed axis, regardless of sequences: the map of
+// a segment is its end state from zero and the sum of its step sizes (the product of its
+// decays is exp(A sum D)), a short pass joins the maps, and the segments are walked from
+// their entry states.  The backward pass does the same on reversed tokens.
+//
+// Backward: rebuilds the states of 8 tokens at a time in registers from `states` (every 16th
+// token), then walks them backward.
+//
+// Bound: the exponentials and the instructions around them; HBM for small n.
+#include "layer_ops.h"
+
+#include <type_traits>
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 128;   // forward
+constexpr int kTile = 32;       // tokens of a forward tile; segments are whole tiles
+constexpr int kNs = 8;          // state values a lane, forward
+constexpr int kBack = SELSCAN_CHUNK;   // tokens of a backward tile
+constexpr int kSub = 8;         // tokens whose states lie in registers, backward
+static_assert(kTile % SELSCAN_CHUNK == 0 && kBack == 2 * kSub, "tiles hold whole chunks");
+
+// Two floats for the packed instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(F2 r) {
+    float2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+    const float2 v = unpack2(a);
+    return v.x + v.y;
+}
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+// Decays 2^(D A log2 e) as 2^(.. + s) 2^-s: the special-function unit cuts its argument off after
+// 24 fractional bits, which by itself leaves decays near 1, of which a state multiplies hundreds,
+// too small on average; s moves the argument to where the multiply-add has rounded it to those
+// bits already.  s is one of the values whose 2^-s is a float to 1e-12, so a rate of 0 gives
+// exactly 1.
+constexpr float kShift = 0x1.8ca934p-1f, kUnshift = 0x1.2b4368p-1f;
+__device__ __forceinline__ F2 decay2(F2 step, F2 rate) {
+    const float2 v = unpack2(fma2(step, rate, pack2(kShift, kShift)));
+    return mul2(pack2(ex2(v.x), ex2(v.y)), pack2(kUnshift, kUnshift));
+}
+
+// ln(1 + e^v) = max(v, 0) + ln(1 + e), e = e^-|v|, with ln(1 + e) = 2 artanh(e / (2 + e)) by its
+// series (the argument is at most 1/3: seven terms leave 1e-8 of the value), so that small
+// steps keep their relative precision.
+__device__ __forceinline__ float softplus(float v) {
+    const float a = fabsf(v), t = a * kLog2e;
+    // what the product's rounding left out of the exponent
+    const float rest = a < 80.f ? fmaf(a, kLog2e, -t) : 0.f;
+    float e = ex2(-t);
+    e = fmaf(e, -kLn2 * rest, e);
+    const float s = __fdividef(e, 2.f + e), q = s * s;
+    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(p, q, 1.f / 9.f);
+    p = fmaf(p, q, 1.f / 7.f);
+    p = fmaf(p, q, 1.f / 5.f);
+    p = fmaf(p, q, 1.f / 3.f);
+    p = fmaf(p, q, 1.f);
+    return fmaf(2.f * s, p, fmaxf(v, 0.f));
+}
+
+// How the work is cut: segments along the tokens (whole sequences when seg == 0) and blocks of
+// channels, none of which spans two groups.
+struct Cut {
+    int64_t seg;        // tokens of a segment
+    int64_t nseg;       // segments, or sequences
+    int32_t per_group;  // channel blocks of a group
+    int64_t items;      // nseg x blocks
+};
+
+// The maps of the segments, in the workspace.
+struct Maps {
+    float* sum;     // [nseg][D]      sum of the step sizes
+    float* state;   // [nseg][D][n]   end state from zero; then, joined, the entry state
+    int32_t* reset; // [nseg]         whether what comes before the segment stays in it
+};
+
+// Values k .. k + 7 of a state row of n.
+__device__ __forceinline__ void load8(const float* p, int k, int n, float (&v)[kNs]) {
+#pragma unroll
+    for (int i = 0; i < kNs; ++i) v[i] = 0.f;
+    if (!p) return;
+    if (n % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kNs; i += 4)
+            if (k + i < n) {
+                const float4 u = *reinterpret_cast<const float4*>(p + k + i);
+                v[i] = u.x; v[i + 1] = u.y; v[i + 2] = u.z; v[i + 3] = u.w;
+            }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kNs; ++i)
+            if (k + i < n) v[i] = p[k + i];
+    }
+}
+__device__ __forceinline__ void store8(float* p, int k, int n, const F2 (&h)[kNs / 2]) {
+    float v[kNs];
+#pragma unroll
+    for (int i = 0; i < kNs / 2; ++i) {
+        const float2 u = unpack2(h[i]);
+        v[2 * i] = u.x;
+        v[2 * i + 1] = u.y;
+    }
+    if (n % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < kNs; i += 4)
+            if (k + i < n)
+                *reinterpret_cast<float4*>(p + k + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kNs; ++i)
+            if (k + i < n) p[k + i] = v[i];
+    }
+}
+
+// What a forward kernel does with the tokens: the outputs, the maps of the segments, or the
+// maps of the gradients' recurrence (on reversed tokens).
+enum { kOutputs = 0, kMaps = 1, kGradMaps = 2 };
+
+template <int L>
+struct FwdShared {
+    static constexpr int kCh = kThreads / L;
+    float2 du[kTile][kCh];        // step size and what drives the state; then, in y, the output
+    float B[kTile][kNs * L], C[kTile][kNs * L];
+};
+
+template <typename T, int L, int V, int PASS>
+__global__ void __launch_bounds__(kThreads)
+scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
+    using S = FwdShared<L>;
+    constexpr int CH = S::kCh, NP = kNs * L;
+    constexpr int VR = CH / V;                                     // vectors of a row
+    constexpr int NI = (kTile * VR + kThreads - 1) / kThreads;     // of a tile, a thread
+    __shared__ S s;
+    const int32_t* cu = p.cu_seqlens;
+    if (!offsets_ok(cu, p.num_seqs, p.total_tokens, status)) return;
+    const int tid = threadIdx.x, cl = tid / L, li = tid % L;
+    const int64_t D = (int64_t)p.H * p.d, last = cu[p.num_seqs];
+    const T* const X = static_cast<const T*>(PASS == kGradMaps ? p.dy : p.in.x);
+    const int64_t ldx = PASS == kGradMaps ? D : p.in.ldx;
+    const T* const DT = static_cast<const T*>(p.in.dt);
+    const T* const Z = static_cast<const T*>(p.in.z);
+
+    for (int64_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
+        const int64_t blocks = (int64_t)cut.per_group * p.H;
+        const int64_t sg = item / blocks;
+        const int32_t cb = (int32_t)(item - sg * blocks);
+        const int32_t g = cb / cut.per_group;
+        const int32_t c0 = (cb - g * cut.per_group) * CH;          // first channel in the group
+        const int32_t width = p.d - c0 < CH ? p.d - c0 : CH;
+        const int64_t base = (int64_t)g * p.d + c0;                // and of all
+        const bool on = cl < width;
+        const int64_t state_at = (base + cl) * p.n;
+
+        int64_t t0, t1;   // tokens to walk, the sequence of the next one, and its end
+        int32_t n;
+        bool reset = false;
+        if (cut.seg == 0) {
+            n = (int32_t)sg;
+            t0 = cu[n];
+            t1 = cu[n + 1];
+        } else {
+            t0 = sg * cut.seg;
+            t1 = t0 + cut.seg < last ? t0 + cut.seg : last;
+            if (t0 >= t1) continue;
+            if (PASS == kMaps) {
+                n = sequence_of(cu, p.num_seqs, t1 - 1);
+                reset = cu[n] >= t0;
+                if (reset) t0 = cu[n];
+            } else if (PASS == kGradMaps) {
+                n = sequence_of(cu, p.num_seqs, t0);
+                reset = cu[n + 1] <= t1;
+                if (reset) t1 = cu[n + 1];
+            } else {
+                n = sequence_of(cu, p.num_seqs, t0);
+            }
+        }
+
+        F2 A[kNs / 2], h[kNs / 2];
+        {
+            float v[kNs];
+            load8(on ? p.A + state_at : nullptr, li * kNs, p.n, v);
+#pragma unroll
+            for (int i = 0; i < kNs / 2; ++i) A[i] = pack2(v[2 * i] * kLog2e, v[2 * i + 1] * kLog2e);
+        }
+        auto set_state = [&](const float* from) {
+            float v[kNs];
+            load8(on && from ? from + state_at : nullptr, li * kNs, p.n, v);
+#pragma unroll
+            for (int i = 0; i < kNs / 2; ++i) h[i] = pack2(v[2 * i], v[2 * i + 1]);
+        };
+        if (PASS == kGradMaps)
+            set_state(reset && p.dS_T ? p.dS_T + n * D * p.n : nullptr);
+        else if (t0 == cu[n])
+            set_state(p.S0 ? p.S0 + n * D * p.n : nullptr);
+        else
+            set_state(PASS == kOutputs ? maps.state + sg * D * p.n : nullptr);
+        if (PASS == kOutputs && cut.seg == 0 && t0 >= t1) {   // an empty sequence
+            if (on && p.S_T) store8(p.S_T + n * D * p.n + state_at, li * kNs, p.n, h);
+            continue;
+        }
+        float sum = 0.f;
+
+        Pack<T, V> rx[NI], rd[NI], rz[NI];
+        // this tile's tokens [a, b) of the walk
+        int64_t a, b;
+        auto tile_of = [&](int64_t t) {   // t: the first token, or one behind the last (reversed)
+            if (PASS == kGradMaps) {
+                b = t;
+                a = (t - 1) / kTile * kTile;
+                if (a < t0) a = t0;
+            } else {
+                a = t;
+                b = t / kTile * kTile + kTile;
+                if (b > t1) b = t1;
+            }
+        };
+        // the vector i of this thread: its row and first channel
+        auto row_of = [&](int i) { return (tid + i * kThreads) / VR; };
+        auto col_of = [&](int i) { return (tid + i * kThreads) % VR * V; };
+        auto fetch = [&](int64_t from, int64_t to) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = row_of(i), c = col_of(i);
+                if (from + r < to && c < width) {
+                    rx[i].load(X + (from + r) * ldx + base + c);
+                    rd[i].load(DT + (from + r) * p.in.lddt + base + c);
+                    if (PASS == kGradMaps && Z) rz[i].load(Z + (from + r) * p.in.ldz + base + c);
+                }
+            }
+        };
+        tile_of(PASS == kGradMaps ? t1 : t0);
+        if (V > 1) fetch(a, b);
+        while (true) {
+            int64_t end = b;
+            if (PASS == kOutputs) {   // tiles end with their sequence
+                const int64_t e = cu[n + 1];
+                if (e < end) end = e;
+            }
+            const int cnt = (int)(end - a);
+            if (V == 1) fetch(a, end);
+            Pack<T, V> kx[NI];
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = row_of(i), c = col_of(i);
+                kx[i] = rx[i];
+                if (r < cnt && c < width) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        float v = rd[i].get(k) + (p.dt_bias ? p.dt_bias[base + c + k] : 0.f);
+                        if (p.softplus) v = softplus(v);
+                        float u = rx[i].get(k);
+                        if (PASS == kGradMaps) u = Z ? u * silu(rz[i].get(k)) : u;
+                        else u *= v;
+                        s.du[r][c + k] = make_float2(v, u);
+                    }
+                }
+            }
+            for (int i = tid; i < kTile * NP; i += kThreads) {
+                const int r = i / NP, k = i % NP;
+                float bv = 0.f, cv = 0.f;
+                if (r < cnt && k < p.n) {
+                    if (PASS != kGradMaps)
+                        bv = Elem<T>::load(static_cast<const T*>(p.in.B) + (a + r) * p.in.ldB +
+                                           (int64_t)g * p.n + k);
+                    if (PASS != kMaps)
+                        cv = Elem<T>::load(static_cast<const T*>(p.in.C) + (a + r) * p.in.ldC +
+                                           (int64_t)g * p.n + k);
+                }
+                s.B[r][k] = bv;
+                s.C[r][k] = cv;
+            }
+            __syncthreads();
+            const int64_t a_now = a;
+            bool more;
+            if (PASS == kGradMaps) {
+                more = a > t0;
+                if (more) tile_of(a);
+            } else {
+                more = end < t1;
+                if (more) tile_of(end);
+            }
+            if (V > 1 && more) fetch(a, b);
+            if (PASS == kOutputs && Z && V > 1) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int r = row_of(i), c = col_of(i);
+                    if (r < cnt && c < width) rz[i].load(Z + (a_now + r) * p.in.ldz + base + c);
+                }
+            }
+            const int64_t start = PASS == kOutputs ? cu[n] : 0;
+            // (channels that are not there take part in the sums over the lanes)
+            {
+#pragma unroll 4
+                for (int j = 0; j < cnt; ++j) {
+                    const int r = PASS == kGradMaps ? cnt - 1 - j : j;
+                    if (PASS == kOutputs && p.states && on && ((a_now + r) & (SELSCAN_CHUNK - 1)) == 0 &&
+                        a_now + r > start)
+                        store8(p.states + (a_now + r) / SELSCAN_CHUNK * D * p.n + state_at, li * kNs,
+                               p.n, h);
+                    const float2 du = s.du[r][cl];
+                    const F2 dd = pack2(du.x, du.x), uu = pack2(du.y, du.y);
+                    if (PASS != kOutputs) sum += du.x;
+                    F2 y = 0;
+                    const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(&s.B[r][li * kNs]);
+                    const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(&s.C[r][li * kNs]);
+#pragma unroll
+                    for (int i = 0; i < kNs / 4; ++i) {
+                        ulonglong2 bv = {}, cv = {};
+                        if (PASS != kGradMaps) bv = Bp[i];
+                        if (PASS != kMaps) cv = Cp[i];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int k = 2 * i + q;
+                            const F2 dec = decay2(dd, A[k]);
+                            if (PASS == kGradMaps) {
+                                h[k] = mul2(dec, fma2(uu, q ? cv.y : cv.x, h[k]));
+                            } else {
+                                h[k] = fma2(dec, h[k], mul2(uu, q ? bv.y : bv.x));
+                                if (PASS == kOutputs) y = fma2(h[k], q ? cv.y : cv.x, y);
+                            }
+                        }
+                    }
+                    if (PASS == kOutputs) {
+                        float v = sum2(y);
+#pragma unroll
+                        for (int o = 1; o < L; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                        if (li == 0) s.du[r][cl].y = v;   // (the channel's lanes have read it)
+                    }
+                }
+            }
+            __syncthreads();
+            if (PASS == kOutputs && p.y) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int r = row_of(i), c = col_of(i);
+                    if (r < cnt && c < width) {
+                        if (V == 1 && Z) rz[i].load(Z + (a_now + r) * p.in.ldz + base + c);
+                        float o[V];
+#pragma unroll
+                        for (int k = 0; k < V; ++k) {
+                            o[k] = s.du[r][c + k].y;
+                            if (p.skip) o[k] = fmaf(p.skip[base + c + k], kx[i].get(k), o[k]);
+                            if (Z) o[k] *= silu(rz[i].get(k));
+                        }
+                        Pack<T, V> ky;
+                        ky.set(o);
+                        ky.store(static_cast<T*>(p.y) + (a_now + r) * D + base + c);
+                    }
+                }
+            }
+            if (PASS == kOutputs && end == cu[n + 1]) {
+                if (on && p.S_T) store8(p.S_T + n * D * p.n + state_at, li * kNs, p.n, h);
+                if (more) {
+                    while (cu[n + 1] <= end) ++n;
+                    set_state(p.S0 ? p.S0 + n * D * p.n : nullptr);
+                }
+            }
+            if (!more) break;
+        }
+        if (PASS != kOutputs && on) {
+            store8(maps.state + sg * D * p.n + state_at, li * kNs, p.n, h);
+            if (li == 0) maps.sum[sg * D + base + cl] = sum;
+            if (cb == 0 && tid == 0) maps.reset[sg] = reset;
+        }
+    }
+}
+
+// Joins the segments' maps: state[s] becomes the state that enters segment s (reversed: that
+// reaches it from behind).
+constexpr int kJoin = 8;   // segments loaded at once
+__global__ void __launch_bounds__(kThreads)
+join_kernel(const ScanArgs p, const Cut cut, const Maps maps, bool reversed, const int32_t* status) {
+    if (*status != KDA_OK) return;
+    const int64_t D = (int64_t)p.H * p.d, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (i >= D * p.n) return;
+    const int64_t last = p.cu_seqlens[p.num_seqs], segs = (last + cut.seg - 1) / cut.seg;
+    const int64_t c = i / p.n;
+    const float A = p.A[i] * kLog2e;
+    float h = 0.f;
+    for (int64_t s0 = 0; s0 < segs; s0 += kJoin) {
+        float e[kJoin], d[kJoin];
+        bool r[kJoin];
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+            const int64_t s = reversed ? segs - 1 - (s0 + k) : s0 + k;
+            if (s0 + k < segs) {
+                e[k] = maps.state[s * D * p.n + i];
+                d[k] = maps.sum[s * D + c];
+                r[k] = maps.reset[s] != 0;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kJoin; ++k) {
+            const int64_t s = reversed ? segs - 1 - (s0 + k) : s0 + k;
+            if (s0 + k < segs) {
+                maps.state[s * D * p.n + i] = h;
+                h = r[k] ? e[k] : fmaf(ex2(fmaf(d[k], A, kShift)) * kUnshift, h, e[k]);
+            }
+        }
+    }
+}
+
+// out[n] = in[n] (or zeros) for the empty sequences, which no segment holds.
+__global__ void __launch_bounds__(kThreads)
+empty_kernel(const int32_t* cu, int32_t N, int64_t row, const float* in, float* out,
+             const int32_t* status) {
+    if (*status != KDA_OK) return;
+    for (int64_t n = blockIdx.x; n < N; n += gridDim.x) {
+        if (cu[n] != cu[n + 1]) continue;
+        for (int64_t i = threadIdx.x; i < row; i += kThreads)
+            out[n * row + i] = in ? in[n * row + i] : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------- backward
+
+// NL lanes share a channel's state, four values each; a thread holds two channels.
+template <int NL>
+struct Back {
+    static constexpr int kCl = 32 / NL;                       // channel pairs of a warp
+    static constexpr int kWarps = NL == 2 ? 4 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kCh = kWarps * kCl * 2;
+    static constexpr int kRows = kThreads / kCh;              // tokens side by side in the other passes
+    struct Shared {
+        float2 du[kBack][kCh];
+        float dr[kBack][kCh];
+        float B[kBack][4 * NL], C[kBack][4 * NL];
+        float y[kBack][kCh], s1[kBack][kCh], s2[kBack][kCh];
+        float part[kWarps][kBack][8 * NL];
+    };
+};
+
+// The sums of 8 values over the lanes that differ in the bits from NL up: each exchange halves
+// the values a lane carries.  Returns the index of v[0] among the eight (v[1..] follow).
+template <int NL>
+__device__ __forceinline__ int sum_channels(float (&v)[8], int lane) {
+    int at = 0, nv = 8;
+#pragma unroll
+    for (int o = 16; o >= NL; o >>= 1) {
+        if (nv > 1) {
+            nv /= 2;
+            const bool upper = lane & o;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < nv) {
+                    const float give = upper ? v[i] : v[i + nv];
+                    v[i] = (upper ? v[i + nv] : v[i]) + __shfl_xor_sync(0xffffffffu, give, o);
+                }
+            at += upper ? nv : 0;
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        }
+    }
+    return at;
+}
+template <int NL>
+constexpr int kLeft = NL >= 16 ? 4 : NL >= 8 ? 2 : 1;   // values a lane is left with
+
+template <typename T, int NL>
+__global__ void __launch_bounds__(Back<NL>::kThreads)
+scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A, float* part_c,
+                float* part_BC, const int32_t* status) {
+    using G = Back<NL>;
+    constexpr int CH = G::kCh, TH = G::kThreads, NP = 4 * NL;
+    extern __shared__ __align__(16) char raw[];
+    typename G::Shared& s = *reinterpret_cast<typename G::Shared*>(raw);
+    if (*status != KDA_OK) return;
+    const int32_t* cu = p.cu_seqlens;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nl = lane % NL, cp = warp * G::kCl + lane / NL;   // my values, my channel pair
+    const int64_t D = (int64_t)p.H * p.d, last = cu[p.num_seqs];
+    const T* const X = static_cast<const T*>(p.in.x);
+    const T* const DT = static_cast<const T*>(p.in.dt);
+    const T* const Z = static_cast<const T*>(p.in.z);
+    const T* const DY = static_cast<const T*>(p.dy);
+
+    for (int64_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
+        const int64_t blocks = (int64_t)cut.per_group * p.H;
+        const int64_t sg = item / blocks;
+        const int32_t cb = (int32_t)(item - sg * blocks);
+        const int32_t g = cb / cut.per_group, cg = cb - g * cut.per_group;
+        const int32_t c0 = cg * CH;
+        const int32_t width = p.d - c0 < CH ? p.d - c0 : CH;
+        const int64_t base = (int64_t)g * p.d + c0;
+        int64_t t0, t1;
+        int32_t n;
+        if (cut.seg == 0) {
+            n = (int32_t)sg;
+            t0 = cu[n];
+            t1 = cu[n + 1];
+        } else {
+            t0 = sg * cut.seg;
+            t1 = t0 + cut.seg < last ? t0 + cut.seg : last;
+            n = t0 < t1 ? sequence_of(cu, p.num_seqs, t1 - 1) : 0;
+        }
+        // rows of four values of my two channels in a [..][D][n] tensor
+        auto load4 = [&](const float* from, F2 (&v)[2][2]) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                float u[4] = {0.f, 0.f, 0.f, 0.f};
+                if (from && 2 * cp + q < width) {
+                    const float* r = from + (base + 2 * cp + q) * p.n + nl * 4;
+                    if (p.n % 4 == 0) {
+                        if (nl * 4 < p.n) {
+                            const float4 w = *reinterpret_cast<const float4*>(r);
+                            u[0] = w.x; u[1] = w.y; u[2] = w.z; u[3] = w.w;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (nl * 4 + i < p.n) u[i] = r[i];
+                    }
+                }
+                v[q][0] = pack2(u[0], u[1]);
+                v[q][1] = pack2(u[2], u[3]);
+            }
+        };
+        auto store4 = [&](float* to, const F2 (&v)[2][2]) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (2 * cp + q >= width) continue;
+                float* r = to + (base + 2 * cp + q) * p.n + nl * 4;
+                const float2 lo = unpack2(v[q][0]), hi = unpack2(v[q][1]);
+                const float u[4] = {lo.x, lo.y, hi.x, hi.y};
+                if (p.n % 4 == 0) {
+                    if (nl * 4 < p.n)
+                        *reinterpret_cast<float4*>(r) = make_float4(u[0], u[1], u[2], u[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (nl * 4 + i < p.n) r[i] = u[i];
+                }
+            }
+        };
+        F2 A[2][2], dA[2][2], r[2][2];   // rates, their gradients, the gradient from behind
+        load4(p.A, A);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                A[q][i] = mul2(A[q][i], pack2(kLog2e, kLog2e));
+                dA[q][i] = 0;
+            }
+        const float* behind = nullptr;
+        if (t0 < t1 && t1 != cu[n + 1]) behind = maps.state + sg * D * p.n;
+        else if (p.dS_T && (t0 < t1 || cut.seg == 0)) behind = p.dS_T + n * D * p.n;
+        load4(behind, r);
+        // the passes over (token, channel): a channel and every kRows-th token a thread
+        const int mc = tid % CH, mr = tid / CH;
+        const bool mine = mc < width && mr < G::kRows;
+        const float bias = mine && p.dt_bias ? p.dt_bias[base + mc] : 0.f;
+        const float skip = mine && p.skip ? p.skip[base + mc] : 0.f;
+        float dskip = 0.f, dbias = 0.f;
+
+        int64_t te = t1;
+        if (cut.seg == 0 && t0 >= t1 && p.g.dS0) store4(p.g.dS0 + n * D * p.n, r);
+        while (te > t0) {
+            const int64_t start = cu[n];
+            int64_t ta = (te - 1) / kBack * kBack;
+            if (ta < start) ta = start;
+            if (ta < t0) ta = t0;
+            const int cnt = (int)(te - ta);
+            if (mine) {
+                for (int k = mr; k < cnt; k += G::kRows) {
+                    const int64_t t = ta + k;
+                    float v = Elem<T>::load(DT + t * p.in.lddt + base + mc) + bias;
+                    if (p.softplus) v = softplus(v);
+                    float dr = Elem<T>::load(DY + t * D + base + mc);
+                    if (Z) dr *= silu(Elem<T>::load(Z + t * p.in.ldz + base + mc));
+                    s.du[k][mc] = make_float2(v, v * Elem<T>::load(X + t * p.in.ldx + base + mc));
+                    s.dr[k][mc] = dr;
+                }
+            } else if (mr < G::kRows) {   // channels that are not there
+                for (int k = mr; k < cnt; k += G::kRows) {
+                    s.du[k][mc] = make_float2(0.f, 0.f);
+                    s.dr[k][mc] = 0.f;
+                }
+            }
+            for (int i = tid; i < kBack * NP; i += TH) {
+                const int k = i / NP, j = i % NP;
+                const bool in = k < cnt && j < p.n;
+                s.B[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.B) + (ta + k) * p.in.ldB +
+                                               (int64_t)g * p.n + j) : 0.f;
+                s.C[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.C) + (ta + k) * p.in.ldC +
+                                               (int64_t)g * p.n + j) : 0.f;
+            }
+            __syncthreads();
+            F2 h0[2][2];   // the state before token ta
+            if (ta == start) load4(p.S0 ? p.S0 + n * D * p.n : nullptr, h0);
+            else load4(p.states + ta / kBack * D * p.n, h0);
+
+            auto advance = [&](int k, F2 (&h)[2][2]) {
+                const float4 du = *reinterpret_cast<const float4*>(&s.du[k][2 * cp]);
+                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.B[k][nl * 4]);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float dv = q ? du.z : du.x, uv = q ? du.w : du.y;
+                    const F2 dd = pack2(dv, dv), uu = pack2(uv, uv);
+                    h[q][0] = fma2(decay2(dd, A[q][0]), h[q][0], mul2(uu, b.x));
+                    h[q][1] = fma2(decay2(dd, A[q][1]), h[q][1], mul2(uu, b.y));
+                }
+            };
+            // tokens [from, to) of the tile, at most kSub, from state h: rebuilt, then backward
+            auto sub = [&](int from, int to, F2 (&h)[2][2]) {
+                F2 before[kSub][2][2];
+#pragma unroll
+                for (int j = 0; j < kSub; ++j) {
+                    if (from + j < to) {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            before[j][q][0] = h[q][0];
+                            before[j][q][1] = h[q][1];
+                        }
+                        advance(from + j, h);
+                        if (Z) {
+                            const ulonglong2 c =
+                                *reinterpret_cast<const ulonglong2*>(&s.C[from + j][nl * 4]);
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                float y = sum2(fma2(h[q][0], c.x, mul2(h[q][1], c.y)));
+#pragma unroll
+                                for (int o = 1; o < NL; o *= 2)
+                                    y += __shfl_xor_sync(0xffffffffu, y, o);
+                                if (nl == 0) s.y[from + j][2 * cp + q] = y;
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = kSub - 1; j >= 0; --j) {
+                    if (from + j >= to) continue;
+                    const int k = from + j;
+                    const float4 du = *reinterpret_cast<const float4*>(&s.du[k][2 * cp]);
+                    const float2 dr = *reinterpret_cast<const float2*>(&s.dr[k][2 * cp]);
+                    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.B[k][nl * 4]);
+                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s.C[k][nl * 4]);
+                    F2 vB[2] = {0, 0}, vC[2] = {0, 0};
+                    float s1[2], s2[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float dv = q ? du.z : du.x, uv = q ? du.w : du.y;
+                        const float rv = q ? dr.y : dr.x;
+                        const F2 dd = pack2(dv, dv), uu = pack2(uv, uv), rr = pack2(rv, rv);
+                        F2 t1 = 0, t2 = 0;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const F2 a = decay2(dd, A[q][i]);
+                            const F2 gr = fma2(i ? c.y : c.x, rr, r[q][i]);   // gradient of h
+                            vC[i] = fma2(h[q][i], rr, vC[i]);
+                            vB[i] = fma2(gr, uu, vB[i]);
+                            t1 = fma2(gr, i ? b.y : b.x, t1);
+                            const F2 w = mul2(gr, mul2(a, before[j][q][i]));
+                            dA[q][i] = fma2(w, dd, dA[q][i]);
+                            t2 = fma2(w, A[q][i], t2);
+                            r[q][i] = mul2(a, gr);
+                            h[q][i] = before[j][q][i];
+                        }
+                        s1[q] = sum2(t1);
+                        s2[q] = sum2(t2);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int o = 1; o < NL; o *= 2) {
+                            s1[q] += __shfl_xor_sync(0xffffffffu, s1[q], o);
+                            s2[q] += __shfl_xor_sync(0xffffffffu, s2[q], o);
+                        }
+                        if (nl == 0) {
+                            s.s1[k][2 * cp + q] = s1[q];
+                            s.s2[k][2 * cp + q] = s2[q] * kLn2;
+                        }
+                    }
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float2 x = unpack2(vB[i]), y = unpack2(vC[i]);
+                        v[2 * i] = x.x;
+                        v[2 * i + 1] = x.y;
+                        v[4 + 2 * i] = y.x;
+                        v[4 + 2 * i + 1] = y.y;
+                    }
+                    const int at = sum_channels<NL>(v, lane);
+#pragma unroll
+                    for (int i = 0; i < kLeft<NL>; ++i) s.part[warp][k][(at + i) * NL + nl] = v[i];
+                }
+            };
+            // the tile's halves, the later one first
+            const int half = (int)(ta / kBack * kBack + kSub - ta);
+            if (half > 0 && half < cnt) {
+                F2 h[2][2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) h[q][i] = h0[q][i];
+                for (int k = 0; k < half; ++k) advance(k, h);
+                sub(half, cnt, h);
+                sub(0, half, h0);
+            } else {
+                sub(0, cnt, h0);
+            }
+            __syncthreads();
+            if (mine) {
+                for (int k = mr; k < cnt; k += G::kRows) {
+                    const int64_t t = ta + k, at = t * D + base + mc;
+                    const float x = Elem<T>::load(X + t * p.in.ldx + base + mc);
+                    const float raw_dt = Elem<T>::load(DT + t * p.in.lddt + base + mc) + bias;
+                    const float s1 = s.s1[k][mc], dr = s.dr[k][mc], step = s.du[k][mc].x;
+                    float ddt = fmaf(x, s1, s.s2[k][mc]);
+                    if (p.softplus) ddt *= sigmoid(raw_dt);
+                    p.g.ddt[at] = ddt;
+                    p.g.dx[at] = fmaf(step, s1, skip * dr);
+                    if (Z) {
+                        const float dy = Elem<T>::load(DY + at);
+                        const float z = Elem<T>::load(Z + t * p.in.ldz + base + mc);
+                        p.g.dz[at] = dy * fmaf(skip, x, s.y[k][mc]) * silu_grad(z);
+                    }
+                    dskip = fmaf(dr, x, dskip);
+                    dbias += ddt;
+                }
+            }
+            // sums over the CTA's channels: to the outputs if it has the whole group
+            for (int i = tid; i < cnt * 8 * NL; i += TH) {
+                const int k = i / (8 * NL), j = i % (8 * NL);
+                const int v = j / NL, st = (j % NL) * 4 + (v & 3);
+                if (st >= p.n) continue;
+                float sum = s.part[0][k][j];
+#pragma unroll
+                for (int w = 1; w < G::kWarps; ++w) sum += s.part[w][k][j];
+                const int64_t row = (ta + k) * p.H + g;
+                if (cut.per_group == 1) (v < 4 ? p.g.dB : p.g.dC)[row * p.n + st] = sum;
+                else part_BC[((int64_t)cg * p.total_tokens * p.H + row) * 2 * p.n +
+                             (v < 4 ? 0 : p.n) + st] = sum;
+            }
+            __syncthreads();
+            te = ta;
+            if (te == start) {
+                if (p.g.dS0) store4(p.g.dS0 + n * D * p.n, r);
+                if (te > t0) {
+                    do --n; while (cu[n] == cu[n + 1]);
+                    load4(p.dS_T ? p.dS_T + n * D * p.n : nullptr, r);
+                }
+            }
+        }
+        store4(part_A + sg * D * p.n, dA);
+        // the threads of a channel, in order
+        if (G::kRows > 1) {
+            float* j = &s.y[0][0];
+            if (mr < G::kRows) {
+                j[mr * 2 * CH + mc] = dskip;
+                j[mr * 2 * CH + CH + mc] = dbias;
+            }
+            __syncthreads();
+            if (mr == 0) {
+#pragma unroll
+                for (int k = 1; k < G::kRows; ++k) {
+                    dskip += j[k * 2 * CH + mc];
+                    dbias += j[k * 2 * CH + CH + mc];
+                }
+            }
+            __syncthreads();
+        }
+        if (mine && mr == 0) {
+            part_c[sg * 2 * D + base + mc] = dskip;
+            part_c[sg * 2 * D + D + base + mc] = dbias;
+        }
+    }
+}
+
+// dB, dC: the sums over the groups' channel blocks, in order.
+__global__ void __launch_bounds__(256)
+sum_blocks_kernel(const ScanArgs p, int32_t blocks, const float* __restrict__ part,
+                  const int32_t* status) {
+    if (*status != KDA_OK) return;
+    const int64_t rows = (int64_t)p.cu_seqlens[p.num_seqs] * p.H, w = 2 * p.n;
+    const int64_t stride = p.total_tokens * p.H * w;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * w;
+         i += (int64_t)gridDim.x * 256) {
+        float sum = 0.f;
+        int32_t b = 0;
+        for (; b + 4 <= blocks; b += 4) {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = part[(b + k) * stride + i];
+            sum += (v[0] + v[1]) + (v[2] + v[3]);
+        }
+        for (; b < blocks; ++b) sum += part[b * stride + i];
+        const int64_t row = i / w;
+        const int k = (int)(i - row * w);
+        (k < p.n ? p.g.dB : p.g.dC)[row * p.n + (k < p.n ? k : k - p.n)] = sum;
+    }
+}
+
+// ---------------------------------------------------------------- decode step
+
+// One token a row: L lanes a channel, 8 values each.
+template <typename T, int L>
+__global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanStepArgs p, int64_t blocks) {
+    const int64_t D = (int64_t)p.H * p.d;
+    const int64_t b = blockIdx.x / blocks;
+    const int64_t ch = (blockIdx.x - b * blocks) * (kThreads / L) + threadIdx.x / L;
+    const int li = threadIdx.x % L;
+    const bool on = ch < D;   // (all lanes of a warp take part in its sums)
+    const int64_t c = on ? ch : 0;
+    const int32_t row = p.parents ? p.parents[b] : (int32_t)b;
+    const bool live = row >= 0 && row < p.num_rows;
+    float A[kNs], h[kNs];
+    load8(p.A + c * p.n, li * kNs, p.n, A);
+    load8(live ? p.S + ((int64_t)row * D + c) * p.n : nullptr, li * kNs, p.n, h);
+    const float x = Elem<T>::load(static_cast<const T*>(p.in.x) + b * p.in.ldx + c);
+    float step = Elem<T>::load(static_cast<const T*>(p.in.dt) + b * p.in.lddt + c) +
+                 (p.dt_bias ? p.dt_bias[c] : 0.f);
+    if (p.softplus) step = softplus(step);
+    const int64_t g = c / p.d;
+    const T* B = static_cast<const T*>(p.in.B) + b * p.in.ldB + g * p.n;
+    const T* C = static_cast<const T*>(p.in.C) + b * p.in.ldC + g * p.n;
+    F2 hv[kNs / 2];
+    float y = 0.f;
+#pragma unroll
+    for (int i = 0; i < kNs; ++i) {
+        const int k = li * kNs + i;
+        const float bv = k < p.n ? Elem<T>::load(B + k) : 0.f, cv = k < p.n ? Elem<T>::load(C + k) : 0.f;
+        const float a = ex2(fmaf(step, A[i] * kLog2e, kShift)) * kUnshift;
+        h[i] = fmaf(a, h[i], step * x * bv);
+        y = fmaf(h[i], cv, y);
+    }
+#pragma unroll
+    for (int i = 0; i < kNs / 2; ++i) hv[i] = pack2(h[2 * i], h[2 * i + 1]);
+#pragma unroll
+    for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if (!on) return;
+    store8(p.S_out + (b * D + c) * p.n, li * kNs, p.n, hv);
+    if (li != 0) return;
+    if (p.skip) y = fmaf(p.skip[c], x, y);
+    if (p.in.z) y *= silu(Elem<T>::load(static_cast<const T*>(p.in.z) + b * p.in.ldz + c));
+    Elem<T>::store(static_cast<T*>(p.y) + b * D + c, y);
+}
+
+// ---------------------------------------------------------------- host
+
+size_t pad(size_t b) { return (b + 255) & ~(size_t)255; }
+constexpr size_t kHead = 256;   // the status word's part of the workspace
+int64_t sms() { return sm_count() > 0 ? sm_count() : 1; }
+
+int lanes_of(int n) { return n <= 8 ? 1 : n <= 16 ? 2 : n <= 32 ? 4 : 8; }
+int back_lanes_of(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
+int back_channels(int n) {
+    switch (back_lanes_of(n)) {
+        case 2: return Back<2>::kCh;
+        case 4: return Back<4>::kCh;
+        case 8: return Back<8>::kCh;
+        default: return Back<16>::kCh;
+    }
+}
+
+// Whole sequences where they and the channel blocks of `ch` make at least `want` CTAs an SM, or
+// are short; else segments that do.
+Cut make_cut(int32_t N, int64_t T, int32_t H, int32_t d, int ch, int want) {
+    Cut c = {};
+    c.per_group = (d + ch - 1) / ch;
+    const int64_t blocks = (int64_t)c.per_group * H, fill = want * sms();
+    if (N == 0 || N * blocks >= fill || T < (int64_t)N * 2 * kTile) {
+        c.nseg = N;
+    } else {
+        const int64_t most = (2 * fill + blocks - 1) / blocks;   // segments that fill it twice
+        c.seg = ((T + most - 1) / most + kTile - 1) / kTile * kTile;
+        if (c.seg < 2 * kTile) c.seg = 2 * kTile;
+        c.nseg = (T + c.seg - 1) / c.seg;
+    }
+    c.items = c.nseg * blocks;
+    return c;
+}
+Cut forward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
+    return make_cut(N, T, H, d, kThreads / lanes_of(n), 3);
+}
+Cut backward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
+    return make_cut(N, T, H, d, back_channels(n), 1);
+}
+// The maps of the gradients' recurrence are formed by the forward kernel: the same segments, but
+// its own channel blocks.
+Cut grad_map_cut(const Cut& back, int32_t H, int32_t d, int32_t n) {
+    Cut c = back;
+    const int ch = kThreads / lanes_of(n);
+    c.per_group = (d + ch - 1) / ch;
+    c.items = c.nseg * c.per_group * H;
+    return c;
+}
+
+size_t maps_bytes(const Cut& c, int64_t D, int32_t n) {
+    if (c.seg == 0) return 0;
+    return pad((size_t)c.nseg * D * 4) + pad((size_t)c.nseg * D * n * 4) + pad((size_t)c.nseg * 4);
+}
+Maps place_maps(const Cut& c, int64_t D, int32_t n, char* ws) {
+    Maps m = {};
+    if (c.seg == 0) return m;
+    m.sum = reinterpret_cast<float*>(ws);
+    m.state = reinterpret_cast<float*>(ws + pad((size_t)c.nseg * D * 4));
+    m.reset = reinterpret_cast<int32_t*>(ws + pad((size_t)c.nseg * D * 4) +
+                                         pad((size_t)c.nseg * D * n * 4));
+    return m;
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+template <typename F>
+cudaError_t by_type(kda_dtype dtype, F&& f) {
+    return dtype == KDA_BF16 ? f((__nv_bfloat16*)nullptr) : f((float*)nullptr);
+}
+template <typename F>
+cudaError_t by_lanes(int n, F&& f) {
+    switch (lanes_of(n)) {
+        case 1: return f(Int<1>());
+        case 2: return f(Int<2>());
+        case 4: return f(Int<4>());
+        default: return f(Int<8>());
+    }
+}
+template <typename F>
+cudaError_t by_back_lanes(int n, F&& f) {
+    switch (back_lanes_of(n)) {
+        case 2: return f(Int<2>());
+        case 4: return f(Int<4>());
+        case 8: return f(Int<8>());
+        default: return f(Int<16>());
+    }
+}
+
+template <int PASS>
+cudaError_t run_scan(const ScanArgs& a, const Cut& cut, const Maps& maps, int32_t* status,
+                     cudaStream_t stream) {
+    const int64_t D = (int64_t)a.H * a.d;
+    return by_type(a.dtype, [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        constexpr int V = 16 / sizeof(T);
+        const bool wide =
+            a.d % V == 0 && rows_fit(a.in.dt, a.in.lddt, D, sizeof(T), V) &&
+            (PASS == kGradMaps || rows_fit(a.in.x, a.in.ldx, D, sizeof(T), V)) &&
+            (PASS == kMaps || !a.in.z || rows_fit(a.in.z, a.in.ldz, D, sizeof(T), V));
+        return by_lanes(a.n, [&](auto l) {
+            constexpr int L = decltype(l)::value;
+            const int64_t most = (int64_t)1 << 30;
+            const unsigned grid = (unsigned)(cut.items < 1 ? 1 : cut.items < most ? cut.items : most);
+            auto kernel = wide ? scan_kernel<T, L, V, PASS> : scan_kernel<T, L, 1, PASS>;
+            kernel<<<grid, kThreads, 0, stream>>>(a, cut, maps, status);
+            return cudaGetLastError();
+        });
+    });
+}
+
+cudaError_t run_join(const ScanArgs& a, const Cut& cut, const Maps& maps, bool reversed,
+                     const int32_t* status, cudaStream_t stream) {
+    const int64_t D = (int64_t)a.H * a.d;
+    join_kernel<<<(unsigned)((D * a.n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
+        a, cut, maps, reversed, status);
+    return cudaGetLastError();
+}
+
+cudaError_t run_empty(const ScanArgs& a, const float* in, float* out, const int32_t* status,
+                      cudaStream_t stream) {
+    if (a.num_seqs == 0 || !out) return cudaSuccess;
+    const int64_t row = (int64_t)a.H * a.d * a.n;
+    empty_kernel<<<(unsigned)(a.num_seqs < 1024 ? a.num_seqs : 1024), kThreads, 0, stream>>>(
+        a.cu_seqlens, a.num_seqs, row, in, out, status);
+    return cudaGetLastError();
+}
+
+// The forward scan in a workspace of forward_bytes behind the status word.
+size_t forward_bytes(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
+    const Cut c = forward_cut(N, T, H, d, n);
+    const int64_t D = (int64_t)H * d;
+    return maps_bytes(c, D, n) + (c.seg ? pad((size_t)N * D * n * 4) : 0);
+}
+cudaError_t run_forward(const ScanArgs& args, char* ws, int32_t* status, cudaStream_t stream) {
+    ScanArgs a = args;
+    const Cut cut = forward_cut(a.num_seqs, a.total_tokens, a.H, a.d, a.n);
+    const int64_t D = (int64_t)a.H * a.d;
+    const Maps maps = place_maps(cut, D, a.n, ws);
+    if (cut.seg) {
+        if (a.S0 && a.S0 == a.S_T) {   // in place: segments read S0 while others write S_T
+            float* copy = reinterpret_cast<float*>(ws + maps_bytes(cut, D, a.n));
+            const cudaError_t err = cudaMemcpyAsync(copy, a.S0, (size_t)a.num_seqs * D * a.n * 4,
+                                                    cudaMemcpyDeviceToDevice, stream);
+            if (err != cudaSuccess) return err;
+            a.S0 = copy;
+        }
+        cudaError_t err = run_scan<kMaps>(a, cut, maps, status, stream);
+        if (err == cudaSuccess) err = run_join(a, cut, maps, false, status, stream);
+        if (err == cudaSuccess) err = run_empty(a, a.S0, a.S_T, status, stream);
+        if (err != cudaSuccess) return err;
+    }
+    return run_scan<kOutputs>(a, cut, maps, status, stream);
+}
+
+struct BackLayout {
+    size_t maps, part_A, part_c, part_BC, states, forward, end;
+};
+BackLayout back_layout(const Cut& cut, int32_t N, int64_t T, int32_t H, int32_t d, int32_t n,
+                       bool with_states) {
+    BackLayout L;
+    const size_t D = (size_t)H * d;
+    size_t at = kHead;
+    L.maps = at;
+    at += maps_bytes(cut, D, n);
+    L.part_A = at;
+    at += pad((size_t)cut.nseg * D * n * 4);
+    L.part_c = at;
+    at += pad((size_t)cut.nseg * 2 * D * 4);
+    L.part_BC = at;
+    if (cut.per_group > 1) at += pad((size_t)cut.per_group * T * H * 2 * n * 4);
+    L.states = at;
+    if (!with_states) at += pad((size_t)(T + SELSCAN_CHUNK - 1) / SELSCAN_CHUNK * D * n * 4);
+    L.forward = at;
+    if (!with_states) at += forward_bytes(N, T, H, d, n);
+    L.end = at;
+    return L;
+}
+
+}  // namespace
+
+size_t scan_prefill_bytes(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
+    return kHead + forward_bytes(N, T, H, d, n);
+}
+size_t scan_backward_bytes(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n,
+                           bool with_states) {
+    return back_layout(backward_cut(N, T, H, d, n), N, T, H, d, n, with_states).end;
+}
+
+cudaError_t launch_scan_prefill(const ScanArgs& a, char* ws, cudaStream_t stream) {
+    int32_t* status = reinterpret_cast<int32_t*>(ws);
+    const cudaError_t err = launch_offsets_check(a.cu_seqlens, a.num_seqs, a.total_tokens, status,
+                                                 stream);
+    if (err != cudaSuccess) return err;
+    return run_forward(a, ws + kHead, status, stream);
+}
+
+cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t stream) {
+    ScanArgs a = args;
+    int32_t* status = reinterpret_cast<int32_t*>(ws);
+    const int64_t D = (int64_t)a.H * a.d;
+    const Cut cut = backward_cut(a.num_seqs, a.total_tokens, a.H, a.d, a.n);
+    const BackLayout L = back_layout(cut, a.num_seqs, a.total_tokens, a.H, a.d, a.n,
+                                     a.states != nullptr);
+    const Maps maps = place_maps(cut, D, a.n, ws + L.maps);
+    float* part_A = reinterpret_cast<float*>(ws + L.part_A);
+    float* part_c = reinterpret_cast<float*>(ws + L.part_c);
+    float* part_BC = reinterpret_cast<float*>(ws + L.part_BC);
+    // (the backward kernels read the outcome, whatever the batch's size)
+    cudaError_t err = launch_offsets_check(a.cu_seqlens, a.num_seqs, a.total_tokens, status, stream,
+                                           true);
+    if (err != cudaSuccess) return err;
+    if (!a.states) {   // the forward scan once more, for the states alone
+        ScanArgs f = a;
+        f.y = nullptr;
+        f.S_T = nullptr;
+        f.states = reinterpret_cast<float*>(ws + L.states);
+        err = run_forward(f, ws + L.forward, status, stream);
+        if (err != cudaSuccess) return err;
+        a.states = f.states;
+    }
+    if (cut.seg) {
+        err = run_scan<kGradMaps>(a, grad_map_cut(cut, a.H, a.d, a.n), maps, status, stream);
+        if (err == cudaSuccess) err = run_join(a, cut, maps, true, status, stream);
+        if (err == cudaSuccess) err = run_empty(a, a.dS_T, a.g.dS0, status, stream);
+        if (err != cudaSuccess) return err;
+    }
+    err = by_type(a.dtype, [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        return by_back_lanes(a.n, [&](auto l) {
+            constexpr int NL = decltype(l)::value;
+            auto kernel = scan_bwd_kernel<T, NL>;
+            constexpr int smem = sizeof(typename Back<NL>::Shared);
+            if (smem > 48 * 1024) {
+                const cudaError_t e = cudaFuncSetAttribute(
+                    kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                if (e != cudaSuccess) return e;
+            }
+            const int64_t most = (int64_t)1 << 30;
+            const unsigned grid = (unsigned)(cut.items < 1 ? 1 : cut.items < most ? cut.items : most);
+            kernel<<<grid, Back<NL>::kThreads, smem, stream>>>(a, cut, maps, part_A, part_c, part_BC,
+                                                               status);
+            return cudaGetLastError();
+        });
+    });
+    if (err != cudaSuccess) return err;
+    if (cut.per_group > 1 && a.total_tokens > 0) {
+        const int64_t n = a.total_tokens * a.H * 2 * a.n, most = 32 * sms();
+        const int64_t blocks = (n + 255) / 256;
+        sum_blocks_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(
+            a, cut.per_group, part_BC, status);
+        err = cudaGetLastError();
+        if (err != cudaSuccess) return err;
+    }
+    err = launch_column_sums(part_A, cut.nseg, D * a.n, 0, a.g.dA, nullptr, status, stream);
+    if (err != cudaSuccess || (!a.g.dskip && !a.g.ddt_bias)) return err;
+    return launch_column_sums(part_c, cut.nseg, D, D, a.g.dskip, a.g.ddt_bias, status, stream);
+}
+
+cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream) {
+    const int64_t D = (int64_t)a.H * a.d;
+    const int ch = kThreads / lanes_of(a.n);
+    const int64_t blocks = (D + ch - 1) / ch;
+    if (a.B * blocks > INT32_MAX) return cudaErrorInvalidValue;
+    return by_type(a.dtype, [&](auto* t) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        return by_lanes(a.n, [&](auto l) {
+            scan_step_kernel<T, decltype(l)::value>
+                <<<(unsigned)(a.B * blocks), kThreads, 0, stream>>>(a, blocks);
+            return cudaGetLastError();
+        });
+    });
+}
+
+}  // namespace kda

@@ -15,7 +15,10 @@ The names follow the C ABI: ``prefill`` / ``prefill_into`` wrap
 Residuals call of ``include/attnres.h``; the ``linrec_*`` functions wrap the
 gated linear recurrence of ``include/linrec.h``, and ``beam_select``,
 ``beam_reorder`` and ``decode_step_parents`` the beam search calls of
-``include/beam.h``.
+``include/beam.h``.  What a layer has around its recurrence: the ``causalconv_*``
+functions wrap the short causal convolution of ``include/causalconv.h``, the
+``selscan_*`` functions the selective scan of ``include/selscan.h`` and the
+``groupnorm_*`` functions the gated group norm of ``include/groupnorm.h``.
 """
 from __future__ import annotations
 
@@ -40,6 +43,16 @@ _GATES = {"channel": (GATE_CHANNEL_F32, torch.float32, 3),
           "log_bf16": (GATE_CHANNEL_LOG_BF16, torch.bfloat16, 3)}
 
 _lib = None
+
+
+class _ScanRows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "dt", "B", "C", "z")] + \
+        [(n, ctypes.c_int64) for n in ("ldx", "lddt", "ldB", "ldC", "ldz")]
+
+
+class _ScanGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("dx", "ddt", "dB", "dC", "dz", "dA", "dD",
+                                               "ddt_bias", "dS0")]
 
 
 class KdaError(RuntimeError):
@@ -133,6 +146,41 @@ def load(path: str | None = None):
     lib.kda_decode_step_parents.restype = ctypes.c_int
     lib.kda_decode_step_parents.argtypes = [vp, vp, vp, vp, ctypes.c_int, vp, vp, i32, vp, vp,
                                             i32, i32, i32, i32, ctypes.c_int, vp, vp]
+    flt, rows = ctypes.c_float, ctypes.POINTER(_ScanRows)
+    lib.causalconv_prefill_workspace_size.restype = sz
+    lib.causalconv_prefill_workspace_size.argtypes = [i32, i64, i32, i32, ctypes.c_int]
+    lib.causalconv_prefill.restype = ctypes.c_int
+    lib.causalconv_prefill.argtypes = [vp, i64, vp, vp, vp, vp, i32, i64, i32, i32, ctypes.c_int,
+                                       ctypes.c_int, vp, vp, vp, sz, vp]
+    lib.causalconv_backward_workspace_size.restype = sz
+    lib.causalconv_backward_workspace_size.argtypes = [i32, i64, i32, i32]
+    lib.causalconv_backward.restype = ctypes.c_int
+    lib.causalconv_backward.argtypes = [vp, i64, vp, vp, vp, vp, i32, i64, i32, i32, ctypes.c_int,
+                                        ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.causalconv_decode_step.restype = ctypes.c_int
+    lib.causalconv_decode_step.argtypes = [vp, i64, vp, vp, vp, i32, vp, i32, i32, i32,
+                                           ctypes.c_int, ctypes.c_int, vp, vp, vp]
+    lib.selscan_prefill_workspace_size.restype = sz
+    lib.selscan_prefill_workspace_size.argtypes = [i32, i64, i32, i32, i32]
+    scan_args = [rows, vp, vp, vp, vp, vp, i32, i64, i32, i32, i32, ctypes.c_int, ctypes.c_int]
+    lib.selscan_prefill.restype = ctypes.c_int
+    lib.selscan_prefill.argtypes = scan_args + [vp, vp, vp, vp, sz, vp]
+    lib.selscan_backward_workspace_size.restype = sz
+    lib.selscan_backward_workspace_size.argtypes = [i32, i64, i32, i32, i32, i32]
+    lib.selscan_backward.restype = ctypes.c_int
+    lib.selscan_backward.argtypes = scan_args + [vp, vp, vp, ctypes.POINTER(_ScanGrads), vp, sz,
+                                                 vp]
+    lib.selscan_decode_step.restype = ctypes.c_int
+    lib.selscan_decode_step.argtypes = [rows, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32,
+                                        ctypes.c_int, ctypes.c_int, vp, vp, vp]
+    norm_args = [vp, i64, vp, vp, i32, vp, i64, i64, i32, i32, ctypes.c_int, ctypes.c_int,
+                 ctypes.c_int, flt]
+    lib.groupnorm_forward.restype = ctypes.c_int
+    lib.groupnorm_forward.argtypes = norm_args + [vp, vp]
+    lib.groupnorm_backward_workspace_size.restype = sz
+    lib.groupnorm_backward_workspace_size.argtypes = [i64, i32, i32]
+    lib.groupnorm_backward.restype = ctypes.c_int
+    lib.groupnorm_backward.argtypes = norm_args + [vp, vp, vp, vp, vp, vp, sz, vp]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_version.restype = i32
@@ -930,3 +978,556 @@ def beam_reorder(states, parents, beams: int, *, stream=None) -> None:
                              raw)
     if st != OK:
         raise KdaError(st, "beam_reorder")
+
+
+# ---- around a layer's recurrence: the short causal convolution (include/causalconv.h), the
+# ---- selective scan (include/selscan.h) and the gated group norm (include/groupnorm.h)
+
+SELSCAN_CHUNK = 16
+_ACTIVATIONS = {"none": 0, "silu": 1, "sigmoid": 2}
+
+
+def _storage(x) -> int:
+    code = _DTYPE_CODES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"the storage dtype must be bfloat16 or float32, got {x.dtype}")
+    return code
+
+
+def _row_stride(what: str, t) -> int:
+    """Distance in elements between the rows of t, each of which must be dense."""
+    if t.is_contiguous():
+        return t.numel() // t.shape[0] if t.shape[0] else _width(t)
+    width = 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and step != width:
+            raise ValueError(f"each row of {what} must be contiguous")
+        width *= size
+    if t.shape[0] < 2:
+        return width
+    if t.stride(0) < width:
+        raise ValueError(f"the rows of {what} must not overlap")
+    return t.stride(0)
+
+
+def _width(t) -> int:
+    n = 1
+    for size in t.shape[1:]:
+        n *= size
+    return n
+
+
+def _place_rows(stream, rows, *ts) -> int:
+    """``_place`` for `ts`; `rows` may be strided but must be on the same device."""
+    dev = rows[0].get_device()
+    for t in rows:
+        if t is not None and (t.get_device() != dev or dev < 0):
+            raise ValueError("all tensors must be CUDA tensors on one device")
+    for t in ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous CUDA tensors on one device")
+    return _stream_on(dev, stream)
+
+
+def _conv_args(x, w, b):
+    """(channels' shape, D, W, dtype code) of x [rows, ...] and its filter."""
+    code = _storage(x)
+    ch = x.shape[1:]
+    if x.dim() < 2 or w.dim() != x.dim():
+        raise ValueError(f"x must be [T, ...] and w [..., W], got {tuple(x.shape)} and "
+                         f"{tuple(w.shape)}")
+    W = w.shape[-1]
+    _check("w", w, torch.float32, (*ch, W))
+    if b is not None:
+        _check("b", b, torch.float32, ch)
+    return ch, _width(x), W, code
+
+
+def _conv_inputs(x, w, b, S0, cu_seqlens):
+    ch, D, W, code = _conv_args(x, w, b)
+    N = cu_seqlens.numel() - 1
+    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
+    if S0 is not None:
+        _check("S0", S0, x.dtype, (N, W - 1, *ch))
+    return ch, D, W, code, N
+
+
+def causalconv_workspace_size(num_seqs: int, total_tokens: int, D: int, W: int,
+                              dtype=torch.bfloat16) -> int:
+    """causalconv_prefill_workspace_size: bytes of workspace (0: size not supported)."""
+    return load().causalconv_prefill_workspace_size(num_seqs, total_tokens, D, W,
+                                                    _DTYPE_CODES[dtype])
+
+
+def causalconv_prefill_into(x, w, b, S0, cu_seqlens, y, S_T, workspace, *, silu: bool = True,
+                            stream=None) -> None:
+    """Enqueue causalconv_prefill into preallocated outputs: the depthwise filter over each
+    channel's last W inputs, then silu.
+
+    x: [T, ...] (bf16 or fp32; any channel shape; rows may be strided: a slice of a wider
+    projection); w: [..., W] fp32, the token itself last, 2 <= W <= 4; b: [...] fp32 or None;
+    S0: [N, W-1, ...] like x or None, the inputs before each sequence; cu_seqlens: int32
+    [N+1] on the device; y: like x; S_T: like S0 (may be S0); workspace: uint8, at least
+    ``causalconv_workspace_size`` bytes."""
+    ch, D, W, code, N = _conv_inputs(x, w, b, S0, cu_seqlens)
+    _check("y", y, x.dtype, x.shape)
+    _check("S_T", S_T, x.dtype, (N, W - 1, *ch))
+    ld = _row_stride("x", x)
+    raw = _place_rows(stream, (x,), w, b, S0, cu_seqlens, y, S_T, workspace)
+    st = load().causalconv_prefill(_p(x), ld, _p(w), _p(b), _p(S0), _p(cu_seqlens), N, x.shape[0],
+                                   D, W, code, int(silu), _p(y), _p(S_T), _p(workspace),
+                                   workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "causalconv_prefill")
+
+
+def causalconv_prefill(x, w, b, S0, cu_seqlens, *, silu: bool = True, stream=None,
+                       check_device_status: bool = False):
+    """Allocate outputs with PyTorch and run causalconv_prefill; returns (y, S_T).  y of
+    tokens past cu_seqlens[-1] is not written."""
+    ch, D, W, code, N = _conv_inputs(x, w, b, S0, cu_seqlens)
+    ld = _row_stride("x", x)
+    raw = _place_rows(stream, (x,), w, b, S0, cu_seqlens)
+    lib, dev, T = load(), x.device, x.shape[0]
+    nbytes = lib.causalconv_prefill_workspace_size(N, T, D, W, code)
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED, "causalconv_prefill")
+    y = _empty(stream, x.shape, x.dtype, dev)
+    S_T = _empty(stream, (N, W - 1, *ch), x.dtype, dev)
+    ws = _empty(stream, nbytes, torch.uint8, dev)
+    st = lib.causalconv_prefill(x.data_ptr(), ld, w.data_ptr(), _p(b), _p(S0),
+                                cu_seqlens.data_ptr(), N, T, D, W, code, int(silu), y.data_ptr(),
+                                S_T.data_ptr(), ws.data_ptr(), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "causalconv_prefill")
+    if check_device_status:
+        device_status(ws, stream=stream)
+    return y, S_T
+
+
+def causalconv_backward_workspace_size(num_seqs: int, total_tokens: int, D: int, W: int) -> int:
+    """causalconv_backward_workspace_size: bytes of workspace (0: size not supported)."""
+    return load().causalconv_backward_workspace_size(num_seqs, total_tokens, D, W)
+
+
+def _conv_cotangents(x, dy, dS_T, N, W, ch):
+    _check("dy", dy, x.dtype, x.shape)
+    if dS_T is not None:
+        _check("dS_T", dS_T, torch.float32, (N, W - 1, *ch))
+
+
+def causalconv_backward_into(x, w, b, S0, cu_seqlens, dy, dS_T, grads, workspace, *,
+                             silu: bool = True, stream=None) -> None:
+    """Enqueue causalconv_backward into preallocated fp32 gradients.
+
+    Inputs as ``causalconv_prefill_into``; dy: like x; dS_T: [N, W-1, ...] fp32 or None;
+    grads: dict with "dx" [T, ...], "dw" [..., W] and optionally "db" [...] and "dS0"
+    [N, W-1, ...]; workspace: uint8, at least ``causalconv_backward_workspace_size`` bytes."""
+    ch, D, W, code, N = _conv_inputs(x, w, b, S0, cu_seqlens)
+    dx, dw, db, dS0 = grads["dx"], grads["dw"], grads.get("db"), grads.get("dS0")
+    _conv_cotangents(x, dy, dS_T, N, W, ch)
+    _check("dx", dx, torch.float32, x.shape)
+    _check("dw", dw, torch.float32, w.shape)
+    if db is not None:
+        _check("db", db, torch.float32, ch)
+    if dS0 is not None:
+        _check("dS0", dS0, torch.float32, (N, W - 1, *ch))
+    ld = _row_stride("x", x)
+    raw = _place_rows(stream, (x,), w, b, S0, cu_seqlens, dy, dS_T, dx, dw, db, dS0, workspace)
+    st = load().causalconv_backward(_p(x), ld, _p(w), _p(b), _p(S0), _p(cu_seqlens), N,
+                                    x.shape[0], D, W, code, int(silu), _p(dy), _p(dS_T), _p(dx),
+                                    _p(dw), _p(db), _p(dS0), _p(workspace),
+                                    workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "causalconv_backward")
+
+
+def causalconv_backward(x, w, b, S0, cu_seqlens, dy, dS_T=None, *, silu: bool = True, stream=None,
+                        check_device_status: bool = False):
+    """Allocate fp32 gradients with PyTorch and run causalconv_backward; returns a dict with
+    dx, dw, dS0 and, with a bias, db.  Rows of tokens past cu_seqlens[-1] are not written."""
+    ch, D, W, code, N = _conv_inputs(x, w, b, S0, cu_seqlens)
+    _conv_cotangents(x, dy, dS_T, N, W, ch)
+    ld = _row_stride("x", x)
+    raw = _place_rows(stream, (x,), w, b, S0, cu_seqlens, dy, dS_T)
+    lib, dev, T = load(), x.device, x.shape[0]
+    nbytes = lib.causalconv_backward_workspace_size(N, T, D, W)
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED, "causalconv_backward")
+    grads = {"dx": _empty(stream, x.shape, torch.float32, dev),
+             "dw": _empty(stream, w.shape, torch.float32, dev),
+             "dS0": _empty(stream, (N, W - 1, *ch), torch.float32, dev)}
+    if b is not None:
+        grads["db"] = _empty(stream, ch, torch.float32, dev)
+    ws = _empty(stream, nbytes, torch.uint8, dev)
+    st = lib.causalconv_backward(x.data_ptr(), ld, w.data_ptr(), _p(b), _p(S0),
+                                 cu_seqlens.data_ptr(), N, T, D, W, code, int(silu),
+                                 dy.data_ptr(), _p(dS_T), grads["dx"].data_ptr(),
+                                 grads["dw"].data_ptr(), _p(grads.get("db")),
+                                 grads["dS0"].data_ptr(), ws.data_ptr(), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "causalconv_backward")
+    if check_device_status:
+        device_status(ws, stream=stream)
+    return grads
+
+
+def causalconv_decode_step(x, w, b, S, y=None, *, parents=None, S_out=None, silu: bool = True,
+                           stream=None):
+    """Enqueue causalconv_decode_step: one token for each of B sequences; returns y [B, ...].
+
+    x: [B, ...] (rows may be strided); w, b: as for ``causalconv_prefill_into``; S: like x
+    [B, W-1, ...], the inputs before, moved on in place unless S_out is given.  parents:
+    int32 [B] or None: sequence b continues row parents[b] of S [rows, W-1, ...] (zeros for an
+    entry outside it) and S_out [B, W-1, ...] must be given."""
+    ch, D, W, code = _conv_args(x, w, b)
+    B = x.shape[0]
+    if parents is None:
+        _check("S", S, x.dtype, (B, W - 1, *ch))
+    else:
+        _check("parents", parents, torch.int32, (B,))
+        _check("S", S, x.dtype, (S.shape[0], W - 1, *ch))
+        if S_out is None:
+            raise ValueError("parents need S_out: the states cannot move in place")
+    if S_out is None:
+        S_out = S
+    else:
+        _check("S_out", S_out, x.dtype, (B, W - 1, *ch))
+    ld = _row_stride("x", x)
+    raw = _place_rows(stream, (x,), w, b, S, parents, S_out, y)
+    if y is None:
+        y = _empty(stream, x.shape, x.dtype, x.device)
+    else:
+        _check("y", y, x.dtype, x.shape)
+    st = load().causalconv_decode_step(x.data_ptr(), ld, w.data_ptr(), _p(b), S.data_ptr(),
+                                       S.shape[0], _p(parents), B, D, W, code, int(silu),
+                                       y.data_ptr(), S_out.data_ptr(), raw)
+    if st != OK:
+        raise KdaError(st, "causalconv_decode_step")
+    return y
+
+
+def _scan_args(x, dt, A, B, C, D, z, dt_bias, rows: str):
+    """(H, d, n, dtype code, row descriptor) of the scan's inputs."""
+    code = _storage(x)
+    if x.dim() != 3 or A.dim() != 3:
+        raise ValueError(f"x must be [{rows}, H, d] and A [H, d, n], got {tuple(x.shape)} and "
+                         f"{tuple(A.shape)}")
+    T, H, d = x.shape
+    n = A.shape[2]
+    _check("A", A, torch.float32, (H, d, n))
+    _check("dt", dt, x.dtype, x.shape)
+    _check("B", B, x.dtype, (T, H, n))
+    _check("C", C, x.dtype, (T, H, n))
+    if z is not None:
+        _check("z", z, x.dtype, x.shape)
+    if D is not None:
+        _check("D", D, torch.float32, (H, d))
+    if dt_bias is not None:
+        _check("dt_bias", dt_bias, torch.float32, (H, d))
+    r = _ScanRows(_p(x), _p(dt), _p(B), _p(C), _p(z), _row_stride("x", x), _row_stride("dt", dt),
+                  _row_stride("B", B), _row_stride("C", C),
+                  0 if z is None else _row_stride("z", z))
+    return H, d, n, code, r
+
+
+def _scan_inputs(x, dt, A, B, C, S0, cu_seqlens, D, z, dt_bias):
+    H, d, n, code, r = _scan_args(x, dt, A, B, C, D, z, dt_bias, "T")
+    N = cu_seqlens.numel() - 1
+    _check("cu_seqlens", cu_seqlens, torch.int32, (N + 1,))
+    if S0 is not None:
+        _check("S0", S0, torch.float32, (N, H, d, n))
+    return x.shape[0], N, H, d, n, code, r
+
+
+def selscan_workspace_size(num_seqs: int, total_tokens: int, H: int, d: int, n: int) -> int:
+    """selscan_prefill_workspace_size on the current device: bytes of workspace (0: size not
+    supported)."""
+    return load().selscan_prefill_workspace_size(num_seqs, total_tokens, H, d, n)
+
+
+def _scan_chunks(T: int) -> int:
+    return -(-T // SELSCAN_CHUNK)
+
+
+def selscan_prefill_into(x, dt, A, B, C, S0, cu_seqlens, y, S_T, workspace, *, D=None, z=None,
+                         dt_bias=None, softplus: bool = True, states=None, stream=None) -> None:
+    """Enqueue selscan_prefill into preallocated outputs: h_t = exp(step_t A) h_{t-1} + step_t
+    x_t B_t per channel over n values, y_t = (C_t . h_t + D x_t) silu(z_t), step = softplus(dt
+    + dt_bias) (without `softplus` dt + dt_bias).
+
+    x, dt, z: [T, H, d] (bf16 or fp32; z may be None); B, C: [T, H, n] like x, one for the d
+    channels of a group; all five may have strided rows (slices of a wider projection); A:
+    [H, d, n] fp32; D, dt_bias: [H, d] fp32 or None; S0: [N, H, d, n] fp32 or None; cu_seqlens:
+    int32 [N+1] on the device; y: like x; S_T: like S0 (may be S0); states: [ceil(T /
+    SELSCAN_CHUNK), H, d, n] fp32 or None, kept for ``selscan_backward``; workspace: uint8, at
+    least ``selscan_workspace_size`` bytes."""
+    T, N, H, d, n, code, r = _scan_inputs(x, dt, A, B, C, S0, cu_seqlens, D, z, dt_bias)
+    _check("y", y, x.dtype, x.shape)
+    _check("S_T", S_T, torch.float32, (N, H, d, n))
+    if states is not None:
+        _check("states", states, torch.float32, (_scan_chunks(T), H, d, n))
+    raw = _place_rows(stream, (x, dt, B, C, z), A, D, dt_bias, S0, cu_seqlens, y, S_T, states,
+                      workspace)
+    st = load().selscan_prefill(ctypes.byref(r), _p(A), _p(D), _p(dt_bias), _p(S0),
+                                _p(cu_seqlens), N, T, H, d, n, code, int(softplus), _p(y),
+                                _p(S_T), _p(states), _p(workspace),
+                                workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "selscan_prefill")
+
+
+def selscan_prefill(x, dt, A, B, C, S0, cu_seqlens, *, D=None, z=None, dt_bias=None,
+                    softplus: bool = True, save_states: bool = False, stream=None,
+                    check_device_status: bool = False):
+    """Allocate outputs with PyTorch and run selscan_prefill; returns (y, S_T), or with
+    `save_states` (y, S_T, states) for ``selscan_backward``.  y of tokens past cu_seqlens[-1]
+    is not written."""
+    T, N, H, d, n, code, r = _scan_inputs(x, dt, A, B, C, S0, cu_seqlens, D, z, dt_bias)
+    raw = _place_rows(stream, (x, dt, B, C, z), A, D, dt_bias, S0, cu_seqlens)
+    lib, dev = load(), x.device
+    nbytes = lib.selscan_prefill_workspace_size(N, T, H, d, n)
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED, "selscan_prefill")
+    y = _empty(stream, x.shape, x.dtype, dev)
+    S_T = _empty(stream, (N, H, d, n), torch.float32, dev)
+    states = _empty(stream, (_scan_chunks(T), H, d, n), torch.float32, dev) if save_states \
+        else None
+    ws = _empty(stream, nbytes, torch.uint8, dev)
+    st = lib.selscan_prefill(ctypes.byref(r), A.data_ptr(), _p(D), _p(dt_bias), _p(S0),
+                             cu_seqlens.data_ptr(), N, T, H, d, n, code, int(softplus),
+                             y.data_ptr(), S_T.data_ptr(), _p(states), ws.data_ptr(), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "selscan_prefill")
+    if check_device_status:
+        device_status(ws, stream=stream)
+    return (y, S_T, states) if save_states else (y, S_T)
+
+
+def selscan_backward_workspace_size(num_seqs: int, total_tokens: int, H: int, d: int, n: int, *,
+                                    with_states: bool = True) -> int:
+    """selscan_backward_workspace_size on the current device: bytes of workspace (0: size not
+    supported)."""
+    return load().selscan_backward_workspace_size(num_seqs, total_tokens, H, d, n,
+                                                  int(with_states))
+
+
+def _scan_cotangents(x, dy, dS_T, states, T, N, H, d, n):
+    _check("dy", dy, x.dtype, x.shape)
+    if dS_T is not None:
+        _check("dS_T", dS_T, torch.float32, (N, H, d, n))
+    if states is not None:
+        _check("states", states, torch.float32, (_scan_chunks(T), H, d, n))
+
+
+def _scan_grad_shapes(T, N, H, d, n, z, D, dt_bias):
+    shapes = {"dx": (T, H, d), "ddt": (T, H, d), "dB": (T, H, n), "dC": (T, H, n),
+              "dA": (H, d, n), "dS0": (N, H, d, n)}
+    if z is not None:
+        shapes["dz"] = (T, H, d)
+    if D is not None:
+        shapes["dD"] = (H, d)
+    if dt_bias is not None:
+        shapes["ddt_bias"] = (H, d)
+    return shapes
+
+
+def selscan_backward_into(x, dt, A, B, C, S0, cu_seqlens, dy, dS_T, grads, workspace, *, D=None,
+                          z=None, dt_bias=None, softplus: bool = True, states=None,
+                          stream=None) -> None:
+    """Enqueue selscan_backward into preallocated fp32 gradients.
+
+    Inputs as ``selscan_prefill_into``; dy: like x; dS_T: [N, H, d, n] fp32 or None; states:
+    what selscan_prefill saved, or None (the forward scan runs again); grads: dict with "dx",
+    "ddt" [T, H, d], "dB", "dC" [T, H, n], "dA" [H, d, n], with a gate "dz" [T, H, d], and
+    optionally "dD", "ddt_bias" [H, d] and "dS0" [N, H, d, n]; workspace: uint8, at least
+    ``selscan_backward_workspace_size`` bytes."""
+    T, N, H, d, n, code, r = _scan_inputs(x, dt, A, B, C, S0, cu_seqlens, D, z, dt_bias)
+    _scan_cotangents(x, dy, dS_T, states, T, N, H, d, n)
+    shapes = _scan_grad_shapes(T, N, H, d, n, True, True, True)
+    for name in ("dx", "ddt", "dB", "dC", "dA") + (("dz",) if z is not None else ()):
+        _check(name, grads[name], torch.float32, shapes[name])
+    for name in ("dD", "ddt_bias", "dS0"):
+        if grads.get(name) is not None:
+            _check(name, grads[name], torch.float32, shapes[name])
+    outs = [grads.get(f) if f != "dz" or z is not None else None for f, _ in _ScanGrads._fields_]
+    raw = _place_rows(stream, (x, dt, B, C, z), A, D, dt_bias, S0, cu_seqlens, dy, dS_T, states,
+                      workspace, *outs)
+    g = _ScanGrads(*(_p(t) for t in outs))
+    st = load().selscan_backward(ctypes.byref(r), _p(A), _p(D), _p(dt_bias), _p(S0),
+                                 _p(cu_seqlens), N, T, H, d, n, code, int(softplus), _p(dy),
+                                 _p(dS_T), _p(states), ctypes.byref(g), _p(workspace),
+                                 workspace.numel() * workspace.element_size(), raw)
+    if st != OK:
+        raise KdaError(st, "selscan_backward")
+
+
+def selscan_backward(x, dt, A, B, C, S0, cu_seqlens, dy, dS_T=None, *, D=None, z=None,
+                     dt_bias=None, softplus: bool = True, states=None, stream=None,
+                     check_device_status: bool = False):
+    """Allocate fp32 gradients with PyTorch and run selscan_backward; returns a dict with dx,
+    ddt, dB, dC, dA, dS0 and, for each that is given, dz, dD and ddt_bias.  Rows of tokens past
+    cu_seqlens[-1] are not written."""
+    T, N, H, d, n, code, r = _scan_inputs(x, dt, A, B, C, S0, cu_seqlens, D, z, dt_bias)
+    _scan_cotangents(x, dy, dS_T, states, T, N, H, d, n)
+    raw = _place_rows(stream, (x, dt, B, C, z), A, D, dt_bias, S0, cu_seqlens, dy, dS_T, states)
+    lib, dev = load(), x.device
+    nbytes = lib.selscan_backward_workspace_size(N, T, H, d, n, int(states is not None))
+    if nbytes == 0:
+        raise KdaError(ERR_UNSUPPORTED, "selscan_backward")
+    grads = {name: _empty(stream, shape, torch.float32, dev)
+             for name, shape in _scan_grad_shapes(T, N, H, d, n, z, D, dt_bias).items()}
+    ws = _empty(stream, nbytes, torch.uint8, dev)
+    g = _ScanGrads(*(_p(grads.get(f)) for f, _ in _ScanGrads._fields_))
+    st = lib.selscan_backward(ctypes.byref(r), A.data_ptr(), _p(D), _p(dt_bias), _p(S0),
+                              cu_seqlens.data_ptr(), N, T, H, d, n, code, int(softplus),
+                              dy.data_ptr(), _p(dS_T), _p(states), ctypes.byref(g),
+                              ws.data_ptr(), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "selscan_backward")
+    if check_device_status:
+        device_status(ws, stream=stream)
+    return grads
+
+
+def selscan_decode_step(x, dt, A, B, C, S, y=None, *, D=None, z=None, dt_bias=None,
+                        softplus: bool = True, parents=None, S_out=None, stream=None):
+    """Enqueue selscan_decode_step: one token for each of R sequences; returns y [R, H, d].
+
+    Inputs as ``selscan_prefill_into`` with R in T's place; S: fp32 [R, H, d, n], updated in
+    place unless S_out is given.  parents: int32 [R] or None: sequence b continues row
+    parents[b] of S [rows, H, d, n] (a zero state for an entry outside it) and S_out [R, H, d,
+    n] must be given."""
+    H, d, n, code, r = _scan_args(x, dt, A, B, C, D, z, dt_bias, "R")
+    R = x.shape[0]
+    if parents is None:
+        _check("S", S, torch.float32, (R, H, d, n))
+    else:
+        _check("parents", parents, torch.int32, (R,))
+        _check("S", S, torch.float32, (S.shape[0], H, d, n))
+        if S_out is None:
+            raise ValueError("parents need S_out: the states cannot move in place")
+    if S_out is None:
+        S_out = S
+    else:
+        _check("S_out", S_out, torch.float32, (R, H, d, n))
+    raw = _place_rows(stream, (x, dt, B, C, z), A, D, dt_bias, S, parents, S_out, y)
+    if y is None:
+        y = _empty(stream, x.shape, x.dtype, x.device)
+    else:
+        _check("y", y, x.dtype, x.shape)
+    st = load().selscan_decode_step(ctypes.byref(r), A.data_ptr(), _p(D), _p(dt_bias),
+                                    S.data_ptr(), S.shape[0], _p(parents), R, H, d, n, code,
+                                    int(softplus), y.data_ptr(), S_out.data_ptr(), raw)
+    if st != OK:
+        raise KdaError(st, "selscan_decode_step")
+    return y
+
+
+def _norm_args(x, w, b, z, act: str):
+    """(T, H, d, heads of the parameters, dtype code, activation) of the norm's inputs."""
+    code = _storage(x)
+    if x.dim() != 3:
+        raise ValueError(f"x must be [T, H, d], got {tuple(x.shape)}")
+    T, H, d = x.shape
+    if act not in _ACTIVATIONS:
+        raise ValueError(f"the activation must be one of {sorted(_ACTIVATIONS)}, got {act!r}")
+    heads = 1
+    for what, t in (("w", w), ("b", b)):
+        if t is None:
+            continue
+        if t.dim() not in (1, 2):
+            raise ValueError(f"{what} must be [d] or [H, d], got {tuple(t.shape)}")
+        _check(what, t, torch.float32, (H, d) if t.dim() == 2 else (d,))
+    if w is not None and b is not None and w.dim() != b.dim():
+        raise ValueError("w and b must have one shape")
+    for t in (w, b):
+        if t is not None and t.dim() == 2:
+            heads = H
+    if z is not None:
+        _check("z", z, x.dtype, x.shape)
+    return T, H, d, heads, code, _ACTIVATIONS[act]
+
+
+def groupnorm_forward(x, w=None, b=None, y=None, *, z=None, act: str = "silu", eps: float = 1e-5,
+                      center: bool = False, stream=None):
+    """Enqueue groupnorm_forward: the norm of each head's d channels, then its gate; returns y.
+
+    x: [T, H, d] (bf16 or fp32); w, b: [d] or [H, d] fp32 or None; z: the gate like x or None;
+    rows of x and z may be strided.  y = v act(z) with a gate and act(v) without, v = w (x - m)
+    / sqrt(mean((x - m)^2) + eps) + b, m the mean with `center` and else 0; act "silu",
+    "sigmoid" or "none".  y: like x, allocated when not given (may be x, or z)."""
+    T, H, d, heads, code, acode = _norm_args(x, w, b, z, act)
+    ldx, ldz = _row_stride("x", x), 0 if z is None else _row_stride("z", z)
+    raw = _place_rows(stream, (x, z), w, b, y)
+    if y is None:
+        y = _empty(stream, x.shape, x.dtype, x.device)
+    else:
+        _check("y", y, x.dtype, x.shape)
+    st = load().groupnorm_forward(x.data_ptr(), ldx, _p(w), _p(b), heads, _p(z), ldz, T, H, d,
+                                  code, int(center), acode, eps, y.data_ptr(), raw)
+    if st != OK:
+        raise KdaError(st, "groupnorm_forward")
+    return y
+
+
+def groupnorm_backward_workspace_size(T: int, H: int, d: int) -> int:
+    """groupnorm_backward_workspace_size: bytes of workspace (0: size not supported)."""
+    return load().groupnorm_backward_workspace_size(T, H, d)
+
+
+def groupnorm_backward_into(x, w, b, dy, grads, workspace, *, z=None, act: str = "silu",
+                            eps: float = 1e-5, center: bool = False, stream=None) -> None:
+    """Enqueue groupnorm_backward into preallocated fp32 gradients.
+
+    Inputs as ``groupnorm_forward``; dy: like x; grads: dict with "dx" [T, H, d] and optionally
+    "dz" (with a gate), "dw" and "db" ([d], or [H, d] when w or b are); workspace: uint8, at
+    least ``groupnorm_backward_workspace_size`` bytes (may be None without dw and db)."""
+    T, H, d, heads, code, acode = _norm_args(x, w, b, z, act)
+    _check("dy", dy, x.dtype, x.shape)
+    dx, dz, dw, db = grads["dx"], grads.get("dz"), grads.get("dw"), grads.get("db")
+    _check("dx", dx, torch.float32, x.shape)
+    if dz is not None:
+        _check("dz", dz, torch.float32, x.shape)
+    for what, t in (("dw", dw), ("db", db)):
+        if t is not None:
+            _check(what, t, torch.float32, (H, d) if heads > 1 else (d,) if t.dim() == 1 else (1, d))
+    ldx, ldz = _row_stride("x", x), 0 if z is None else _row_stride("z", z)
+    raw = _place_rows(stream, (x, z), w, b, dy, dx, dz, dw, db, workspace)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    st = load().groupnorm_backward(_p(x), ldx, _p(w), _p(b), heads, _p(z), ldz, T, H, d, code,
+                                   int(center), acode, eps, _p(dy), _p(dx), _p(dz), _p(dw),
+                                   _p(db), _p(workspace), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "groupnorm_backward")
+
+
+def groupnorm_backward(x, w, b, dy, *, z=None, act: str = "silu", eps: float = 1e-5,
+                       center: bool = False, stream=None):
+    """Allocate fp32 gradients with PyTorch and run groupnorm_backward; returns a dict with dx
+    and, for each that is given, dz, dw and db."""
+    T, H, d, heads, code, acode = _norm_args(x, w, b, z, act)
+    _check("dy", dy, x.dtype, x.shape)
+    ldx, ldz = _row_stride("x", x), 0 if z is None else _row_stride("z", z)
+    raw = _place_rows(stream, (x, z), w, b, dy)
+    lib, dev = load(), x.device
+    grads = {"dx": _empty(stream, x.shape, torch.float32, dev)}
+    if z is not None:
+        grads["dz"] = _empty(stream, x.shape, torch.float32, dev)
+    ws, nbytes = None, 0
+    if w is not None or b is not None:
+        nbytes = lib.groupnorm_backward_workspace_size(T, H, d)
+        if nbytes == 0:
+            raise KdaError(ERR_UNSUPPORTED, "groupnorm_backward")
+        ws = _empty(stream, nbytes, torch.uint8, dev)
+        if w is not None:
+            grads["dw"] = _empty(stream, w.shape, torch.float32, dev)
+        if b is not None:
+            grads["db"] = _empty(stream, b.shape, torch.float32, dev)
+    st = lib.groupnorm_backward(_p(x), ldx, _p(w), _p(b), heads, _p(z), ldz, T, H, d, code,
+                                int(center), acode, eps, _p(dy), _p(grads["dx"]),
+                                _p(grads.get("dz")), _p(grads.get("dw")), _p(grads.get("db")),
+                                _p(ws), nbytes, raw)
+    if st != OK:
+        raise KdaError(st, "groupnorm_backward")
+    return grads
