@@ -28,12 +28,12 @@
 namespace kda {
 namespace {
 
-constexpr int kThreads = 128;   // forward
-constexpr int kTile = 32;       // tokens of a forward tile; segments are whole tiles
+constexpr int kThreads = 128;   // of the small kernels
+constexpr int kTile = SELSCAN_CHUNK;   // tokens of a forward tile; segments are whole tiles
 constexpr int kNs = 8;          // state values a lane, forward
 constexpr int kBack = SELSCAN_CHUNK;   // tokens of a backward tile
 constexpr int kSub = 8;         // tokens whose states lie in registers, backward
-static_assert(kTile % SELSCAN_CHUNK == 0 && kBack == 2 * kSub, "tiles hold whole chunks");
+static_assert(kTile == SELSCAN_CHUNK && kBack == 2 * kSub, "tiles hold whole chunks");
 
 // Two floats for the packed instructions.
 using F2 = unsigned long long;
@@ -68,35 +68,35 @@ __device__ __forceinline__ float sum2(F2 a) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// Decays 2^(D A log2 e) as 2^(.. + s) 2^-s: the special-function unit cuts its argument off after
-// 24 fractional bits, which by itself leaves decays near 1, of which a state multiplies hundreds,
-// too small on average; s moves the argument to where the multiply-add has rounded it to those
-// bits already.  s is one of the values whose 2^-s is a float to 1e-12, so a rate of 0 gives
-// exactly 1.
-constexpr float kShift = 0x1.8ca934p-1f, kUnshift = 0x1.2b4368p-1f;
+// Decays 2^(D A log2 e).  The special-function unit cuts its argument off after 24 fractional
+// bits, which by itself leaves decays near 1, of which a state multiplies hundreds, 1e-8 to
+// 2.5e-8 too small on average; three quarters of half its last bit, added in the multiply-add
+// that forms the argument, leave 1e-8 at most either way (measured over steps of 1e-6 to 0.5).  A
+// rate of 0 still gives exactly 1: the addend itself is cut off.
+constexpr float kNudge = 0x1.8p-26f;
+__device__ __forceinline__ float decay(float step, float rate) {
+    return ex2(fmaf(step, rate, kNudge));
+}
 __device__ __forceinline__ F2 decay2(F2 step, F2 rate) {
-    const float2 v = unpack2(fma2(step, rate, pack2(kShift, kShift)));
-    return mul2(pack2(ex2(v.x), ex2(v.y)), pack2(kUnshift, kUnshift));
+    const float2 v = unpack2(fma2(step, rate, pack2(kNudge, kNudge)));
+    return pack2(ex2(v.x), ex2(v.y));
 }
 
-// ln(1 + e^v) = max(v, 0) + ln(1 + e), e = e^-|v|, with ln(1 + e) = 2 artanh(e / (2 + e)) by its
-// series (the argument is at most 1/3: seven terms leave 1e-8 of the value), so that small
-// steps keep their relative precision.
-__device__ __forceinline__ float softplus(float v) {
-    const float a = fabsf(v), t = a * kLog2e;
-    // what the product's rounding left out of the exponent
-    const float rest = a < 80.f ? fmaf(a, kLog2e, -t) : 0.f;
-    float e = ex2(-t);
-    e = fmaf(e, -kLn2 * rest, e);
-    const float s = __fdividef(e, 2.f + e), q = s * s;
-    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaf(2.f * s, p, fmaxf(v, 0.f));
+// ln(1 + e^v) = max(v, 0) + ln(1 + e), e = e^-|v|: ln(1 + e) / e on [0, 1] by a polynomial fitted
+// for the least relative error (3e-8), so that small steps keep their relative precision.
+constexpr int kLogTerms = 9;
+__device__ __constant__ const float kLog1p[kLogTerms] = {
+    9.999999404e-01f, -4.999949336e-01f, 3.331909776e-01f, -2.484298050e-01f, 1.910600215e-01f,
+    -1.366323531e-01f, 7.822583616e-02f, -2.950516902e-02f, 5.232676864e-03f};
+__device__ __forceinline__ F2 softplus2(F2 v) {
+    const float2 u = unpack2(v);
+    const F2 e = pack2(ex2(-fabsf(u.x) * kLog2e), ex2(-fabsf(u.y) * kLog2e));
+    F2 q = pack2(kLog1p[kLogTerms - 1], kLog1p[kLogTerms - 1]);
+#pragma unroll
+    for (int i = kLogTerms - 2; i >= 0; --i) q = fma2(q, e, pack2(kLog1p[i], kLog1p[i]));
+    return fma2(q, e, pack2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
 }
+__device__ __forceinline__ float softplus(float v) { return unpack2(softplus2(pack2(v, 0.f))).x; }
 
 // How the work is cut: segments along the tokens (whole sequences when seg == 0) and blocks of
 // channels, none of which spans two groups.
@@ -156,29 +156,62 @@ __device__ __forceinline__ void store8(float* p, int k, int n, const F2 (&h)[kNs
 // maps of the gradients' recurrence (on reversed tokens).
 enum { kOutputs = 0, kMaps = 1, kGradMaps = 2 };
 
+// L lanes share two neighbouring channels, 8 values of each a lane.
 template <int L>
-struct FwdShared {
-    static constexpr int kCh = kThreads / L;
-    float2 du[kTile][kCh];        // step size and what drives the state; then, in y, the output
-    float B[kTile][kNs * L], C[kTile][kNs * L];
+struct Fwd {
+    static constexpr int kWarps = L == 1 ? 1 : L == 2 ? 2 : 4;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kCh = kThreads / L * 2;
+    static constexpr int kNp = kNs * L;
+    // Step size and what drives the state, of a pair of channels side by side: (D, u) of one, (D,
+    // u) of the other.  Where a thread writes V channels at once, the pairs of a row lie in the
+    // order of the threads (pair_slot), so that neither side meets bank conflicts.  An output
+    // takes the place of its u.
+    struct Buffer {
+        float4 du[kTile][kCh / 2];
+        float B[kTile][kNp], C[kTile][kNp];
+    };
+};
+// Where the pair of channel c (even) lies in a row of CH channels written V at a time.
+template <int CH, int V>
+__device__ __forceinline__ int pair_slot(int c) {
+    return V == 1 ? c / 2 : c % V / 2 * (CH / V) + c / V;
+}
+template <int CH, int V>
+__device__ __forceinline__ int slot_channel(int s) {
+    return V == 1 ? s * 2 : s % (CH / V) * V + s / (CH / V) * 2;
+}
+
+// One tile: tokens [a, a + cnt) of sequence n, whose first token is `start`; whether the walk
+// goes on behind it, and whether the sequence ends with it.
+struct Tile {
+    int64_t a, start;
+    int32_t cnt, n;
+    bool ends;
 };
 
 template <typename T, int L, int V, int PASS>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(Fwd<L>::kThreads)
 scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
-    using S = FwdShared<L>;
-    constexpr int CH = S::kCh, NP = kNs * L;
-    constexpr int VR = CH / V;                                     // vectors of a row
-    constexpr int NI = (kTile * VR + kThreads - 1) / kThreads;     // of a tile, a thread
-    __shared__ S s;
+    using G = Fwd<L>;
+    constexpr int CH = G::kCh, NP = G::kNp, TH = G::kThreads;
+    constexpr int VR = CH / V;                          // vectors of a row
+    constexpr int NI = (kTile * VR + TH - 1) / TH;      // of a tile, a thread
+    constexpr int VB = 16 / sizeof(T);                  // values of B and C at once
+    constexpr int NB = (2 * kTile * NP / VB + TH - 1) / TH;
+    static_assert(V == 1 || TH % VR == 0, "a thread keeps its channels");
+    __shared__ __align__(16) typename G::Buffer buf[2];
     const int32_t* cu = p.cu_seqlens;
     if (!offsets_ok(cu, p.num_seqs, p.total_tokens, status)) return;
-    const int tid = threadIdx.x, cl = tid / L, li = tid % L;
+    const int tid = threadIdx.x, li = tid % L, slot = tid / L;
+    const int cp = slot_channel<CH, V>(slot);           // my two channels
     const int64_t D = (int64_t)p.H * p.d, last = cu[p.num_seqs];
     const T* const X = static_cast<const T*>(PASS == kGradMaps ? p.dy : p.in.x);
     const int64_t ldx = PASS == kGradMaps ? D : p.in.ldx;
     const T* const DT = static_cast<const T*>(p.in.dt);
-    const T* const Z = static_cast<const T*>(p.in.z);
+    const T* const Z = static_cast<const T*>(PASS == kMaps ? nullptr : p.in.z);
+    const bool packed = p.n % VB == 0 && p.in.ldB % VB == 0 && p.in.ldC % VB == 0 &&
+                        ((uint64_t)p.in.B | (uint64_t)p.in.C) % 16 == 0;
 
     for (int64_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
         const int64_t blocks = (int64_t)cut.per_group * p.H;
@@ -188,10 +221,8 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         const int32_t c0 = (cb - g * cut.per_group) * CH;          // first channel in the group
         const int32_t width = p.d - c0 < CH ? p.d - c0 : CH;
         const int64_t base = (int64_t)g * p.d + c0;                // and of all
-        const bool on = cl < width;
-        const int64_t state_at = (base + cl) * p.n;
 
-        int64_t t0, t1;   // tokens to walk, the sequence of the next one, and its end
+        int64_t t0, t1;   // tokens to walk
         int32_t n;
         bool reset = false;
         if (cut.seg == 0) {
@@ -215,193 +246,321 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             }
         }
 
-        F2 A[kNs / 2], h[kNs / 2];
-        {
-            float v[kNs];
-            load8(on ? p.A + state_at : nullptr, li * kNs, p.n, v);
+        F2 A[2][kNs / 2], h[2][kNs / 2];
+        auto row_of_state = [&](int q) { return (base + cp + q) * p.n; };
+        auto load_state = [&](const float* from, F2 (&to)[2][kNs / 2]) {
 #pragma unroll
-            for (int i = 0; i < kNs / 2; ++i) A[i] = pack2(v[2 * i] * kLog2e, v[2 * i + 1] * kLog2e);
-        }
-        auto set_state = [&](const float* from) {
-            float v[kNs];
-            load8(on && from ? from + state_at : nullptr, li * kNs, p.n, v);
+            for (int q = 0; q < 2; ++q) {
+                float v[kNs];
+                load8(from && cp + q < width ? from + row_of_state(q) : nullptr, li * kNs, p.n, v);
 #pragma unroll
-            for (int i = 0; i < kNs / 2; ++i) h[i] = pack2(v[2 * i], v[2 * i + 1]);
+                for (int i = 0; i < kNs / 2; ++i) to[q][i] = pack2(v[2 * i], v[2 * i + 1]);
+            }
         };
+        auto store_state = [&](float* to) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (cp + q < width) store8(to + row_of_state(q), li * kNs, p.n, h[q]);
+        };
+        auto first_state = [&](int32_t m) { load_state(p.S0 ? p.S0 + m * D * p.n : nullptr, h); };
+        load_state(p.A, A);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < kNs / 2; ++i) A[q][i] = mul2(A[q][i], pack2(kLog2e, kLog2e));
         if (PASS == kGradMaps)
-            set_state(reset && p.dS_T ? p.dS_T + n * D * p.n : nullptr);
+            load_state(reset && p.dS_T ? p.dS_T + n * D * p.n : nullptr, h);
         else if (t0 == cu[n])
-            set_state(p.S0 ? p.S0 + n * D * p.n : nullptr);
+            first_state(n);
         else
-            set_state(PASS == kOutputs ? maps.state + sg * D * p.n : nullptr);
-        if (PASS == kOutputs && cut.seg == 0 && t0 >= t1) {   // an empty sequence
-            if (on && p.S_T) store8(p.S_T + n * D * p.n + state_at, li * kNs, p.n, h);
+            load_state(PASS == kOutputs ? maps.state + sg * D * p.n : nullptr, h);
+        if (PASS == kOutputs && t0 >= t1) {   // an empty sequence
+            if (p.S_T) store_state(p.S_T + n * D * p.n);
             continue;
         }
-        float sum = 0.f;
+        F2 sum = 0;   // of the step sizes of my channels
 
-        Pack<T, V> rx[NI], rd[NI], rz[NI];
-        // this tile's tokens [a, b) of the walk
-        int64_t a, b;
-        auto tile_of = [&](int64_t t) {   // t: the first token, or one behind the last (reversed)
+        // the tile that holds token t (reversed: that ends before t) of sequence m
+        auto tile_at = [&](int64_t t, int32_t m) {
+            Tile k;
+            k.n = m;
+            k.start = cu[m];
+            int64_t b;
             if (PASS == kGradMaps) {
                 b = t;
-                a = (t - 1) / kTile * kTile;
-                if (a < t0) a = t0;
+                k.a = (t - 1) / kTile * kTile;
+                if (k.a < t0) k.a = t0;
+                k.ends = false;
             } else {
-                a = t;
+                const int64_t end = cu[m + 1];
+                k.a = t;
                 b = t / kTile * kTile + kTile;
                 if (b > t1) b = t1;
+                if (b > end) b = end;
+                k.ends = b == end;
             }
+            k.cnt = (int32_t)(b - k.a);
+            return k;
         };
-        // the vector i of this thread: its row and first channel
-        auto row_of = [&](int i) { return (tid + i * kThreads) / VR; };
-        auto col_of = [&](int i) { return (tid + i * kThreads) % VR * V; };
-        auto fetch = [&](int64_t from, int64_t to) {
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int r = row_of(i), c = col_of(i);
-                if (from + r < to && c < width) {
-                    rx[i].load(X + (from + r) * ldx + base + c);
-                    rd[i].load(DT + (from + r) * p.in.lddt + base + c);
-                    if (PASS == kGradMaps && Z) rz[i].load(Z + (from + r) * p.in.ldz + base + c);
-                }
-            }
+        auto has_next = [&](const Tile& k) {
+            return PASS == kGradMaps ? k.a > t0 : k.a + k.cnt < t1;
         };
-        tile_of(PASS == kGradMaps ? t1 : t0);
-        if (V > 1) fetch(a, b);
-        while (true) {
-            int64_t end = b;
-            if (PASS == kOutputs) {   // tiles end with their sequence
-                const int64_t e = cu[n + 1];
-                if (e < end) end = e;
-            }
-            const int cnt = (int)(end - a);
-            if (V == 1) fetch(a, end);
-            Pack<T, V> kx[NI];
+        auto next_of = [&](const Tile& k) {
+            if (PASS == kGradMaps) return tile_at(k.a, k.n);
+            int32_t m = k.n;
+            const int64_t t = k.a + k.cnt;
+            if (PASS == kOutputs && k.ends)
+                while (cu[m + 1] <= t) ++m;
+            return tile_at(t, m);
+        };
+
+        // my vectors of a tile: row row_of(i), V channels from my_c on
+        const int my_c = tid % VR * V;
+        const bool in_row = my_c < width;
+        auto row_of = [&](int i) { return (tid + i * TH) / VR; };
+        auto col_of = [&](int i) { return V == 1 ? (tid + i * TH) % VR : my_c; };
+        float bias[V], skip[V];
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int r = row_of(i), c = col_of(i);
-                kx[i] = rx[i];
-                if (r < cnt && c < width) {
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        float v = rd[i].get(k) + (p.dt_bias ? p.dt_bias[base + c + k] : 0.f);
-                        if (p.softplus) v = softplus(v);
-                        float u = rx[i].get(k);
-                        if (PASS == kGradMaps) u = Z ? u * silu(rz[i].get(k)) : u;
-                        else u *= v;
-                        s.du[r][c + k] = make_float2(v, u);
-                    }
-                }
-            }
-            for (int i = tid; i < kTile * NP; i += kThreads) {
-                const int r = i / NP, k = i % NP;
-                float bv = 0.f, cv = 0.f;
-                if (r < cnt && k < p.n) {
-                    if (PASS != kGradMaps)
-                        bv = Elem<T>::load(static_cast<const T*>(p.in.B) + (a + r) * p.in.ldB +
-                                           (int64_t)g * p.n + k);
-                    if (PASS != kMaps)
-                        cv = Elem<T>::load(static_cast<const T*>(p.in.C) + (a + r) * p.in.ldC +
-                                           (int64_t)g * p.n + k);
-                }
-                s.B[r][k] = bv;
-                s.C[r][k] = cv;
-            }
-            __syncthreads();
-            const int64_t a_now = a;
-            bool more;
-            if (PASS == kGradMaps) {
-                more = a > t0;
-                if (more) tile_of(a);
-            } else {
-                more = end < t1;
-                if (more) tile_of(end);
-            }
-            if (V > 1 && more) fetch(a, b);
-            if (PASS == kOutputs && Z && V > 1) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int r = row_of(i), c = col_of(i);
-                    if (r < cnt && c < width) rz[i].load(Z + (a_now + r) * p.in.ldz + base + c);
-                }
-            }
-            const int64_t start = PASS == kOutputs ? cu[n] : 0;
-            // (channels that are not there take part in the sums over the lanes)
-            {
-#pragma unroll 4
-                for (int j = 0; j < cnt; ++j) {
-                    const int r = PASS == kGradMaps ? cnt - 1 - j : j;
-                    if (PASS == kOutputs && p.states && on && ((a_now + r) & (SELSCAN_CHUNK - 1)) == 0 &&
-                        a_now + r > start)
-                        store8(p.states + (a_now + r) / SELSCAN_CHUNK * D * p.n + state_at, li * kNs,
-                               p.n, h);
-                    const float2 du = s.du[r][cl];
-                    const F2 dd = pack2(du.x, du.x), uu = pack2(du.y, du.y);
-                    if (PASS != kOutputs) sum += du.x;
-                    F2 y = 0;
-                    const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(&s.B[r][li * kNs]);
-                    const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(&s.C[r][li * kNs]);
-#pragma unroll
-                    for (int i = 0; i < kNs / 4; ++i) {
-                        ulonglong2 bv = {}, cv = {};
-                        if (PASS != kGradMaps) bv = Bp[i];
-                        if (PASS != kMaps) cv = Cp[i];
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int k = 2 * i + q;
-                            const F2 dec = decay2(dd, A[k]);
-                            if (PASS == kGradMaps) {
-                                h[k] = mul2(dec, fma2(uu, q ? cv.y : cv.x, h[k]));
-                            } else {
-                                h[k] = fma2(dec, h[k], mul2(uu, q ? bv.y : bv.x));
-                                if (PASS == kOutputs) y = fma2(h[k], q ? cv.y : cv.x, y);
-                            }
-                        }
-                    }
-                    if (PASS == kOutputs) {
-                        float v = sum2(y);
-#pragma unroll
-                        for (int o = 1; o < L; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                        if (li == 0) s.du[r][cl].y = v;   // (the channel's lanes have read it)
-                    }
-                }
-            }
-            __syncthreads();
-            if (PASS == kOutputs && p.y) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int r = row_of(i), c = col_of(i);
-                    if (r < cnt && c < width) {
-                        if (V == 1 && Z) rz[i].load(Z + (a_now + r) * p.in.ldz + base + c);
-                        float o[V];
-#pragma unroll
-                        for (int k = 0; k < V; ++k) {
-                            o[k] = s.du[r][c + k].y;
-                            if (p.skip) o[k] = fmaf(p.skip[base + c + k], kx[i].get(k), o[k]);
-                            if (Z) o[k] *= silu(rz[i].get(k));
-                        }
-                        Pack<T, V> ky;
-                        ky.set(o);
-                        ky.store(static_cast<T*>(p.y) + (a_now + r) * D + base + c);
-                    }
-                }
-            }
-            if (PASS == kOutputs && end == cu[n + 1]) {
-                if (on && p.S_T) store8(p.S_T + n * D * p.n + state_at, li * kNs, p.n, h);
-                if (more) {
-                    while (cu[n + 1] <= end) ++n;
-                    set_state(p.S0 ? p.S0 + n * D * p.n : nullptr);
-                }
-            }
-            if (!more) break;
+        for (int k = 0; k < V; ++k) {
+            bias[k] = V > 1 && in_row && p.dt_bias ? p.dt_bias[base + my_c + k] : 0.f;
+            skip[k] = V > 1 && in_row && p.skip && PASS == kOutputs ? p.skip[base + my_c + k] : 0.f;
         }
-        if (PASS != kOutputs && on) {
-            store8(maps.state + sg * D * p.n + state_at, li * kNs, p.n, h);
-            if (li == 0) maps.sum[sg * D + base + cl] = sum;
+        Pack<T, V> rx[NI], rd[NI], rz[NI], kx[NI], kz[NI];
+        Pack<T, VB> rb[NB];
+        auto fetch = [&](const Tile& k) {
+            // (odd rows are read where they are used)
+#pragma unroll
+            for (int i = 0; i < (V > 1 ? NI : 0); ++i) {
+                const int r = row_of(i);
+                if (r < k.cnt && in_row) {
+                    rx[i].load(X + (k.a + r) * ldx + base + my_c);
+                    rd[i].load(DT + (k.a + r) * p.in.lddt + base + my_c);
+                    if (Z) rz[i].load(Z + (k.a + r) * p.in.ldz + base + my_c);
+                }
+            }
+        };
+        // vector i of the tile's B and C: which of the two, its row and first value
+        auto bc_of = [&](int i, int& row, int& at) {
+            const int v = tid + i * TH;
+            row = v % (kTile * NP / VB) / (NP / VB);
+            at = v % (NP / VB) * VB;
+            return v / (kTile * NP / VB);
+        };
+        auto fetch_bc = [&](const Tile& k) {
+            if (!packed) return;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) {
+                int r, at;
+                const int which = bc_of(i, r, at);
+                rb[i].zero();
+                if (which < 2 && r < k.cnt && at < p.n && !(PASS == kMaps && which == 1) &&
+                    !(PASS == kGradMaps && which == 0))
+                    rb[i].load(static_cast<const T*>(which ? p.in.C : p.in.B) +
+                               (k.a + r) * (which ? p.in.ldC : p.in.ldB) + (int64_t)g * p.n + at);
+            }
+        };
+        // what the tile's tokens drive the states with, into s
+        auto convert = [&](const Tile& k, typename G::Buffer& s) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = row_of(i), c = col_of(i);
+                if (r >= k.cnt || c >= width) continue;
+                if constexpr (V == 1) {
+                    rx[0].load(X + (k.a + r) * ldx + base + c);
+                    rd[0].load(DT + (k.a + r) * p.in.lddt + base + c);
+                    float v = rd[0].get(0) + (p.dt_bias ? p.dt_bias[base + c] : 0.f);
+                    if (p.softplus) v = softplus(v);
+                    float u = rx[0].get(0);
+                    if (PASS == kGradMaps) {
+                        if (Z) {
+                            rz[0].load(Z + (k.a + r) * p.in.ldz + base + c);
+                            u *= silu(rz[0].get(0));
+                        }
+                    } else {
+                        u *= v;
+                    }
+                    reinterpret_cast<float2*>(s.du[r])[c] = make_float2(v, u);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < V; q += 2) {
+                        F2 v = pack2(rd[i].get(q) + bias[q], rd[i].get(q + 1) + bias[q + 1]);
+                        if (p.softplus) v = softplus2(v);
+                        float2 u = make_float2(rx[i].get(q), rx[i].get(q + 1));
+                        if (PASS == kGradMaps) {
+                            if (Z) {
+                                u.x *= silu(rz[i].get(q));
+                                u.y *= silu(rz[i].get(q + 1));
+                            }
+                        } else {
+                            u = unpack2(mul2(v, pack2(u.x, u.y)));
+                        }
+                        const float2 w = unpack2(v);
+                        s.du[r][q / 2 * VR + my_c / V] = make_float4(w.x, u.x, w.y, u.y);
+                    }
+                }
+            }
+            if (packed) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                    int r, at;
+                    const int which = bc_of(i, r, at);
+                    if (which > 1) continue;
+                    float* to = which ? &s.C[r][at] : &s.B[r][at];
+#pragma unroll
+                    for (int q = 0; q < VB; q += 4)
+                        *reinterpret_cast<float4*>(to + q) = make_float4(
+                            rb[i].get(q), rb[i].get(q + 1), rb[i].get(q + 2), rb[i].get(q + 3));
+                }
+            } else {
+                for (int i = tid; i < kTile * NP; i += TH) {
+                    const int r = i / NP, q = i % NP;
+                    float bv = 0.f, cv = 0.f;
+                    if (r < k.cnt && q < p.n) {
+                        if (PASS != kGradMaps)
+                            bv = Elem<T>::load(static_cast<const T*>(p.in.B) +
+                                               (k.a + r) * p.in.ldB + (int64_t)g * p.n + q);
+                        if (PASS != kMaps)
+                            cv = Elem<T>::load(static_cast<const T*>(p.in.C) +
+                                               (k.a + r) * p.in.ldC + (int64_t)g * p.n + q);
+                    }
+                    s.B[r][q] = bv;
+                    s.C[r][q] = cv;
+                }
+            }
+        };
+        // one token: row r of s
+        auto token = [&](typename G::Buffer& s, int r) {
+            const float4 du = s.du[r][slot];
+            const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(&s.B[r][li * kNs]);
+            const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(&s.C[r][li * kNs]);
+            if (PASS != kOutputs) {
+                const float2 t = unpack2(sum);
+                sum = pack2(t.x + du.x, t.y + du.z);
+            }
+            F2 y[2] = {0, 0};
+            const F2 dd[2] = {pack2(du.x, du.x), pack2(du.z, du.z)};
+            const F2 uu[2] = {pack2(du.y, du.y), pack2(du.w, du.w)};
+#pragma unroll
+            for (int i = 0; i < kNs / 4; ++i) {
+                ulonglong2 bv = {}, cv = {};
+                if (PASS != kGradMaps) bv = Bp[i];
+                if (PASS != kMaps) cv = Cp[i];
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int k = 2 * i + o;
+                        const F2 a = decay2(dd[q], A[q][k]);
+                        if (PASS == kGradMaps) {
+                            h[q][k] = mul2(a, fma2(uu[q], o ? cv.y : cv.x, h[q][k]));
+                        } else {
+                            h[q][k] = fma2(a, h[q][k], mul2(uu[q], o ? bv.y : bv.x));
+                            if (PASS == kOutputs) y[q] = fma2(h[q][k], o ? cv.y : cv.x, y[q]);
+                        }
+                    }
+            }
+            if (PASS == kOutputs) {
+                float v0 = sum2(y[0]), v1 = sum2(y[1]);
+                if constexpr (L == 1) {
+                    s.du[r][slot].y = v0;
+                    s.du[r][slot].w = v1;
+                } else {   // even lanes end with the first channel, odd ones with the second
+                    const bool odd = li & 1;
+                    float v = (odd ? v1 : v0) + __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+#pragma unroll
+                    for (int o = 2; o < L; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    // (the channels' lanes have read the place by now)
+                    if (li < 2) reinterpret_cast<float*>(&s.du[r][slot])[2 * li + 1] = v;
+                }
+            }
+        };
+        // the outputs of a tile whose sums are in s
+        auto finish = [&](const Tile& k, const typename G::Buffer& s) {
+            if (!p.y) return;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int r = row_of(i), c = col_of(i);
+                if (r >= k.cnt || c >= width) continue;
+                float o[V];
+                if constexpr (V == 1) {
+                    o[0] = reinterpret_cast<const float2*>(s.du[r])[c].y;
+                    kx[0].load(X + (k.a + r) * ldx + base + c);
+                    if (p.skip) o[0] = fmaf(p.skip[base + c], kx[0].get(0), o[0]);
+                    if (Z) {
+                        kz[0].load(Z + (k.a + r) * p.in.ldz + base + c);
+                        o[0] *= silu(kz[0].get(0));
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < V; q += 2) {
+                        const float4 v = s.du[r][q / 2 * VR + my_c / V];
+                        o[q] = fmaf(skip[q], kx[i].get(q), v.y);
+                        o[q + 1] = fmaf(skip[q + 1], kx[i].get(q + 1), v.w);
+                        if (Z) {
+                            o[q] *= silu(kz[i].get(q));
+                            o[q + 1] *= silu(kz[i].get(q + 1));
+                        }
+                    }
+                }
+                Pack<T, V> ky;
+                ky.set(o);
+                ky.store(static_cast<T*>(p.y) + (k.a + r) * D + base + c);
+            }
+        };
+
+        Tile now = tile_at(PASS == kGradMaps ? t1 : t0, n), before = now;
+        fetch(now);
+        fetch_bc(now);
+        convert(now, buf[0]);
+        int side = 0;
+        bool first = true;
+        while (true) {
+            // One barrier a tile: behind it this tile's buffer is written, the other's sums are
+            // done, and the next tile's may go where those have been read.
+            __syncthreads();
+            if constexpr (PASS == kOutputs)
+                if (!first) finish(before, buf[side ^ 1]);
+            first = false;
+            if (V > 1) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    kx[i] = rx[i];
+                    kz[i] = rz[i];
+                }
+            }
+            const bool more = has_next(now);
+            Tile next = now;
+            if (more) {
+                next = next_of(now);
+                fetch(next);
+                fetch_bc(next);
+            }
+            typename G::Buffer& s = buf[side];
+            if (PASS == kOutputs && p.states && now.a % SELSCAN_CHUNK == 0 && now.a > now.start)
+                store_state(p.states + now.a / SELSCAN_CHUNK * D * p.n);
+#pragma unroll 4
+            for (int j = 0; j < now.cnt; ++j) token(s, PASS == kGradMaps ? now.cnt - 1 - j : j);
+            if (PASS == kOutputs && now.ends) {
+                if (p.S_T) store_state(p.S_T + now.n * D * p.n);
+                if (more) first_state(next.n);
+            }
+            before = now;
+            if (!more) break;
+            // (the threads that read the other buffer's outputs are those that write there now)
+            convert(next, buf[side ^ 1]);
+            now = next;
+            side ^= 1;
+        }
+        __syncthreads();
+        if constexpr (PASS == kOutputs) finish(before, buf[side]);
+        if (PASS != kOutputs) {
+            store_state(maps.state + sg * D * p.n);
+            const float2 t = unpack2(sum);
+            if (li == 0 && cp < width) maps.sum[sg * D + base + cp] = t.x;
+            if (li == 0 && cp + 1 < width) maps.sum[sg * D + base + cp + 1] = t.y;
             if (cb == 0 && tid == 0) maps.reset[sg] = reset;
         }
+        __syncthreads();
     }
 }
 
@@ -434,7 +593,7 @@ join_kernel(const ScanArgs p, const Cut cut, const Maps maps, bool reversed, con
             const int64_t s = reversed ? segs - 1 - (s0 + k) : s0 + k;
             if (s0 + k < segs) {
                 maps.state[s * D * p.n + i] = h;
-                h = r[k] ? e[k] : fmaf(ex2(fmaf(d[k], A, kShift)) * kUnshift, h, e[k]);
+                h = r[k] ? e[k] : fmaf(decay(d[k], A), h, e[k]);
             }
         }
     }
@@ -860,7 +1019,7 @@ __global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanStepArgs 
     for (int i = 0; i < kNs; ++i) {
         const int k = li * kNs + i;
         const float bv = k < p.n ? Elem<T>::load(B + k) : 0.f, cv = k < p.n ? Elem<T>::load(C + k) : 0.f;
-        const float a = ex2(fmaf(step, A[i] * kLog2e, kShift)) * kUnshift;
+        const float a = decay(step, A[i] * kLog2e);
         h[i] = fmaf(a, h[i], step * x * bv);
         y = fmaf(h[i], cv, y);
     }
@@ -883,6 +1042,14 @@ constexpr size_t kHead = 256;   // the status word's part of the workspace
 int64_t sms() { return sm_count() > 0 ? sm_count() : 1; }
 
 int lanes_of(int n) { return n <= 8 ? 1 : n <= 16 ? 2 : n <= 32 ? 4 : 8; }
+int forward_channels(int n) {
+    switch (lanes_of(n)) {
+        case 1: return Fwd<1>::kCh;
+        case 2: return Fwd<2>::kCh;
+        case 4: return Fwd<4>::kCh;
+        default: return Fwd<8>::kCh;
+    }
+}
 int back_lanes_of(int n) { return n <= 8 ? 2 : n <= 16 ? 4 : n <= 32 ? 8 : 16; }
 int back_channels(int n) {
     switch (back_lanes_of(n)) {
@@ -899,19 +1066,19 @@ Cut make_cut(int32_t N, int64_t T, int32_t H, int32_t d, int ch, int want) {
     Cut c = {};
     c.per_group = (d + ch - 1) / ch;
     const int64_t blocks = (int64_t)c.per_group * H, fill = want * sms();
-    if (N == 0 || N * blocks >= fill || T < (int64_t)N * 2 * kTile) {
+    if (N == 0 || N * blocks >= fill || T < (int64_t)N * 64) {
         c.nseg = N;
     } else {
         const int64_t most = (2 * fill + blocks - 1) / blocks;   // segments that fill it twice
         c.seg = ((T + most - 1) / most + kTile - 1) / kTile * kTile;
-        if (c.seg < 2 * kTile) c.seg = 2 * kTile;
+        if (c.seg < 64) c.seg = 64;
         c.nseg = (T + c.seg - 1) / c.seg;
     }
     c.items = c.nseg * blocks;
     return c;
 }
 Cut forward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
-    return make_cut(N, T, H, d, kThreads / lanes_of(n), 3);
+    return make_cut(N, T, H, d, forward_channels(n), 3);
 }
 Cut backward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
     return make_cut(N, T, H, d, back_channels(n), 1);
@@ -920,7 +1087,7 @@ Cut backward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
 // its own channel blocks.
 Cut grad_map_cut(const Cut& back, int32_t H, int32_t d, int32_t n) {
     Cut c = back;
-    const int ch = kThreads / lanes_of(n);
+    const int ch = forward_channels(n);
     c.per_group = (d + ch - 1) / ch;
     c.items = c.nseg * c.per_group * H;
     return c;
@@ -981,7 +1148,7 @@ cudaError_t run_scan(const ScanArgs& a, const Cut& cut, const Maps& maps, int32_
             const int64_t most = (int64_t)1 << 30;
             const unsigned grid = (unsigned)(cut.items < 1 ? 1 : cut.items < most ? cut.items : most);
             auto kernel = wide ? scan_kernel<T, L, V, PASS> : scan_kernel<T, L, 1, PASS>;
-            kernel<<<grid, kThreads, 0, stream>>>(a, cut, maps, status);
+            kernel<<<grid, Fwd<L>::kThreads, 0, stream>>>(a, cut, maps, status);
             return cudaGetLastError();
         });
     });
