@@ -164,13 +164,11 @@ struct Fwd {
     static constexpr int kCh = kThreads / L * 2;
     static constexpr int kNp = kNs * L;
     // Step size and what drives the state, of a pair of channels side by side: (D, u) of one, (D,
-    // u) of the other.  Where a thread writes V channels at once, the pairs of a row lie in the
-    // order of the threads (pair_slot), so that neither side meets bank conflicts.  An output
-    // takes the place of its u.
-    struct Buffer {
-        float4 du[kTile][kCh / 2];
-        float B[kTile][kNp], C[kTile][kNp];
-    };
+    // u) of the other; and their outputs.  Where a thread writes V channels at once, the pairs of
+    // a row lie in the order of the threads (pair_slot), so that neither side meets bank conflicts.
+    using Steps = float4[kTile][kCh / 2];
+    using Outs = float2[kTile][kCh / 2];
+    using Rows = float[kTile][kNp];      // of B or C
 };
 // Where the pair of channel c (even) lies in a row of CH channels written V at a time.
 template <int CH, int V>
@@ -200,7 +198,10 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
     constexpr int VB = 16 / sizeof(T);                  // values of B and C at once
     constexpr int NB = (2 * kTile * NP / VB + TH - 1) / TH;
     static_assert(V == 1 || TH % VR == 0, "a thread keeps its channels");
-    __shared__ __align__(16) typename G::Buffer buf[2];
+    // (objects of their own: a store to one does not hold up the loads from another)
+    __shared__ __align__(16) typename G::Steps s_du[2];
+    __shared__ __align__(16) typename G::Rows s_B[2], s_C[2];
+    __shared__ __align__(16) typename G::Outs s_y[PASS == kOutputs ? 2 : 1];
     const int32_t* cu = p.cu_seqlens;
     if (!offsets_ok(cu, p.num_seqs, p.total_tokens, status)) return;
     const int tid = threadIdx.x, li = tid % L, slot = tid / L;
@@ -360,7 +361,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             }
         };
         // what the tile's tokens drive the states with, into s
-        auto convert = [&](const Tile& k, typename G::Buffer& s) {
+        auto convert = [&](const Tile& k, int side) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int r = row_of(i), c = col_of(i);
@@ -379,7 +380,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                     } else {
                         u *= v;
                     }
-                    reinterpret_cast<float2*>(s.du[r])[c] = make_float2(v, u);
+                    reinterpret_cast<float2*>(s_du[side][r])[c] = make_float2(v, u);
                 } else {
 #pragma unroll
                     for (int q = 0; q < V; q += 2) {
@@ -395,7 +396,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                             u = unpack2(mul2(v, pack2(u.x, u.y)));
                         }
                         const float2 w = unpack2(v);
-                        s.du[r][q / 2 * VR + my_c / V] = make_float4(w.x, u.x, w.y, u.y);
+                        s_du[side][r][q / 2 * VR + my_c / V] = make_float4(w.x, u.x, w.y, u.y);
                     }
                 }
             }
@@ -405,7 +406,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                     int r, at;
                     const int which = bc_of(i, r, at);
                     if (which > 1) continue;
-                    float* to = which ? &s.C[r][at] : &s.B[r][at];
+                    float* to = which ? &s_C[side][r][at] : &s_B[side][r][at];
 #pragma unroll
                     for (int q = 0; q < VB; q += 4)
                         *reinterpret_cast<float4*>(to + q) = make_float4(
@@ -423,23 +424,37 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                             cv = Elem<T>::load(static_cast<const T*>(p.in.C) +
                                                (k.a + r) * p.in.ldC + (int64_t)g * p.n + q);
                     }
-                    s.B[r][q] = bv;
-                    s.C[r][q] = cv;
+                    s_B[side][r][q] = bv;
+                    s_C[side][r][q] = cv;
                 }
             }
         };
-        // one token: row r of s
-        auto token = [&](typename G::Buffer& s, int r) {
-            const float4 du = s.du[r][slot];
-            const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(&s.B[r][li * kNs]);
-            const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(&s.C[r][li * kNs]);
+        // The decays of a token are formed one token ahead: the special-function unit and the
+        // multiply-adds then work on different tokens.
+        struct Step {
+            float4 du;
+            F2 a[2][kNs / 2];
+        };
+        auto step_of = [&](int side, int r) {
+            Step t;
+            t.du = s_du[side][r][slot];
+            const F2 dd[2] = {pack2(t.du.x, t.du.x), pack2(t.du.z, t.du.z)};
+#pragma unroll
+            for (int k = 0; k < kNs / 2; ++k)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) t.a[q][k] = decay2(dd[q], A[q][k]);
+            return t;
+        };
+        // one token: row r
+        auto token = [&](const Step& t, int side, int r) {
+            const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(&s_B[side][r][li * kNs]);
+            const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(&s_C[side][r][li * kNs]);
             if (PASS != kOutputs) {
-                const float2 t = unpack2(sum);
-                sum = pack2(t.x + du.x, t.y + du.z);
+                const float2 v = unpack2(sum);
+                sum = pack2(v.x + t.du.x, v.y + t.du.z);
             }
             F2 y[2] = {0, 0};
-            const F2 dd[2] = {pack2(du.x, du.x), pack2(du.z, du.z)};
-            const F2 uu[2] = {pack2(du.y, du.y), pack2(du.w, du.w)};
+            const F2 uu[2] = {pack2(t.du.y, t.du.y), pack2(t.du.w, t.du.w)};
 #pragma unroll
             for (int i = 0; i < kNs / 4; ++i) {
                 ulonglong2 bv = {}, cv = {};
@@ -450,11 +465,10 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const int k = 2 * i + o;
-                        const F2 a = decay2(dd[q], A[q][k]);
                         if (PASS == kGradMaps) {
-                            h[q][k] = mul2(a, fma2(uu[q], o ? cv.y : cv.x, h[q][k]));
+                            h[q][k] = mul2(t.a[q][k], fma2(uu[q], o ? cv.y : cv.x, h[q][k]));
                         } else {
-                            h[q][k] = fma2(a, h[q][k], mul2(uu[q], o ? bv.y : bv.x));
+                            h[q][k] = fma2(t.a[q][k], h[q][k], mul2(uu[q], o ? bv.y : bv.x));
                             if (PASS == kOutputs) y[q] = fma2(h[q][k], o ? cv.y : cv.x, y[q]);
                         }
                     }
@@ -462,20 +476,18 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             if (PASS == kOutputs) {
                 float v0 = sum2(y[0]), v1 = sum2(y[1]);
                 if constexpr (L == 1) {
-                    s.du[r][slot].y = v0;
-                    s.du[r][slot].w = v1;
+                    s_y[side][r][slot] = make_float2(v0, v1);
                 } else {   // even lanes end with the first channel, odd ones with the second
                     const bool odd = li & 1;
                     float v = (odd ? v1 : v0) + __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
 #pragma unroll
                     for (int o = 2; o < L; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    // (the channels' lanes have read the place by now)
-                    if (li < 2) reinterpret_cast<float*>(&s.du[r][slot])[2 * li + 1] = v;
+                    if (li < 2) reinterpret_cast<float*>(&s_y[side][r][slot])[li] = v;
                 }
             }
         };
-        // the outputs of a tile whose sums are in s
-        auto finish = [&](const Tile& k, const typename G::Buffer& s) {
+        // the outputs of a tile whose sums are there
+        auto finish = [&](const Tile& k, int side) {
             if (!p.y) return;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
@@ -483,7 +495,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                 if (r >= k.cnt || c >= width) continue;
                 float o[V];
                 if constexpr (V == 1) {
-                    o[0] = reinterpret_cast<const float2*>(s.du[r])[c].y;
+                    o[0] = reinterpret_cast<const float*>(s_y[side][r])[c];
                     kx[0].load(X + (k.a + r) * ldx + base + c);
                     if (p.skip) o[0] = fmaf(p.skip[base + c], kx[0].get(0), o[0]);
                     if (Z) {
@@ -493,9 +505,9 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                 } else {
 #pragma unroll
                     for (int q = 0; q < V; q += 2) {
-                        const float4 v = s.du[r][q / 2 * VR + my_c / V];
-                        o[q] = fmaf(skip[q], kx[i].get(q), v.y);
-                        o[q + 1] = fmaf(skip[q + 1], kx[i].get(q + 1), v.w);
+                        const float2 v = s_y[side][r][q / 2 * VR + my_c / V];
+                        o[q] = fmaf(skip[q], kx[i].get(q), v.x);
+                        o[q + 1] = fmaf(skip[q + 1], kx[i].get(q + 1), v.y);
                         if (Z) {
                             o[q] *= silu(kz[i].get(q));
                             o[q + 1] *= silu(kz[i].get(q + 1));
@@ -511,7 +523,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         Tile now = tile_at(PASS == kGradMaps ? t1 : t0, n), before = now;
         fetch(now);
         fetch_bc(now);
-        convert(now, buf[0]);
+        convert(now, 0);
         int side = 0;
         bool first = true;
         while (true) {
@@ -519,7 +531,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             // done, and the next tile's may go where those have been read.
             __syncthreads();
             if constexpr (PASS == kOutputs)
-                if (!first) finish(before, buf[side ^ 1]);
+                if (!first) finish(before, side ^ 1);
             first = false;
             if (V > 1) {
 #pragma unroll
@@ -535,24 +547,36 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                 fetch(next);
                 fetch_bc(next);
             }
-            typename G::Buffer& s = buf[side];
             if (PASS == kOutputs && p.states && now.a % SELSCAN_CHUNK == 0 && now.a > now.start)
                 store_state(p.states + now.a / SELSCAN_CHUNK * D * p.n);
-#pragma unroll 4
-            for (int j = 0; j < now.cnt; ++j) token(s, PASS == kGradMaps ? now.cnt - 1 - j : j);
+            if (now.cnt == kTile) {   // every place known at compile time
+                Step t = step_of(side, PASS == kGradMaps ? kTile - 1 : 0);
+#pragma unroll
+                for (int j = 0; j < kTile; ++j) {
+                    Step ahead = t;
+                    if (j + 1 < kTile) ahead = step_of(side, PASS == kGradMaps ? kTile - 2 - j : j + 1);
+                    token(t, side, PASS == kGradMaps ? kTile - 1 - j : j);
+                    t = ahead;
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < now.cnt; ++j) {
+                    const int r = PASS == kGradMaps ? now.cnt - 1 - j : j;
+                    token(step_of(side, r), side, r);
+                }
+            }
             if (PASS == kOutputs && now.ends) {
                 if (p.S_T) store_state(p.S_T + now.n * D * p.n);
                 if (more) first_state(next.n);
             }
             before = now;
             if (!more) break;
-            // (the threads that read the other buffer's outputs are those that write there now)
-            convert(next, buf[side ^ 1]);
+            convert(next, side ^ 1);
             now = next;
             side ^= 1;
         }
         __syncthreads();
-        if constexpr (PASS == kOutputs) finish(before, buf[side]);
+        if constexpr (PASS == kOutputs) finish(before, side);
         if (PASS != kOutputs) {
             store_state(maps.state + sg * D * p.n);
             const float2 t = unpack2(sum);
