@@ -32,8 +32,9 @@ constexpr int kThreads = 128;   // of the small kernels
 constexpr int kTile = SELSCAN_CHUNK;   // tokens of a forward tile; segments are whole tiles
 constexpr int kNs = 8;          // state values a lane, forward
 constexpr int kBack = SELSCAN_CHUNK;   // tokens of a backward tile
-constexpr int kSub = 8;         // tokens whose states lie in registers, backward
-static_assert(kTile == SELSCAN_CHUNK && kBack == 2 * kSub, "tiles hold whole chunks");
+constexpr int kSub = 4;         // tokens whose states lie in registers, backward
+constexpr int kParts = kBack / kSub;
+static_assert(kTile == SELSCAN_CHUNK, "tiles hold whole chunks");
 
 // Two floats for the packed instructions.
 using F2 = unsigned long long;
@@ -156,12 +157,12 @@ __device__ __forceinline__ void store8(float* p, int k, int n, const F2 (&h)[kNs
 // maps of the gradients' recurrence (on reversed tokens).
 enum { kOutputs = 0, kMaps = 1, kGradMaps = 2 };
 
-// L lanes share two neighbouring channels, 8 values of each a lane.
+// L lanes share a channel, 8 values each.  (Two channels a lane take fewer instructions, but leave
+// too few warps to hide the latencies of a token: see the head of the file.)
 template <int L>
 struct Fwd {
-    static constexpr int kWarps = L == 1 ? 1 : L == 2 ? 2 : 4;
-    static constexpr int kThreads = kWarps * 32;
-    static constexpr int kCh = kThreads / L * 2;
+    static constexpr int kThreads = L == 1 ? 64 : 128;
+    static constexpr int kCh = kThreads / L;
     static constexpr int kNp = kNs * L;
     // Step size and what drives the state, of a pair of channels side by side: (D, u) of one, (D,
     // u) of the other; and their outputs.  Where a thread writes V channels at once, the pairs of
@@ -189,7 +190,7 @@ struct Tile {
 };
 
 template <typename T, int L, int V, int PASS>
-__global__ void __launch_bounds__(Fwd<L>::kThreads)
+__global__ void __launch_bounds__(Fwd<L>::kThreads, V == 1 ? 1 : 512 / Fwd<L>::kThreads)
 scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
     using G = Fwd<L>;
     constexpr int CH = G::kCh, NP = G::kNp, TH = G::kThreads;
@@ -205,7 +206,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
     const int32_t* cu = p.cu_seqlens;
     if (!offsets_ok(cu, p.num_seqs, p.total_tokens, status)) return;
     const int tid = threadIdx.x, li = tid % L, slot = tid / L;
-    const int cp = slot_channel<CH, V>(slot);           // my two channels
+    const int ch = slot_channel<CH, V>(slot / 2) + slot % 2;   // my channel
     const int64_t D = (int64_t)p.H * p.d, last = cu[p.num_seqs];
     const T* const X = static_cast<const T*>(PASS == kGradMaps ? p.dy : p.in.x);
     const int64_t ldx = PASS == kGradMaps ? D : p.in.ldx;
@@ -247,28 +248,22 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             }
         }
 
-        F2 A[2][kNs / 2], h[2][kNs / 2];
-        auto row_of_state = [&](int q) { return (base + cp + q) * p.n; };
-        auto load_state = [&](const float* from, F2 (&to)[2][kNs / 2]) {
+        F2 A[kNs / 2], h[kNs / 2];
+        const bool on = ch < width;
+        const int64_t my_state = (base + ch) * p.n;
+        auto load_state = [&](const float* from, F2 (&to)[kNs / 2]) {
+            float v[kNs];
+            load8(from && on ? from + my_state : nullptr, li * kNs, p.n, v);
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                float v[kNs];
-                load8(from && cp + q < width ? from + row_of_state(q) : nullptr, li * kNs, p.n, v);
-#pragma unroll
-                for (int i = 0; i < kNs / 2; ++i) to[q][i] = pack2(v[2 * i], v[2 * i + 1]);
-            }
+            for (int i = 0; i < kNs / 2; ++i) to[i] = pack2(v[2 * i], v[2 * i + 1]);
         };
         auto store_state = [&](float* to) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (cp + q < width) store8(to + row_of_state(q), li * kNs, p.n, h[q]);
+            if (on) store8(to + my_state, li * kNs, p.n, h);
         };
         auto first_state = [&](int32_t m) { load_state(p.S0 ? p.S0 + m * D * p.n : nullptr, h); };
         load_state(p.A, A);
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-            for (int i = 0; i < kNs / 2; ++i) A[q][i] = mul2(A[q][i], pack2(kLog2e, kLog2e));
+        for (int i = 0; i < kNs / 2; ++i) A[i] = mul2(A[i], pack2(kLog2e, kLog2e));
         if (PASS == kGradMaps)
             load_state(reset && p.dS_T ? p.dS_T + n * D * p.n : nullptr, h);
         else if (t0 == cu[n])
@@ -279,7 +274,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             if (p.S_T) store_state(p.S_T + n * D * p.n);
             continue;
         }
-        F2 sum = 0;   // of the step sizes of my channels
+        float sum = 0.f;   // of the step sizes
 
         // the tile that holds token t (reversed: that ends before t) of sequence m
         auto tile_at = [&](int64_t t, int32_t m) {
@@ -432,58 +427,45 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         // The decays of a token are formed one token ahead: the special-function unit and the
         // multiply-adds then work on different tokens.
         struct Step {
-            float4 du;
-            F2 a[2][kNs / 2];
+            float2 du;
+            F2 a[kNs / 2];
         };
         auto step_of = [&](int side, int r) {
             Step t;
-            t.du = s_du[side][r][slot];
-            const F2 dd[2] = {pack2(t.du.x, t.du.x), pack2(t.du.z, t.du.z)};
+            t.du = reinterpret_cast<const float2*>(s_du[side][r])[slot];
+            const F2 dd = pack2(t.du.x, t.du.x);
 #pragma unroll
-            for (int k = 0; k < kNs / 2; ++k)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) t.a[q][k] = decay2(dd[q], A[q][k]);
+            for (int k = 0; k < kNs / 2; ++k) t.a[k] = decay2(dd, A[k]);
             return t;
         };
         // one token: row r
         auto token = [&](const Step& t, int side, int r) {
             const ulonglong2* Bp = reinterpret_cast<const ulonglong2*>(&s_B[side][r][li * kNs]);
             const ulonglong2* Cp = reinterpret_cast<const ulonglong2*>(&s_C[side][r][li * kNs]);
-            if (PASS != kOutputs) {
-                const float2 v = unpack2(sum);
-                sum = pack2(v.x + t.du.x, v.y + t.du.z);
-            }
-            F2 y[2] = {0, 0};
-            const F2 uu[2] = {pack2(t.du.y, t.du.y), pack2(t.du.w, t.du.w)};
+            if (PASS != kOutputs) sum += t.du.x;
+            F2 y = 0;
+            const F2 uu = pack2(t.du.y, t.du.y);
 #pragma unroll
             for (int i = 0; i < kNs / 4; ++i) {
                 ulonglong2 bv = {}, cv = {};
                 if (PASS != kGradMaps) bv = Bp[i];
                 if (PASS != kMaps) cv = Cp[i];
 #pragma unroll
-                for (int o = 0; o < 2; ++o)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int k = 2 * i + o;
-                        if (PASS == kGradMaps) {
-                            h[q][k] = mul2(t.a[q][k], fma2(uu[q], o ? cv.y : cv.x, h[q][k]));
-                        } else {
-                            h[q][k] = fma2(t.a[q][k], h[q][k], mul2(uu[q], o ? bv.y : bv.x));
-                            if (PASS == kOutputs) y[q] = fma2(h[q][k], o ? cv.y : cv.x, y[q]);
-                        }
+                for (int o = 0; o < 2; ++o) {
+                    const int k = 2 * i + o;
+                    if (PASS == kGradMaps) {
+                        h[k] = mul2(t.a[k], fma2(uu, o ? cv.y : cv.x, h[k]));
+                    } else {
+                        h[k] = fma2(t.a[k], h[k], mul2(uu, o ? bv.y : bv.x));
+                        if (PASS == kOutputs) y = fma2(h[k], o ? cv.y : cv.x, y);
                     }
+                }
             }
             if (PASS == kOutputs) {
-                float v0 = sum2(y[0]), v1 = sum2(y[1]);
-                if constexpr (L == 1) {
-                    s_y[side][r][slot] = make_float2(v0, v1);
-                } else {   // even lanes end with the first channel, odd ones with the second
-                    const bool odd = li & 1;
-                    float v = (odd ? v1 : v0) + __shfl_xor_sync(0xffffffffu, odd ? v0 : v1, 1);
+                float v = sum2(y);
 #pragma unroll
-                    for (int o = 2; o < L; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (li < 2) reinterpret_cast<float*>(&s_y[side][r][slot])[li] = v;
-                }
+                for (int o = 1; o < L; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+                if (li == 0) reinterpret_cast<float*>(s_y[side][r])[slot] = v;
             }
         };
         // the outputs of a tile whose sums are there
@@ -579,9 +561,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         if constexpr (PASS == kOutputs) finish(before, side);
         if (PASS != kOutputs) {
             store_state(maps.state + sg * D * p.n);
-            const float2 t = unpack2(sum);
-            if (li == 0 && cp < width) maps.sum[sg * D + base + cp] = t.x;
-            if (li == 0 && cp + 1 < width) maps.sum[sg * D + base + cp + 1] = t.y;
+            if (li == 0 && on) maps.sum[sg * D + base + ch] = sum;
             if (cb == 0 && tid == 0) maps.reset[sg] = reset;
         }
         __syncthreads();
@@ -637,35 +617,44 @@ empty_kernel(const int32_t* cu, int32_t N, int64_t row, const float* in, float* 
 
 // ---------------------------------------------------------------- backward
 
-// NL lanes share a channel's state, four values each; a thread holds two channels.
+// NL lanes share two channels, four values of each a lane.
 template <int NL>
 struct Back {
-    static constexpr int kCl = 32 / NL;                       // channel pairs of a warp
-    static constexpr int kWarps = NL == 2 ? 4 : 8;
-    static constexpr int kThreads = kWarps * 32;
-    static constexpr int kCh = kWarps * kCl * 2;
-    static constexpr int kRows = kThreads / kCh;              // tokens side by side in the other passes
+    static constexpr int kThreads = 128;
+    static constexpr int kWarps = kThreads / 32;
+    static constexpr int kCh = kThreads / NL * 2;
+    static constexpr int kNp = 4 * NL;
+    static constexpr int kPart = 2 * kNp * kSub > 256 ? 2 * kNp * kSub : 256;
+    // Channels lie in the order of the threads that write them, V at a time (channel_slot); step, u
+    // and dr twice over, as the packed instructions take them.
     struct Shared {
-        float2 du[kBack][kCh];
-        float dr[kBack][kCh];
-        float B[kBack][4 * NL], C[kBack][4 * NL];
-        float y[kBack][kCh], s1[kBack][kCh], s2[kBack][kCh];
-        float part[kWarps][kBack][8 * NL];
+        float4 du[kBack][kCh];               // D, D, D x, D x
+        float2 dr[kBack][kCh];               // dy silu(z), twice
+        float B[kBack][kNp], C[kBack][kNp];
+        float y[kBack][kCh];                 // C . h
+        float s[2][kBack][kCh];              // B . g and A . (g a h)
+        // A warp's states before the tile's parts but the first, a place a lane; and, where a part's
+        // have been used, dB and dC of its tokens over the warp's channels.
+        float part[kWarps][kParts][kPart];
+        float acc[2][kWarps][kCh];           // sums for dskip and ddt_bias
     };
 };
+template <int CH, int V>
+__device__ __forceinline__ int channel_slot(int c) { return c % V * (CH / V) + c / V; }
 
-// The sums of 8 values over the lanes that differ in the bits from NL up: each exchange halves
-// the values a lane carries.  Returns the index of v[0] among the eight (v[1..] follow).
-template <int NL>
-__device__ __forceinline__ int sum_channels(float (&v)[8], int lane) {
-    int at = 0, nv = 8;
+// Sums v[0..N) over the lanes that differ in the bits LO .. HI (powers of two): each exchange
+// halves the values a lane carries, down to one, and adds it up from there on.  Returns the index of
+// v[0] among the N; the others that are left follow it.
+template <int N, int HI, int LO>
+__device__ __forceinline__ int spread_sum(float (&v)[N], int lane) {
+    int at = 0;
 #pragma unroll
-    for (int o = 16; o >= NL; o >>= 1) {
+    for (int o = HI, nv = N; o >= LO; o >>= 1) {
         if (nv > 1) {
             nv /= 2;
             const bool upper = lane & o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < N / 2; ++i)
                 if (i < nv) {
                     const float give = upper ? v[i] : v[i + nv];
                     v[i] = (upper ? v[i + nv] : v[i]) + __shfl_xor_sync(0xffffffffu, give, o);
@@ -677,26 +666,36 @@ __device__ __forceinline__ int sum_channels(float (&v)[8], int lane) {
     }
     return at;
 }
-template <int NL>
-constexpr int kLeft = NL >= 16 ? 4 : NL >= 8 ? 2 : 1;   // values a lane is left with
+// How many are left.
+constexpr int spread_left(int n, int hi, int lo) {
+    for (int o = hi; o >= lo && n > 1; o >>= 1) n /= 2;
+    return n;
+}
 
-template <typename T, int NL>
-__global__ void __launch_bounds__(Back<NL>::kThreads)
+template <typename T, int NL, int V>
+__global__ void __launch_bounds__(Back<NL>::kThreads, V == 1 ? 1 : 4)
 scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A, float* part_c,
                 float* part_BC, const int32_t* status) {
     using G = Back<NL>;
-    constexpr int CH = G::kCh, TH = G::kThreads, NP = 4 * NL;
+    constexpr int CH = G::kCh, TH = G::kThreads, NP = G::kNp;
+    constexpr int VR = CH / V;                              // vectors of a row
+    constexpr int NI = (kBack * VR + TH - 1) / TH;          // of a tile, a thread
+    constexpr int VB = 16 / sizeof(T);                      // values of B and C at once
     extern __shared__ __align__(16) char raw[];
     typename G::Shared& s = *reinterpret_cast<typename G::Shared*>(raw);
     if (*status != KDA_OK) return;
     const int32_t* cu = p.cu_seqlens;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int nl = lane % NL, cp = warp * G::kCl + lane / NL;   // my values, my channel pair
+    const int nl = lane % NL, slot = tid / NL;   // my values; my channels' slots: this and
+    constexpr int kOther = CH / 2;               // that one behind it
     const int64_t D = (int64_t)p.H * p.d, last = cu[p.num_seqs];
     const T* const X = static_cast<const T*>(p.in.x);
     const T* const DT = static_cast<const T*>(p.in.dt);
     const T* const Z = static_cast<const T*>(p.in.z);
     const T* const DY = static_cast<const T*>(p.dy);
+    const bool packed = p.n % VB == 0 && p.in.ldB % VB == 0 && p.in.ldC % VB == 0 &&
+                        ((uint64_t)p.in.B | (uint64_t)p.in.C) % 16 == 0;
+    const int my[2] = {slot % VR * V + slot / VR, (slot + kOther) % VR * V + (slot + kOther) / VR};
 
     for (int64_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
         const int64_t blocks = (int64_t)cut.per_group * p.H;
@@ -717,13 +716,13 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             t1 = t0 + cut.seg < last ? t0 + cut.seg : last;
             n = t0 < t1 ? sequence_of(cu, p.num_seqs, t1 - 1) : 0;
         }
-        // rows of four values of my two channels in a [..][D][n] tensor
+        // four values of my two channels in a [..][D][n] tensor
         auto load4 = [&](const float* from, F2 (&v)[2][2]) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 float u[4] = {0.f, 0.f, 0.f, 0.f};
-                if (from && 2 * cp + q < width) {
-                    const float* r = from + (base + 2 * cp + q) * p.n + nl * 4;
+                if (from && my[q] < width) {
+                    const float* r = from + (base + my[q]) * p.n + nl * 4;
                     if (p.n % 4 == 0) {
                         if (nl * 4 < p.n) {
                             const float4 w = *reinterpret_cast<const float4*>(r);
@@ -742,8 +741,8 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         auto store4 = [&](float* to, const F2 (&v)[2][2]) {
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                if (2 * cp + q >= width) continue;
-                float* r = to + (base + 2 * cp + q) * p.n + nl * 4;
+                if (my[q] >= width) continue;
+                float* r = to + (base + my[q]) * p.n + nl * 4;
                 const float2 lo = unpack2(v[q][0]), hi = unpack2(v[q][1]);
                 const float u[4] = {lo.x, lo.y, hi.x, hi.y};
                 if (p.n % 4 == 0) {
@@ -769,193 +768,306 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         if (t0 < t1 && t1 != cu[n + 1]) behind = maps.state + sg * D * p.n;
         else if (p.dS_T && (t0 < t1 || cut.seg == 0)) behind = p.dS_T + n * D * p.n;
         load4(behind, r);
-        // the passes over (token, channel): a channel and every kRows-th token a thread
-        const int mc = tid % CH, mr = tid / CH;
-        const bool mine = mc < width && mr < G::kRows;
-        const float bias = mine && p.dt_bias ? p.dt_bias[base + mc] : 0.f;
-        const float skip = mine && p.skip ? p.skip[base + mc] : 0.f;
-        float dskip = 0.f, dbias = 0.f;
-
-        int64_t te = t1;
+        for (int i = tid; i < 2 * G::kWarps * CH; i += TH) (&s.acc[0][0][0])[i] = 0.f;
         if (cut.seg == 0 && t0 >= t1 && p.g.dS0) store4(p.g.dS0 + n * D * p.n, r);
-        while (te > t0) {
-            const int64_t start = cu[n];
-            int64_t ta = (te - 1) / kBack * kBack;
-            if (ta < start) ta = start;
-            if (ta < t0) ta = t0;
-            const int cnt = (int)(te - ta);
-            if (mine) {
-                for (int k = mr; k < cnt; k += G::kRows) {
-                    const int64_t t = ta + k;
-                    float v = Elem<T>::load(DT + t * p.in.lddt + base + mc) + bias;
-                    if (p.softplus) v = softplus(v);
-                    float dr = Elem<T>::load(DY + t * D + base + mc);
-                    if (Z) dr *= silu(Elem<T>::load(Z + t * p.in.ldz + base + mc));
-                    s.du[k][mc] = make_float2(v, v * Elem<T>::load(X + t * p.in.ldx + base + mc));
-                    s.dr[k][mc] = dr;
-                }
-            } else if (mr < G::kRows) {   // channels that are not there
-                for (int k = mr; k < cnt; k += G::kRows) {
-                    s.du[k][mc] = make_float2(0.f, 0.f);
-                    s.dr[k][mc] = 0.f;
-                }
-            }
-            for (int i = tid; i < kBack * NP; i += TH) {
-                const int k = i / NP, j = i % NP;
-                const bool in = k < cnt && j < p.n;
-                s.B[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.B) + (ta + k) * p.in.ldB +
-                                               (int64_t)g * p.n + j) : 0.f;
-                s.C[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.C) + (ta + k) * p.in.ldC +
-                                               (int64_t)g * p.n + j) : 0.f;
-            }
-            __syncthreads();
-            F2 h0[2][2];   // the state before token ta
-            if (ta == start) load4(p.S0 ? p.S0 + n * D * p.n : nullptr, h0);
-            else load4(p.states + ta / kBack * D * p.n, h0);
 
-            auto advance = [&](int k, F2 (&h)[2][2]) {
-                const float4 du = *reinterpret_cast<const float4*>(&s.du[k][2 * cp]);
-                const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.B[k][nl * 4]);
+        // my vectors of a tile: V channels of a row
+        auto row_of = [&](int i) { return (tid + i * TH) / VR; };
+        auto col_of = [&](int i) { return (tid + i * TH) % VR * V; };
+        // inputs of tokens [a, a + cnt), to shared memory
+        auto convert = [&](int64_t a, int cnt) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float dv = q ? du.z : du.x, uv = q ? du.w : du.y;
-                    const F2 dd = pack2(dv, dv), uu = pack2(uv, uv);
-                    h[q][0] = fma2(decay2(dd, A[q][0]), h[q][0], mul2(uu, b.x));
-                    h[q][1] = fma2(decay2(dd, A[q][1]), h[q][1], mul2(uu, b.y));
+            for (int i = 0; i < NI; ++i) {
+                const int k = row_of(i), c = col_of(i);
+                if (k >= cnt) continue;
+                const int64_t t = a + k;
+                if (c >= width) {   // channels that are not there
+#pragma unroll
+                    for (int q = 0; q < V; ++q) {
+                        s.du[k][q * VR + c / V] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        s.dr[k][q * VR + c / V] = make_float2(0.f, 0.f);
+                    }
+                    continue;
                 }
-            };
-            // tokens [from, to) of the tile, at most kSub, from state h: rebuilt, then backward
-            auto sub = [&](int from, int to, F2 (&h)[2][2]) {
-                F2 before[kSub][2][2];
+                Pack<T, V> kx, kd, kg, kz;
+                kx.load(X + t * p.in.ldx + base + c);
+                kd.load(DT + t * p.in.lddt + base + c);
+                kg.load(DY + t * D + base + c);
+                if (Z) kz.load(Z + t * p.in.ldz + base + c);
 #pragma unroll
-                for (int j = 0; j < kSub; ++j) {
-                    if (from + j < to) {
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            before[j][q][0] = h[q][0];
-                            before[j][q][1] = h[q][1];
-                        }
-                        advance(from + j, h);
-                        if (Z) {
-                            const ulonglong2 c =
-                                *reinterpret_cast<const ulonglong2*>(&s.C[from + j][nl * 4]);
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                float y = sum2(fma2(h[q][0], c.x, mul2(h[q][1], c.y)));
-#pragma unroll
-                                for (int o = 1; o < NL; o *= 2)
-                                    y += __shfl_xor_sync(0xffffffffu, y, o);
-                                if (nl == 0) s.y[from + j][2 * cp + q] = y;
-                            }
-                        }
-                    }
+                for (int q = 0; q < V; ++q) {
+                    float v = kd.get(q) + (p.dt_bias ? p.dt_bias[base + c + q] : 0.f);
+                    if (p.softplus) v = softplus(v);
+                    const float u = v * kx.get(q), dr = Z ? kg.get(q) * silu(kz.get(q)) : kg.get(q);
+                    s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
+                    s.dr[k][q * VR + c / V] = make_float2(dr, dr);
                 }
-#pragma unroll
-                for (int j = kSub - 1; j >= 0; --j) {
-                    if (from + j >= to) continue;
-                    const int k = from + j;
-                    const float4 du = *reinterpret_cast<const float4*>(&s.du[k][2 * cp]);
-                    const float2 dr = *reinterpret_cast<const float2*>(&s.dr[k][2 * cp]);
-                    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(&s.B[k][nl * 4]);
-                    const ulonglong2 c = *reinterpret_cast<const ulonglong2*>(&s.C[k][nl * 4]);
-                    F2 vB[2] = {0, 0}, vC[2] = {0, 0};
-                    float s1[2], s2[2];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float dv = q ? du.z : du.x, uv = q ? du.w : du.y;
-                        const float rv = q ? dr.y : dr.x;
-                        const F2 dd = pack2(dv, dv), uu = pack2(uv, uv), rr = pack2(rv, rv);
-                        F2 t1 = 0, t2 = 0;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const F2 a = decay2(dd, A[q][i]);
-                            const F2 gr = fma2(i ? c.y : c.x, rr, r[q][i]);   // gradient of h
-                            vC[i] = fma2(h[q][i], rr, vC[i]);
-                            vB[i] = fma2(gr, uu, vB[i]);
-                            t1 = fma2(gr, i ? b.y : b.x, t1);
-                            const F2 w = mul2(gr, mul2(a, before[j][q][i]));
-                            dA[q][i] = fma2(w, dd, dA[q][i]);
-                            t2 = fma2(w, A[q][i], t2);
-                            r[q][i] = mul2(a, gr);
-                            h[q][i] = before[j][q][i];
-                        }
-                        s1[q] = sum2(t1);
-                        s2[q] = sum2(t2);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-#pragma unroll
-                        for (int o = 1; o < NL; o *= 2) {
-                            s1[q] += __shfl_xor_sync(0xffffffffu, s1[q], o);
-                            s2[q] += __shfl_xor_sync(0xffffffffu, s2[q], o);
-                        }
-                        if (nl == 0) {
-                            s.s1[k][2 * cp + q] = s1[q];
-                            s.s2[k][2 * cp + q] = s2[q] * kLn2;
-                        }
-                    }
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float2 x = unpack2(vB[i]), y = unpack2(vC[i]);
-                        v[2 * i] = x.x;
-                        v[2 * i + 1] = x.y;
-                        v[4 + 2 * i] = y.x;
-                        v[4 + 2 * i + 1] = y.y;
-                    }
-                    const int at = sum_channels<NL>(v, lane);
-#pragma unroll
-                    for (int i = 0; i < kLeft<NL>; ++i) s.part[warp][k][(at + i) * NL + nl] = v[i];
-                }
-            };
-            // the tile's halves, the later one first
-            const int half = (int)(ta / kBack * kBack + kSub - ta);
-            if (half > 0 && half < cnt) {
-                F2 h[2][2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) h[q][i] = h0[q][i];
-                for (int k = 0; k < half; ++k) advance(k, h);
-                sub(half, cnt, h);
-                sub(0, half, h0);
-            } else {
-                sub(0, cnt, h0);
             }
-            __syncthreads();
-            if (mine) {
-                for (int k = mr; k < cnt; k += G::kRows) {
-                    const int64_t t = ta + k, at = t * D + base + mc;
-                    const float x = Elem<T>::load(X + t * p.in.ldx + base + mc);
-                    const float raw_dt = Elem<T>::load(DT + t * p.in.lddt + base + mc) + bias;
-                    const float s1 = s.s1[k][mc], dr = s.dr[k][mc], step = s.du[k][mc].x;
-                    float ddt = fmaf(x, s1, s.s2[k][mc]);
-                    if (p.softplus) ddt *= sigmoid(raw_dt);
-                    p.g.ddt[at] = ddt;
-                    p.g.dx[at] = fmaf(step, s1, skip * dr);
+            if (packed) {
+                for (int i = tid; i < 2 * kBack * NP / VB; i += TH) {
+                    const int which = i / (kBack * NP / VB), j = i % (kBack * NP / VB);
+                    const int k = j / (NP / VB), at = j % (NP / VB) * VB;
+                    Pack<T, VB> b;
+                    b.zero();
+                    if (k < cnt && at < p.n)
+                        b.load(static_cast<const T*>(which ? p.in.C : p.in.B) +
+                               (a + k) * (which ? p.in.ldC : p.in.ldB) + (int64_t)g * p.n + at);
+                    float* to = which ? &s.C[k][at] : &s.B[k][at];
+#pragma unroll
+                    for (int q = 0; q < VB; q += 4)
+                        *reinterpret_cast<float4*>(to + q) =
+                            make_float4(b.get(q), b.get(q + 1), b.get(q + 2), b.get(q + 3));
+                }
+            } else {
+                for (int i = tid; i < kBack * NP; i += TH) {
+                    const int k = i / NP, j = i % NP;
+                    const bool in = k < cnt && j < p.n;
+                    s.B[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.B) +
+                                                   (a + k) * p.in.ldB + (int64_t)g * p.n + j) : 0.f;
+                    s.C[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.C) +
+                                                   (a + k) * p.in.ldC + (int64_t)g * p.n + j) : 0.f;
+                }
+            }
+        };
+        // the gradients of tokens [a, a + cnt), whose sums are in shared memory
+        auto finish = [&](int64_t a, int cnt) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int k = row_of(i), c = col_of(i);
+                const bool in = k < cnt && c < width;
+                const int64_t t = a + k, at = t * D + base + c;
+                Pack<T, V> kx, kd, kg, kz;
+                if (in) {
+                    kx.load(X + t * p.in.ldx + base + c);
+                    kd.load(DT + t * p.in.lddt + base + c);
                     if (Z) {
-                        const float dy = Elem<T>::load(DY + at);
-                        const float z = Elem<T>::load(Z + t * p.in.ldz + base + mc);
-                        p.g.dz[at] = dy * fmaf(skip, x, s.y[k][mc]) * silu_grad(z);
+                        kz.load(Z + t * p.in.ldz + base + c);
+                        kg.load(DY + at);
                     }
-                    dskip = fmaf(dr, x, dskip);
-                    dbias += ddt;
+                }
+                float acc[2 * V];   // for dskip, for ddt_bias
+#pragma unroll
+                for (int q = 0; q < 2 * V; ++q) acc[q] = 0.f;
+                constexpr int U = V < 4 ? V : 4;
+#pragma unroll
+                for (int q0 = 0; q0 < V; q0 += U) {
+                    if (!in) continue;
+                    float dx[U], ddt[U], dz[U];
+#pragma unroll
+                    for (int j = 0; j < U; ++j) {
+                        const int q = q0 + j, sl = q * VR + c / V;
+                        const float skip = p.skip ? p.skip[base + c + q] : 0.f;
+                        const float x = kx.get(q), s1 = s.s[0][k][sl], dr = s.dr[k][sl].x;
+                        ddt[j] = fmaf(x, s1, s.s[1][k][sl] * kLn2);
+                        if (p.softplus)
+                            ddt[j] *= sigmoid(kd.get(q) + (p.dt_bias ? p.dt_bias[base + c + q] : 0.f));
+                        dx[j] = fmaf(s.du[k][sl].x, s1, skip * dr);
+                        if (Z) dz[j] = kg.get(q) * fmaf(skip, x, s.y[k][sl]) * silu_grad(kz.get(q));
+                        acc[q] = dr * x;
+                        acc[V + q] = ddt[j];
+                    }
+                    Pack<float, U> o;
+                    o.set(dx);
+                    o.store(p.g.dx + at + q0);
+                    o.set(ddt);
+                    o.store(p.g.ddt + at + q0);
+                    if (Z) {
+                        o.set(dz);
+                        o.store(p.g.dz + at + q0);
+                    }
+                }
+                // the rows of my warp, then the tiles before
+                const int first = spread_sum<2 * V, 16, VR < 32 ? VR : 32>(acc, lane);
+                constexpr int kLeftV = spread_left(2 * V, 16, VR < 32 ? VR : 32);
+                constexpr int kSame = 32 / (VR < 32 ? VR : 32) / (2 * V / kLeftV);   // lanes with one sum
+                if (kSame <= 1 || lane / VR % kSame == 0) {
+#pragma unroll
+                    for (int q = 0; q < kLeftV; ++q) {
+                        const int j = first + q;
+                        s.acc[j / V][warp][j % V * VR + c / V] += acc[q];
+                    }
                 }
             }
             // sums over the CTA's channels: to the outputs if it has the whole group
-            for (int i = tid; i < cnt * 8 * NL; i += TH) {
-                const int k = i / (8 * NL), j = i % (8 * NL);
-                const int v = j / NL, st = (j % NL) * 4 + (v & 3);
+            for (int i = tid; i < cnt * NP / 2; i += TH) {
+                const int k = i / (NP / 2), j = i % (NP / 2) * 4, st = j % NP;
                 if (st >= p.n) continue;
-                float sum = s.part[0][k][j];
+                const int row_at = (int)(a % kBack) + k;   // in the grid of parts
+                const int at = row_at % kSub * 2 * NP + j;
+                float4 v = *reinterpret_cast<const float4*>(&s.part[0][row_at / kSub][at]);
 #pragma unroll
-                for (int w = 1; w < G::kWarps; ++w) sum += s.part[w][k][j];
-                const int64_t row = (ta + k) * p.H + g;
-                if (cut.per_group == 1) (v < 4 ? p.g.dB : p.g.dC)[row * p.n + st] = sum;
-                else part_BC[((int64_t)cg * p.total_tokens * p.H + row) * 2 * p.n +
-                             (v < 4 ? 0 : p.n) + st] = sum;
+                for (int w = 1; w < G::kWarps; ++w) {
+                    const float4 u = *reinterpret_cast<const float4*>(&s.part[w][row_at / kSub][at]);
+                    v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+                }
+                const int64_t row = (a + k) * p.H + g;
+                float* to = cut.per_group == 1
+                                ? (j < NP ? p.g.dB : p.g.dC) + row * p.n + st
+                                : part_BC + ((int64_t)cg * p.total_tokens * p.H + row) * 2 * p.n +
+                                      (j < NP ? 0 : p.n) + st;
+                if (p.n % 4 == 0) {
+                    *reinterpret_cast<float4*>(to) = v;
+                } else {
+                    const float u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (st + q < p.n) to[q] = u[q];
+                }
+            }
+        };
+
+        struct Inputs {
+            F2 dd[2], uu[2];
+        };
+        auto inputs = [&](int k) {
+            Inputs v;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const ulonglong2 u =
+                    *reinterpret_cast<const ulonglong2*>(&s.du[k][slot + q * kOther]);
+                v.dd[q] = u.x;
+                v.uu[q] = u.y;
+            }
+            return v;
+        };
+        auto row4 = [&](const float (&m)[kBack][NP], int k) {
+            return *reinterpret_cast<const ulonglong2*>(&m[k][nl * 4]);
+        };
+        auto advance = [&](int k, F2 (&h)[2][2]) {
+            const Inputs v = inputs(k);
+            const ulonglong2 b = row4(s.B, k);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                h[q][0] = fma2(decay2(v.dd[q], A[q][0]), h[q][0], mul2(v.uu[q], b.x));
+                h[q][1] = fma2(decay2(v.dd[q], A[q][1]), h[q][1], mul2(v.uu[q], b.y));
+            }
+        };
+        // Tokens [from, to) of the tile, at most kSub, from state h: rebuilt, then backward.
+        auto sub = [&](auto whole, int from, int to, F2 (&h)[2][2], float* sums) {
+            F2 before[kSub][2][2];
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+                if (!whole.value && from + j >= to) break;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) before[j][q][i] = h[q][i];
+                advance(from + j, h);
+                if (Z) {
+                    const ulonglong2 c = row4(s.C, from + j);
+                    float y[2];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) y[q] = sum2(fma2(h[q][0], c.x, mul2(h[q][1], c.y)));
+                    const int at = spread_sum<2, NL / 2, 1>(y, lane);
+                    if (nl % (NL / 2) == 0) s.y[from + j][slot + at * kOther] = y[0];
+                }
+            }
+#pragma unroll
+            for (int j = kSub - 1; j >= 0; --j) {
+                if (!whole.value && from + j >= to) continue;
+                const int k = from + j;
+                const Inputs v = inputs(k);
+                const ulonglong2 b = row4(s.B, k), c = row4(s.C, k);
+                F2 vB[2] = {0, 0}, vC[2] = {0, 0}, t1[2] = {0, 0}, t2[2] = {0, 0};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const F2 rr = *reinterpret_cast<const F2*>(&s.dr[k][slot + q * kOther]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const F2 a = decay2(v.dd[q], A[q][i]);
+                        const F2 gr = fma2(i ? c.y : c.x, rr, r[q][i]);   // gradient of h
+                        vC[i] = fma2(h[q][i], rr, vC[i]);
+                        vB[i] = fma2(gr, v.uu[q], vB[i]);
+                        t1[q] = fma2(gr, i ? b.y : b.x, t1[q]);
+                        const F2 ag = mul2(a, gr), w = mul2(ag, before[j][q][i]);
+                        dA[q][i] = fma2(w, v.dd[q], dA[q][i]);
+                        t2[q] = fma2(w, A[q][i], t2[q]);
+                        r[q][i] = ag;
+                        h[q][i] = before[j][q][i];
+                    }
+                }
+                float sv[4] = {sum2(t1[0]), sum2(t1[1]), sum2(t2[0]), sum2(t2[1])};
+                const int sat = spread_sum<4, NL / 2, 1>(sv, lane);
+                constexpr int kLeftS = spread_left(4, NL / 2, 1);
+                if (NL <= 4 || nl % (NL > 4 ? NL / 4 : 1) == 0) {
+#pragma unroll
+                    for (int i = 0; i < kLeftS; ++i)
+                        s.s[(sat + i) / 2][k][slot + (sat + i) % 2 * kOther] = sv[i];
+                }
+                const float2 b0 = unpack2(vB[0]), b1 = unpack2(vB[1]);
+                const float2 e0 = unpack2(vC[0]), e1 = unpack2(vC[1]);
+                float bv[8] = {b0.x, b0.y, b1.x, b1.y, e0.x, e0.y, e1.x, e1.y};
+                const int at = spread_sum<8, 16, NL>(bv, lane);
+#pragma unroll
+                for (int i = 0; i < spread_left(8, 16, NL); ++i)
+                    sums[j * 2 * NP + (at + i) / 4 * NP + nl * 4 + (at + i) % 4] = bv[i];
+            }
+        };
+
+        // the tile that ends before token e of a sequence that starts at `start`
+        auto tile_start = [&](int64_t e, int64_t start) {
+            int64_t a = (e - 1) / kBack * kBack;
+            if (a < start) a = start;
+            return a < t0 ? t0 : a;
+        };
+        int64_t te = t1, ta = t0 < t1 ? tile_start(t1, cu[n]) : t0;
+        __syncthreads();
+        if (te > t0) convert(ta, (int)(te - ta));
+        while (te > t0) {
+            __syncthreads();
+            const int64_t start = cu[n];
+            const int cnt = (int)(te - ta);
+            // The tile in parts on the grid of kSub tokens: the states before all but the first are
+            // formed on one walk, then the parts are taken from the last one on.
+            const int off = (int)(ta % kBack);             // the tile's rows of the grid: from
+            const int p0 = off / kSub, p1 = (off + cnt - 1) / kSub;   // off on; its parts
+            const float* enters = ta == start ? (p.S0 ? p.S0 + n * D * p.n : nullptr)
+                                              : p.states + ta / kBack * D * p.n;
+            F2 h[2][2];
+            load4(enters, h);
+            auto place = [&](int part) { return reinterpret_cast<F2*>(s.part[warp][part]) + lane; };
+            auto keep = [&](int part) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) place(part)[i * 32] = h[i / 2][i % 2];
+            };
+            auto back_to = [&](int part) {
+                if (part == p0) {
+                    load4(enters, h);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) h[i / 2][i % 2] = place(part)[i * 32];
+                }
+                __syncwarp();   // the place takes the part's sums from here on
+            };
+            if (cnt == kBack) {
+#pragma unroll 1
+                for (int part = 1; part < kParts; ++part) {
+#pragma unroll
+                    for (int k = 0; k < kSub; ++k) advance((part - 1) * kSub + k, h);
+                    keep(part);
+                }
+#pragma unroll 1
+                for (int part = kParts - 1; part >= 0; --part) {
+                    back_to(part);
+                    sub(std::true_type(), part * kSub, (part + 1) * kSub, h, s.part[warp][part]);
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < cnt; ++k) {
+                    if (k > 0 && (off + k) % kSub == 0) keep((off + k) / kSub);
+                    if (k + 1 < cnt) advance(k, h);
+                }
+#pragma unroll 1
+                for (int part = p1; part >= p0; --part) {
+                    back_to(part);
+                    const int from = part == p0 ? 0 : part * kSub - off;
+                    const int to = part == p1 ? cnt : (part + 1) * kSub - off;
+                    sub(std::false_type(), from, to, h,
+                        s.part[warp][part] + (off + from) % kSub * 2 * NP);
+                }
             }
             __syncthreads();
+            finish(ta, cnt);
             te = ta;
             if (te == start) {
                 if (p.g.dS0) store4(p.g.dS0 + n * D * p.n, r);
@@ -964,29 +1076,24 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     load4(p.dS_T ? p.dS_T + n * D * p.n : nullptr, r);
                 }
             }
+            if (te > t0) {
+                ta = tile_start(te, cu[n]);
+                // (what finish reads of the inputs' places, the same threads write now; the
+                // sums' places are written behind the barrier)
+                convert(ta, (int)(te - ta));
+            }
         }
         store4(part_A + sg * D * p.n, dA);
-        // the threads of a channel, in order
-        if (G::kRows > 1) {
-            float* j = &s.y[0][0];
-            if (mr < G::kRows) {
-                j[mr * 2 * CH + mc] = dskip;
-                j[mr * 2 * CH + CH + mc] = dbias;
-            }
-            __syncthreads();
-            if (mr == 0) {
+        __syncthreads();
+        // the warps, in order
+        for (int i = tid; i < 2 * CH; i += TH) {
+            const int which = i / CH, sl = i % CH, c = sl % VR * V + sl / VR;
+            float sum = 0.f;
 #pragma unroll
-                for (int k = 1; k < G::kRows; ++k) {
-                    dskip += j[k * 2 * CH + mc];
-                    dbias += j[k * 2 * CH + CH + mc];
-                }
-            }
-            __syncthreads();
+            for (int w = 0; w < G::kWarps; ++w) sum += s.acc[which][w][sl];
+            if (c < width) part_c[sg * 2 * D + which * D + base + c] = sum;
         }
-        if (mine && mr == 0) {
-            part_c[sg * 2 * D + base + mc] = dskip;
-            part_c[sg * 2 * D + D + base + mc] = dbias;
-        }
+        __syncthreads();
     }
 }
 
@@ -1296,15 +1403,17 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
     }
     err = by_type(a.dtype, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
+        constexpr int V = 16 / sizeof(T);
+        const bool wide = a.d % V == 0 && rows_fit(a.in.x, a.in.ldx, D, sizeof(T), V) &&
+                          rows_fit(a.in.dt, a.in.lddt, D, sizeof(T), V) &&
+                          (!a.in.z || rows_fit(a.in.z, a.in.ldz, D, sizeof(T), V));
         return by_back_lanes(a.n, [&](auto l) {
             constexpr int NL = decltype(l)::value;
-            auto kernel = scan_bwd_kernel<T, NL>;
+            auto kernel = wide ? scan_bwd_kernel<T, NL, V> : scan_bwd_kernel<T, NL, 1>;
             constexpr int smem = sizeof(typename Back<NL>::Shared);
-            if (smem > 48 * 1024) {
-                const cudaError_t e = cudaFuncSetAttribute(
-                    kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-                if (e != cudaSuccess) return e;
-            }
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (e != cudaSuccess) return e;
             const int64_t most = (int64_t)1 << 30;
             const unsigned grid = (unsigned)(cut.items < 1 ? 1 : cut.items < most ? cut.items : most);
             kernel<<<grid, Back<NL>::kThreads, smem, stream>>>(a, cut, maps, part_A, part_c, part_BC,
