@@ -18,9 +18,10 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRun = 32;        // tokens a thread, forward
+constexpr int kMaxRun = 64;     // tokens a thread, forward
 constexpr int kBatch = 8;       // rows loaded at once
-constexpr int64_t kMaxParts = 2048;   // runs of the backward pass, at most
+constexpr int kBackBatch = 4;   // and of both tensors, backward
+constexpr int kMinParts = 256;  // runs of the backward pass, where there are tokens for them
 
 struct ConvGrid {
     int32_t nvec;      // vectors of V channels in a row
@@ -61,24 +62,13 @@ __device__ __forceinline__ Place place(const ConvGrid& g, int64_t block) {
 
 template <int W, int V>
 struct Window {
-    float x[W - 1][V];   // the last W - 1 inputs, oldest first
-    __device__ __forceinline__ void push(const float (&v)[V]) {
+    Lane<V> x[W - 1];   // the last W - 1 inputs, oldest first
+    __device__ __forceinline__ void push(const Lane<V>& v) {
 #pragma unroll
-        for (int j = 0; j + 1 < W - 1; ++j)
-#pragma unroll
-            for (int i = 0; i < V; ++i) x[j][i] = x[j + 1][i];
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[W - 2][i] = v[i];
+        for (int j = 0; j + 1 < W - 1; ++j) x[j] = x[j + 1];
+        x[W - 2] = v;
     }
 };
-
-template <typename T, int V>
-__device__ __forceinline__ void load_row(const void* p, int64_t at, float (&v)[V]) {
-    Pack<T, V> k;
-    k.load(static_cast<const T*>(p) + at);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = k.get(i);
-}
 
 // The inputs before token t of sequence n (first token `start`).
 template <typename T, int W, int V>
@@ -88,39 +78,81 @@ __device__ __forceinline__ void enter(const ConvArgs& p, int32_t n, int64_t star
     for (int j = 0; j < W - 1; ++j) {
         const int64_t row = t - (W - 1) + j;
         if (row >= start) {
-            load_row<T, V>(p.x, row * p.ldx + c, win.x[j]);
+            win.x[j] = load_lane<T, V>(p.x, row * p.ldx + c);
         } else if (p.S0) {
             const int64_t r = (int64_t)n * (W - 1) + (row - start + W - 1);
-            load_row<T, V>(p.S0, r * p.D + c, win.x[j]);
+            win.x[j] = load_lane<T, V>(p.S0, r * p.D + c);
         } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i) win.x[j][i] = 0.f;
+            win.x[j].zero();
         }
     }
 }
 
 template <int W, int V>
 struct Filter {
-    float w[W][V], b[V];
+    Lane<V> w[W], b;
     __device__ __forceinline__ void load(const float* wp, const float* bp, int32_t c) {
+        float f[V][W];
+        const float* from = wp + (int64_t)c * W;
+        if constexpr (W == 4) {   // one vector a channel
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+            for (int i = 0; i < V; ++i) {
+                const float4 u = reinterpret_cast<const float4*>(from)[i];
+                f[i][0] = u.x; f[i][1] = u.y; f[i][2] = u.z; f[i][W - 1] = u.w;
+            }
+        } else if constexpr (V % 4 == 0) {
+            float4 u[V * W / 4];
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j][i] = wp[(int64_t)(c + i) * W + j];
-            b[i] = bp ? bp[c + i] : 0.f;
+            for (int i = 0; i < V * W / 4; ++i) u[i] = reinterpret_cast<const float4*>(from)[i];
+#pragma unroll
+            for (int i = 0; i < V * W; ++i) {
+                const float4 t = u[i / 4];
+                f[i / W][i % W] = i % 4 == 0 ? t.x : i % 4 == 1 ? t.y : i % 4 == 2 ? t.z : t.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V * W; ++i) f[i / W][i % W] = from[i];
+        }
+#pragma unroll
+        for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int i = 0; i < Lane<V>::kPairs; ++i)
+                w[j].v[i] = pack2(f[2 * i][j], V > 1 ? f[2 * i + (V > 1 ? 1 : 0)][j] : 0.f);
+        b.zero();
+        if (!bp) return;
+        constexpr int U = V < 4 ? V : 4;
+#pragma unroll
+        for (int i = 0; i < V; i += U) {
+            Pack<float, U> k;
+            k.load(bp + c + i);
+#pragma unroll
+            for (int q = 0; q < U; q += 2)
+                b.v[(i + q) / 2] = pack2(k.get(q), U > 1 ? k.get(q + (U > 1 ? 1 : 0)) : 0.f);
         }
     }
-    __device__ __forceinline__ void apply(const Window<W, V>& win, const float (&x)[V],
-                                          float (&v)[V]) const {
+    __device__ __forceinline__ Lane<V> apply(const Window<W, V>& win, const Lane<V>& x) const {
+        Lane<V> v = b;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[i] = b[i];
-#pragma unroll
-            for (int j = 0; j < W - 1; ++j) v[i] = fmaf(w[j][i], win.x[j][i], v[i]);
-            v[i] = fmaf(w[W - 1][i], x[i], v[i]);
-        }
+        for (int j = 0; j < W - 1; ++j) v.fma(w[j], win.x[j]);
+        v.fma(w[W - 1], x);
+        return v;
     }
 };
+template <int V>
+__device__ __forceinline__ void activate(Lane<V>& v, int32_t on) {
+    if (!on) return;
+#pragma unroll
+    for (int i = 0; i < Lane<V>::kPairs; ++i) v.v[i] = silu2(v.v[i]);
+}
+// dy's way through the activation of v.
+template <int V>
+__device__ __forceinline__ Lane<V> activate_back(const Lane<V>& v, const Lane<V>& dy, int32_t on) {
+    if (!on) return dy;
+    Lane<V> d;
+#pragma unroll
+    for (int i = 0; i < Lane<V>::kPairs; ++i) d.v[i] = mul2(dy.v[i], silu_grad2(v.v[i]));
+    return d;
+}
 
 template <typename T, int W, int V>
 __global__ void __launch_bounds__(kThreads)
@@ -153,17 +185,11 @@ conv_fwd_kernel(const ConvArgs p, const ConvGrid g, int32_t* status) {
     f.load(p.w, p.b, c);
     Window<W, V> win;
     enter<T, W, V>(p, n, cu[n], t, c, win);
-    auto step = [&](const float (&x)[V], int64_t row) {
-        float v[V];
-        f.apply(win, x, v);
+    auto step = [&](const Lane<V>& x, int64_t row) {
+        Lane<V> v = f.apply(win, x);
         win.push(x);
-        if (p.silu) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) v[i] = silu(v[i]);
-        }
-        Pack<T, V> k;
-        k.set(v);
-        k.store(static_cast<T*>(p.y) + row * p.D + c);
+        activate(v, p.silu);
+        v.template to<T>().store(static_cast<T*>(p.y) + row * p.D + c);
     };
     while (true) {
         const int64_t end = cu[n + 1], to = end < stop ? end : stop;
@@ -174,17 +200,12 @@ conv_fwd_kernel(const ConvArgs p, const ConvGrid g, int32_t* status) {
                 k[r].load(static_cast<const T*>(p.x) + (t + r) * p.ldx + c);
 #pragma unroll
             for (int r = 0; r < kBatch; ++r) {
-                float x[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[i] = k[r].get(i);
+                Lane<V> x;
+                x.from(k[r]);
                 step(x, t + r);
             }
         }
-        for (; t < to; ++t) {
-            float x[V];
-            load_row<T, V>(p.x, t * p.ldx + c, x);
-            step(x, t);
-        }
+        for (; t < to; ++t) step(load_lane<T, V>(p.x, t * p.ldx + c), t);
         if (t >= stop) return;
         while (cu[n + 1] <= t) ++n;
         enter<T, W, V>(p, n, t, t, c, win);
@@ -204,13 +225,10 @@ conv_bwd_kernel(const ConvArgs p, const ConvGrid g, float* part, int32_t* status
     const int32_t c = at.c;
     const int64_t last = cu[p.num_seqs], first = at.run * g.run;
     const int64_t stop = first + g.run < last ? first + g.run : last;
-    float dw[W][V], db[V];
+    Lane<V> dw[W], db;
+    db.zero();
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        db[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
-    }
+    for (int j = 0; j < W; ++j) dw[j].zero();
     if (first < stop) {
         int64_t t = first;
         int32_t n = sequence_of(cu, p.num_seqs, t);
@@ -223,64 +241,50 @@ conv_bwd_kernel(const ConvArgs p, const ConvGrid g, float* part, int32_t* status
             // tokens whose inputs' gradients this run writes: from `from` on, up to `to`
             const int64_t from = t, to = end < stop ? end : stop;
             const int64_t walk = to + W - 1 < end ? to + W - 1 : end;
-            float acc[W][V];   // gradients of inputs t - W + 1 .. t, not complete yet
+            Lane<V> acc[W];   // gradients of inputs t - W + 1 .. t, not complete yet
 #pragma unroll
-            for (int j = 0; j < W; ++j)
-#pragma unroll
-                for (int i = 0; i < V; ++i) acc[j][i] = 0.f;
-            auto emit = [&](const float (&v)[V], int64_t row) {
-                Pack<float, V> k;
-                k.set(v);
-                k.store(p.dx + row * p.D + c);
+            for (int j = 0; j < W; ++j) acc[j].zero();
+            auto emit = [&](const Lane<V>& v, int64_t row) {
+                v.template to<float>().store(p.dx + row * p.D + c);
             };
-            auto step = [&](const float (&x)[V], const float (&dy)[V], bool own) {
-                float v[V], dv[V];
-                f.apply(win, x, v);
+            auto step = [&](const Lane<V>& x, const Lane<V>& dy, bool own) {
+                const Lane<V> dv = activate_back(f.apply(win, x), dy, p.silu);
+                if (own) {
+                    db.add(dv);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    dv[i] = p.silu ? dy[i] * silu_grad(v[i]) : dy[i];
-                    if (own) {
-                        db[i] += dv[i];
-#pragma unroll
-                        for (int j = 0; j < W - 1; ++j) dw[j][i] = fmaf(dv[i], win.x[j][i], dw[j][i]);
-                        dw[W - 1][i] = fmaf(dv[i], x[i], dw[W - 1][i]);
-                    }
-#pragma unroll
-                    for (int j = 0; j + 1 < W; ++j) acc[j][i] = acc[j + 1][i];
-                    acc[W - 1][i] = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) acc[j][i] = fmaf(f.w[j][i], dv[i], acc[j][i]);
+                    for (int j = 0; j < W - 1; ++j) dw[j].fma(dv, win.x[j]);
+                    dw[W - 1].fma(dv, x);
                 }
+#pragma unroll
+                for (int j = 0; j + 1 < W; ++j) acc[j] = acc[j + 1];
+                acc[W - 1].zero();
+#pragma unroll
+                for (int j = 0; j < W; ++j) acc[j].fma(f.w[j], dv);
                 win.push(x);
             };
-            for (; t < walk; ++t) {
-                if (t - (W - 1) >= from && t + kBatch / 2 <= to) {
-                    Pack<T, V> kx[kBatch / 2], kd[kBatch / 2];
-#pragma unroll
-                    for (int r = 0; r < kBatch / 2; ++r) {
-                        kx[r].load(static_cast<const T*>(p.x) + (t + r) * p.ldx + c);
-                        kd[r].load(static_cast<const T*>(p.dy) + (t + r) * p.D + c);
-                    }
-#pragma unroll
-                    for (int r = 0; r < kBatch / 2; ++r) {
-                        float x[V], dy[V];
-#pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            x[i] = kx[r].get(i);
-                            dy[i] = kd[r].get(i);
-                        }
-                        step(x, dy, true);
-                        emit(acc[0], t + r - (W - 1));
-                    }
-                    t += kBatch / 2 - 1;
-                    continue;
-                }
-                float x[V], dy[V];
-                load_row<T, V>(p.x, t * p.ldx + c, x);
-                load_row<T, V>(p.dy, t * p.D + c, dy);
-                step(x, dy, t < to);
+            auto one = [&]() {
+                step(load_lane<T, V>(p.x, t * p.ldx + c), load_lane<T, V>(p.dy, t * p.D + c), t < to);
                 if (t - (W - 1) >= from) emit(acc[0], t - (W - 1));
+                ++t;
+            };
+            while (t < walk && t - (W - 1) < from) one();
+            for (; t + kBackBatch <= to; t += kBackBatch) {
+                Pack<T, V> kx[kBackBatch], kd[kBackBatch];
+#pragma unroll
+                for (int r = 0; r < kBackBatch; ++r) {
+                    kx[r].load(static_cast<const T*>(p.x) + (t + r) * p.ldx + c);
+                    kd[r].load(static_cast<const T*>(p.dy) + (t + r) * p.D + c);
+                }
+#pragma unroll
+                for (int r = 0; r < kBackBatch; ++r) {
+                    Lane<V> x, dy;
+                    x.from(kx[r]);
+                    dy.from(kd[r]);
+                    step(x, dy, true);
+                    emit(acc[0], t + r - (W - 1));
+                }
             }
+            while (t < walk) one();
             // at a sequence's end nothing more is added to its last inputs
             if (walk == end) {
 #pragma unroll
@@ -295,13 +299,11 @@ conv_bwd_kernel(const ConvArgs p, const ConvGrid g, float* part, int32_t* status
             enter<T, W, V>(p, n, t, t, c, win);
         }
     }
-    float* row = part + at.run * ((int64_t)p.D * (W + 1));
+    // part[run]: dw by weight, then db
+    float* row = part + at.run * ((int64_t)p.D * (W + 1)) + c;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-#pragma unroll
-        for (int j = 0; j < W; ++j) row[(int64_t)(c + i) * W + j] = dw[j][i];
-        row[(int64_t)p.D * W + c + i] = db[i];
-    }
+    for (int j = 0; j < W; ++j) dw[j].template to<float>().store(row + (int64_t)j * p.D);
+    db.template to<float>().store(row + (int64_t)W * p.D);
 }
 
 // The ends of the sequences: dS_T goes to the last inputs, be they tokens or stored ones, and
@@ -337,50 +339,60 @@ conv_edge_kernel(const ConvArgs p, const int32_t* status) {
 #pragma unroll
     for (int t = 0; t < W - 1; ++t) {
         if (t >= len) break;
-        float x[1], dy[1], v[1];
-        load_row<T, 1>(p.x, (start + t) * p.ldx + c, x);
-        load_row<T, 1>(p.dy, (start + t) * p.D + c, dy);
-        f.apply(win, x, v);
+        const Lane<1> x = load_lane<T, 1>(p.x, (start + t) * p.ldx + c);
+        const Lane<1> dy = load_lane<T, 1>(p.dy, (start + t) * p.D + c);
+        const Lane<1> dv = activate_back(f.apply(win, x), dy, p.silu);
         win.push(x);
-        const float dv = p.silu ? dy[0] * silu_grad(v[0]) : dy[0];
 #pragma unroll
-        for (int r = t; r < W - 1; ++r) g[r] = fmaf(f.w[r - t][0], dv, g[r]);
+        for (int r = t; r < W - 1; ++r)
+            g[r] = fmaf(unpack2(f.w[r - t].v[0]).x, unpack2(dv.v[0]).x, g[r]);
     }
 #pragma unroll
     for (int r = 0; r < W - 1; ++r) p.dS0[((int64_t)n * (W - 1) + r) * p.D + c] = g[r];
 }
 
-// One token a row.  A thread reads all it needs of the state before it writes any.
+// One token a row, kStepRows rows a thread with the same weights.  A thread reads all it needs of
+// a state before it writes any.
+constexpr int kStepRows = 2;
 template <typename T, int W, int V>
-__global__ void __launch_bounds__(kThreads) conv_step_kernel(const ConvStepArgs p, int32_t nvec) {
+__global__ void __launch_bounds__(kThreads)
+conv_step_kernel(const ConvStepArgs p, int32_t nvec, int32_t rows) {
     const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int32_t b = (int32_t)(i / nvec), c = (int32_t)(i - (int64_t)b * nvec) * V;
-    if (b >= p.B) return;
-    const int32_t row = p.parents ? p.parents[b] : b;
-    const bool live = row >= 0 && row < p.num_rows;
-    Pack<T, V> s[W];
+    const int32_t r = (int32_t)(i / nvec), c = (int32_t)(i - (int64_t)r * nvec) * V;
+    if (r >= rows) return;
+    Pack<T, V> s[kStepRows][W];
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        if (live) s[j].load(static_cast<const T*>(p.S) + ((int64_t)row * (W - 1) + j) * p.D + c);
-        else s[j].zero();
+    for (int q = 0; q < kStepRows; ++q) {
+        const int64_t b = (int64_t)q * rows + r;
+        if (b >= p.B) break;
+        const int32_t row = p.parents ? p.parents[b] : (int32_t)b;
+        const bool live = row >= 0 && row < p.num_rows;
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j) {
+            if (live)
+                s[q][j].load(static_cast<const T*>(p.S) + ((int64_t)row * (W - 1) + j) * p.D + c);
+            else s[q][j].zero();
+        }
+        s[q][W - 1].load(static_cast<const T*>(p.x) + b * p.ldx + c);
     }
-    s[W - 1].load(static_cast<const T*>(p.x) + b * p.ldx + c);
     Filter<W, V> f;
     f.load(p.w, p.b, c);
-    float v[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        v[k] = f.b[k];
+    for (int q = 0; q < kStepRows; ++q) {
+        const int64_t b = (int64_t)q * rows + r;
+        if (b >= p.B) break;
+        Window<W, V> win;
+        Lane<V> x;
 #pragma unroll
-        for (int j = 0; j < W; ++j) v[k] = fmaf(f.w[j][k], s[j].get(k), v[k]);
-        if (p.silu) v[k] = silu(v[k]);
+        for (int j = 0; j < W - 1; ++j) win.x[j].from(s[q][j]);
+        x.from(s[q][W - 1]);
+        Lane<V> v = f.apply(win, x);
+        activate(v, p.silu);
+        v.template to<T>().store(static_cast<T*>(p.y) + b * p.D + c);
+#pragma unroll
+        for (int j = 0; j < W - 1; ++j)
+            s[q][j + 1].store(static_cast<T*>(p.S_out) + (b * (W - 1) + j) * p.D + c);
     }
-    Pack<T, V> y;
-    y.set(v);
-    y.store(static_cast<T*>(p.y) + (int64_t)b * p.D + c);
-#pragma unroll
-    for (int j = 0; j < W - 1; ++j)
-        s[j + 1].store(static_cast<T*>(p.S_out) + ((int64_t)b * (W - 1) + j) * p.D + c);
 }
 
 constexpr int kSumCols = 32, kSumRows = 8;
@@ -388,7 +400,7 @@ constexpr int kSumCols = 32, kSumRows = 8;
 // sums are added in order.
 __global__ void __launch_bounds__(kSumCols * kSumRows)
 column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t n1, int64_t n2,
-                  float* out1, float* out2, const int32_t* status) {
+                  float* out1, float* out2, const int32_t* status, int32_t turned) {
     if (status && *status != KDA_OK) return;
     __shared__ float s[kSumRows][kSumCols];
     const int cl = threadIdx.x % kSumCols, rl = threadIdx.x / kSumCols;
@@ -410,7 +422,9 @@ column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t n1, int6
 #pragma unroll
     for (int k = 1; k < kSumRows; ++k) sum += s[k][cl];
     float* out = col < n1 ? out1 : out2;
-    if (out) out[col < n1 ? col : col - n1] = sum;
+    const int64_t at = col >= n1 ? col - n1
+                       : turned > 1 ? col % (n1 / turned) * turned + col / (n1 / turned) : col;
+    if (out) out[at] = sum;
 }
 
 __global__ void __launch_bounds__(1024)
@@ -440,20 +454,22 @@ cudaError_t by_type(kda_dtype dtype, int W, F&& f) {
     return dtype == KDA_BF16 ? pick((__nv_bfloat16*)nullptr) : pick((float*)nullptr);
 }
 
-// Tokens of a backward run.
+// Tokens of a backward run: 32, or more where that leaves kMinParts runs or more, so that their
+// partial sums are few.
 int backward_run(int64_t T) {
-    const int64_t r = (T + kMaxParts - 1) / kMaxParts;
-    return (int)(r < 32 ? 32 : r);
+    int64_t r = 32;
+    while (r < 128 && T / (2 * r) >= kMinParts) r *= 2;
+    while (T / r > 8 * kMinParts) r *= 2;
+    return (int)r;
 }
 
 }  // namespace
 
 cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t n1, int64_t n2,
                                float* out1, float* out2, const int32_t* status,
-                               cudaStream_t stream) {
+                               cudaStream_t stream, int32_t turned) {
     const int64_t blocks = (n1 + n2 + kSumCols - 1) / kSumCols;
-    column_sum_kernel<<<(unsigned)blocks, kSumCols * kSumRows, 0, stream>>>(part, rows, n1, n2,
-                                                                            out1, out2, status);
+    column_sum_kernel<<<(unsigned)blocks, kSumCols * kSumRows, 0, stream>>>(part, rows, n1, n2, out1, out2, status, turned);
     return cudaGetLastError();
 }
 
@@ -487,11 +503,18 @@ cudaError_t launch_conv_prefill(const ConvArgs& a, char* ws, cudaStream_t stream
     return by_type(a.dtype, a.W, [&](auto* t, auto w) {
         using T = std::remove_pointer_t<decltype(t)>;
         constexpr int W = decltype(w)::value;
-        const bool wide = rows_fit(a.x, a.ldx, a.D, esz, 4);
-        const ConvGrid g = conv_grid(a.total_tokens, a.D, wide ? 4 : 1, kRun);
+        constexpr int V = 16 / sizeof(T);
+        const bool wide = rows_fit(a.x, a.ldx, a.D, esz, V);
+        // the longest runs that leave each SM 512 threads or more: a run reads W - 1 rows of
+        // the one before it again, short ones spread few tokens over the GPU
+        int run = kMaxRun;
+        while (run > kBatch && (a.total_tokens + run - 1) / run * ((a.D + (wide ? V - 1 : 0)) / (wide ? V : 1)) <
+                                   512 * (int64_t)(sm_count() > 0 ? sm_count() : 1))
+            run /= 2;
+        const ConvGrid g = conv_grid(a.total_tokens, a.D, wide ? V : 1, run);
         const int64_t copies = (int64_t)a.num_seqs * (W - 1) * g.nvec;
         const int64_t blocks = g.main + (copies + kThreads - 1) / kThreads;
-        auto kernel = wide ? conv_fwd_kernel<T, W, 4> : conv_fwd_kernel<T, W, 1>;
+        auto kernel = wide ? conv_fwd_kernel<T, W, V> : conv_fwd_kernel<T, W, 1>;
         kernel<<<(unsigned)(blocks > 0 ? blocks : 1), kThreads, 0, stream>>>(b, g, status);
         return cudaGetLastError();
     });
@@ -520,7 +543,7 @@ cudaError_t launch_conv_backward(const ConvArgs& a, char* ws, cudaStream_t strea
     if (err != cudaSuccess) return err;
     const int run = backward_run(a.total_tokens);
     return launch_column_sums(part, (a.total_tokens + run - 1) / run, (int64_t)a.D * a.W, a.D, a.dw,
-                              a.db, status, stream);
+                              a.db, status, stream, a.W);
 }
 
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream) {
@@ -530,9 +553,10 @@ cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream) {
         constexpr int W = decltype(w)::value;
         const bool wide = rows_fit(a.x, a.ldx, a.D, esz, 4);
         const int32_t nvec = a.D / (wide ? 4 : 1);
-        const int64_t blocks = ((int64_t)a.B * nvec + kThreads - 1) / kThreads;
+        const int32_t rows = (a.B + kStepRows - 1) / kStepRows;
+        const int64_t blocks = ((int64_t)rows * nvec + kThreads - 1) / kThreads;
         auto kernel = wide ? conv_step_kernel<T, W, 4> : conv_step_kernel<T, W, 1>;
-        kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, nvec);
+        kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, nvec, rows);
         return cudaGetLastError();
     });
 }

@@ -50,6 +50,20 @@ __device__ __forceinline__ float activate_grad(float v, int act) {
     return 1.f;
 }
 
+// act(v) of a pair, and its slope.
+__device__ __forceinline__ F2 activate2(F2 v, int act) {
+    return act == GROUPNORM_SILU ? silu2(v) : act == GROUPNORM_SIGMOID ? sigmoid2(v) : v;
+}
+__device__ __forceinline__ F2 activate_grad2(F2 v, int act) {
+    if (act == GROUPNORM_SILU) return silu_grad2(v);
+    if (act == GROUPNORM_SIGMOID) {
+        const F2 s = sigmoid2(v);
+        return mul2(s, fma2(s, both(-1.f), both(1.f)));
+    }
+    return both(1.f);
+}
+
+// A row as stored: the vectors lane, lane + lanes, ..
 template <typename T, int V, int NV>
 struct Row {
     Pack<T, V> k[NV];
@@ -57,38 +71,39 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = lane + j * lanes;
-            if (on && v < nvec) k[j].load(p + (int64_t)v * V);
+            if (on && v < nvec) k[j].load(p + v * V);
             else k[j].zero();
         }
     }
-    __device__ __forceinline__ float get(int j, int i) const { return k[j].get(i); }
 };
 
 // xh of one row, and its r.
 template <typename T, int V, int NV>
-__device__ __forceinline__ float normalise(const Row<T, V, NV>& x, float (&xh)[NV][V], int lane,
-                                           int lanes, int nvec, int d, bool center, float eps) {
-    float m = 0.f;
+__device__ __forceinline__ float normalise(const Row<T, V, NV>& x, Lane<V> (&xh)[NV], int lane,
+                                           int lanes, int nvec, float inv_d, bool center,
+                                           float eps) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j) xh[j].from(x.k[j]);
     if (center) {
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) m += xh[j].sum();
+        const F2 mean = both(-group_sum(m, lanes) * inv_d);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) m += x.get(j, i);
-        m = group_sum(m, lanes) / d;
+            for (int i = 0; i < Lane<V>::kPairs; ++i)
+                xh[j].v[i] = lane + j * lanes < nvec ? add2(xh[j].v[i], mean) : 0;
     }
-    float q = 0.f;
+    Lane<V> q;
+    q.zero();
+#pragma unroll
+    for (int j = 0; j < NV; ++j) q.fma(xh[j], xh[j]);
+    const float r = 1.f / sqrtf(group_sum(q.sum(), lanes) * inv_d + eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            xh[j][i] = lane + j * lanes < nvec ? x.get(j, i) - m : 0.f;
-            q = fmaf(xh[j][i], xh[j][i], q);
-        }
-    const float r = 1.f / sqrtf(group_sum(q, lanes) / d + eps);
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) xh[j][i] *= r;
+        for (int i = 0; i < Lane<V>::kPairs; ++i) xh[j].v[i] = mul2(xh[j].v[i], both(r));
     return r;
 }
 
@@ -111,47 +126,83 @@ __device__ __forceinline__ NormPlace norm_place(const NormArgs& p, const NormGri
     return a;
 }
 
+// The parameters of a lane's channels.
+template <int V, int NV>
+__device__ __forceinline__ void load_params(const NormArgs& p, const NormPlace& a, int lanes,
+                                            int nvec, Lane<V> (&w)[NV], Lane<V> (&b)[NV]) {
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < Lane<V>::kPairs; ++i) {
+            const int v = a.lane + j * lanes;
+            const bool in = a.on && v < nvec;
+            const int64_t at = (p.param_heads == 1 ? 0 : (int64_t)a.h * p.d) + v * V + 2 * i;
+            constexpr int o = V > 1 ? 1 : 0;
+            w[j].v[i] = in && p.w ? pack2(p.w[at], p.w[at + o]) : both(1.f);
+            b[j].v[i] = in && p.b ? pack2(p.b[at], p.b[at + o]) : 0;
+        }
+}
+
+// The rows of the next token are loaded while this one's are worked on.
 template <typename T, int V, int NV>
 __global__ void __launch_bounds__(kThreads)
 norm_fwd_kernel(const NormArgs p, const NormGrid g) {
     const NormPlace a = norm_place(p, g);
     const int nvec = p.d / V;
-    float w[NV][V], b[NV][V];
-#pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = a.lane + j * g.lanes;
-            const bool in = a.on && v < nvec;
-            const int64_t at = (p.param_heads == 1 ? 0 : (int64_t)a.h * p.d) + v * V + i;
-            w[j][i] = in && p.w ? p.w[at] : 1.f;
-            b[j][i] = in && p.b ? p.b[at] : 0.f;
-        }
+    const float inv_d = 1.f / p.d;
+    Lane<V> w[NV], b[NV];
+    load_params(p, a, g.lanes, nvec, w, b);
+    const T* px = static_cast<const T*>(p.x) + a.t * p.ldx + (int64_t)a.h * p.d;
+    const T* pz = static_cast<const T*>(p.z) + a.t * p.ldz + (int64_t)a.h * p.d;
+    T* y = static_cast<T*>(p.y) + (a.t * p.H + a.h) * p.d;
+    Row<T, V, NV> x, z, nx, nz;
+    bool on = a.on && a.t < p.T;
+    x.load(px, a.lane, g.lanes, nvec, on);
+    if (p.z) z.load(pz, a.lane, g.lanes, nvec, on);
     // (all lanes of a warp take part in its sums, so they leave the loop together)
-    for (int64_t t = a.t; __any_sync(0xffffffffu, a.on && t < p.T); t += a.step) {
-        const bool on = a.on && t < p.T;
-        Row<T, V, NV> x, z;
-        x.load(static_cast<const T*>(p.x) + t * p.ldx + (int64_t)a.h * p.d, a.lane, g.lanes, nvec,
-               on);
-        if (p.z)
-            z.load(static_cast<const T*>(p.z) + t * p.ldz + (int64_t)a.h * p.d, a.lane, g.lanes,
-                   nvec, on);
-        float xh[NV][V];
-        normalise(x, xh, a.lane, g.lanes, nvec, p.d, p.center, p.eps);
-        T* y = static_cast<T*>(p.y) + (t * p.H + a.h) * p.d;
+    for (int64_t t = a.t; __any_sync(0xffffffffu, on); t += a.step) {
+        const bool next = a.on && t + a.step < p.T;
+        px += a.step * p.ldx;
+        nx.load(px, a.lane, g.lanes, nvec, next);
+        if (p.z) {
+            pz += a.step * p.ldz;
+            nz.load(pz, a.lane, g.lanes, nvec, next);
+        }
+        Lane<V> xh[NV];
+        normalise(x, xh, a.lane, g.lanes, nvec, inv_d, p.center, p.eps);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = a.lane + j * g.lanes;
-            float o[V];
+            Lane<V> o, zv;
+            if (p.z) zv.from(z.k[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float n = fmaf(xh[j][i], w[j][i], b[j][i]);
-                o[i] = p.z ? n * activate(z.get(j, i), p.act) : activate(n, p.act);
+            for (int i = 0; i < Lane<V>::kPairs; ++i) {
+                const F2 n = fma2(xh[j].v[i], w[j].v[i], b[j].v[i]);
+                o.v[i] = p.z ? mul2(n, activate2(zv.v[i], p.act)) : activate2(n, p.act);
             }
-            Pack<T, V> k;
-            k.set(o);
-            if (on && v < nvec) k.store(y + (int64_t)v * V);
+            if (on && v < nvec) o.template to<T>().store(y + v * V);
         }
+        y += a.step * p.H * p.d;
+        x = nx;
+        z = nz;
+        on = next;
+    }
+}
+
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, const Lane<V>& l) {
+    constexpr int U = V < 4 ? V : 4;
+#pragma unroll
+    for (int i = 0; i < V; i += U) {
+        float f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float2 t = unpack2(l.v[(i + u) / 2]);
+            f[u] = u % 2 ? t.y : t.x;
+        }
+        Pack<float, U> k;
+        k.set(f);
+        k.store(p + i);
     }
 }
 
@@ -160,84 +211,84 @@ __global__ void __launch_bounds__(kThreads)
 norm_bwd_kernel(const NormArgs p, const NormGrid g, float* part) {
     const NormPlace a = norm_place(p, g);
     const int nvec = p.d / V;
-    float w[NV][V], b[NV][V], dw[NV][V], db[NV][V];
+    const float inv_d = 1.f / p.d;
+    Lane<V> w[NV], b[NV], dw[NV], db[NV];
+    load_params(p, a, g.lanes, nvec, w, b);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int v = a.lane + j * g.lanes;
-            const bool in = a.on && v < nvec;
-            const int64_t at = (p.param_heads == 1 ? 0 : (int64_t)a.h * p.d) + v * V + i;
-            w[j][i] = in && p.w ? p.w[at] : 1.f;
-            b[j][i] = in && p.b ? p.b[at] : 0.f;
-            dw[j][i] = db[j][i] = 0.f;
-        }
-    for (int64_t t = a.t; __any_sync(0xffffffffu, a.on && t < p.T); t += a.step) {
-        const bool on = a.on && t < p.T;
-        const int64_t out = (t * p.H + a.h) * p.d;
-        Row<T, V, NV> x, z, dy;
-        x.load(static_cast<const T*>(p.x) + t * p.ldx + (int64_t)a.h * p.d, a.lane, g.lanes, nvec,
-               on);
-        dy.load(static_cast<const T*>(p.dy) + out, a.lane, g.lanes, nvec, on);
-        if (p.z)
-            z.load(static_cast<const T*>(p.z) + t * p.ldz + (int64_t)a.h * p.d, a.lane, g.lanes,
-                   nvec, on);
-        float xh[NV][V], gv[NV][V];
-        const float r = normalise(x, xh, a.lane, g.lanes, nvec, p.d, p.center, p.eps);
-        float s1 = 0.f, s2 = 0.f;   // sums of g xh and of g
+    for (int j = 0; j < NV; ++j) {
+        dw[j].zero();
+        db[j].zero();
+    }
+    const T* px = static_cast<const T*>(p.x) + a.t * p.ldx + (int64_t)a.h * p.d;
+    const T* pz = static_cast<const T*>(p.z) + a.t * p.ldz + (int64_t)a.h * p.d;
+    int64_t out = (a.t * p.H + a.h) * p.d;
+    const int64_t stride = a.step * p.H * p.d;
+    constexpr bool kAhead = NV <= 2;   // (wider rows leave no registers for the next)
+    Row<T, V, NV> x, z, dy, nx, nz, ndy;
+    bool on = a.on && a.t < p.T;
+    auto load = [&](Row<T, V, NV>& rx, Row<T, V, NV>& rz, Row<T, V, NV>& rd, const T* x_,
+                    const T* z_, int64_t at, bool live) {
+        rx.load(x_, a.lane, g.lanes, nvec, live);
+        rd.load(static_cast<const T*>(p.dy) + at, a.lane, g.lanes, nvec, live);
+        if (p.z) rz.load(z_, a.lane, g.lanes, nvec, live);
+    };
+    if (kAhead) load(x, z, dy, px, pz, out, on);
+    for (int64_t t = a.t; __any_sync(0xffffffffu, on); t += a.step) {
+        const bool next = a.on && t + a.step < p.T;
+        if (kAhead)
+            load(nx, nz, ndy, px + a.step * p.ldx, pz + a.step * p.ldz, out + stride, next);
+        else
+            load(x, z, dy, px, pz, out, on);
+        Lane<V> xh[NV], gv[NV];
+        const float r = normalise(x, xh, a.lane, g.lanes, nvec, inv_d, p.center, p.eps);
+        Lane<V> q1, q2;   // g xh and g
+        q1.zero();
+        q2.zero();
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = a.lane + j * g.lanes;
-            float dz[V];
+            Lane<V> zv, dv, dz;
+            dv.from(dy.k[j]);
+            if (p.z) zv.from(z.k[j]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float n = fmaf(xh[j][i], w[j][i], b[j][i]);
-                float dv;
+            for (int i = 0; i < Lane<V>::kPairs; ++i) {
+                const F2 n = fma2(xh[j].v[i], w[j].v[i], b[j].v[i]);
                 if (p.z) {
-                    const float zv = z.get(j, i);
-                    dv = dy.get(j, i) * activate(zv, p.act);
-                    dz[i] = dy.get(j, i) * n * activate_grad(zv, p.act);
+                    dz.v[i] = mul2(mul2(dv.v[i], n), activate_grad2(zv.v[i], p.act));
+                    dv.v[i] = mul2(dv.v[i], activate2(zv.v[i], p.act));
                 } else {
-                    dv = dy.get(j, i) * activate_grad(n, p.act);
-                    dz[i] = 0.f;
+                    dv.v[i] = mul2(dv.v[i], activate_grad2(n, p.act));
                 }
-                dw[j][i] = fmaf(dv, xh[j][i], dw[j][i]);
-                db[j][i] += dv;
-                gv[j][i] = dv * w[j][i];
-                s1 = fmaf(gv[j][i], xh[j][i], s1);
-                s2 += gv[j][i];
+                gv[j].v[i] = mul2(dv.v[i], w[j].v[i]);
             }
-            if (p.dz && on && v < nvec) {
-#pragma unroll
-                for (int i = 0; i < V; i += V < 4 ? V : 4) {
-                    constexpr int U = V < 4 ? V : 4;
-                    Pack<float, U> k;
-                    float o[U];
-#pragma unroll
-                    for (int u = 0; u < U; ++u) o[u] = dz[i + u];
-                    k.set(o);
-                    k.store(p.dz + out + (int64_t)v * V + i);
-                }
-            }
+            dw[j].fma(dv, xh[j]);
+            db[j].add(dv);
+            q1.fma(gv[j], xh[j]);
+            q2.add(gv[j]);
+            if (p.dz && on && v < nvec) store_f32(p.dz + out + v * V, dz);
         }
-        s1 = group_sum(s1, g.lanes) / p.d;
-        s2 = p.center ? group_sum(s2, g.lanes) / p.d : 0.f;
+        const float s1 = group_sum(q1.sum(), g.lanes) * inv_d;
+        const float s2 = p.center ? group_sum(q2.sum(), g.lanes) * inv_d : 0.f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int v = a.lane + j * g.lanes;
-            if (!on || v >= nvec) continue;
+            Lane<V> dx;
 #pragma unroll
-            for (int i = 0; i < V; i += V < 4 ? V : 4) {
-                constexpr int U = V < 4 ? V : 4;
-                Pack<float, U> k;
-                float o[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    o[u] = r * (gv[j][i + u] - fmaf(xh[j][i + u], s1, s2));
-                k.set(o);
-                k.store(p.dx + out + (int64_t)v * V + i);
+            for (int i = 0; i < Lane<V>::kPairs; ++i) {   // r (g - (xh s1 + s2))
+                const F2 off = fma2(xh[j].v[i], both(s1), both(s2));
+                dx.v[i] = mul2(fma2(off, both(-1.f), gv[j].v[i]), both(r));
             }
+            if (on && v < nvec) store_f32(p.dx + out + v * V, dx);
         }
+        px += a.step * p.ldx;
+        pz += a.step * p.ldz;
+        out += stride;
+        if (kAhead) {
+            x = nx;
+            z = nz;
+            dy = ndy;
+        }
+        on = next;
     }
     if (!part || !a.on) return;
     // part[token part][head][dw, db][d]
@@ -246,11 +297,8 @@ norm_bwd_kernel(const NormArgs p, const NormGrid g, float* part) {
     for (int j = 0; j < NV; ++j) {
         const int v = a.lane + j * g.lanes;
         if (v >= nvec) continue;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            row[v * V + i] = dw[j][i];
-            row[p.d + v * V + i] = db[j][i];
-        }
+        store_f32(row + v * V, dw[j]);
+        store_f32(row + p.d + v * V, db[j]);
     }
 }
 

@@ -96,10 +96,11 @@ cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
 
 // Sums of the rows of part [rows][n1 + n2] in a fixed order: the first n1 columns to out1, the
 // others to out2, either of which may be null.  Nothing is written when *status (may be
-// null) says that the offsets are malformed.  (causalconv.cu)
+// null) says that the offsets are malformed.  The first n1 columns are a [turned][n1 / turned]
+// matrix that goes to out1 transposed.  (causalconv.cu)
 cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t n1, int64_t n2,
                                float* out1, float* out2, const int32_t* status,
-                               cudaStream_t stream);
+                               cudaStream_t stream, int32_t turned = 1);
 // status = whether the offsets are well formed; nothing for up to kSelfCheck sequences, unless
 // `always`.
 cudaError_t launch_offsets_check(const int32_t* cu, int32_t N, int64_t T, int32_t* status,
@@ -187,15 +188,117 @@ struct Pack {
     }
 };
 
-// 1 / (1 + e^-v).  e^-v overflows to inf below -88, where the quotient is 0.
-__device__ __forceinline__ float sigmoid(float v) {
-    return __fdividef(1.f, 1.f + __expf(-v));
+// Two floats for the packed instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pack2(float a, float b) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
 }
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+__device__ __forceinline__ float2 unpack2(F2 r) {
+    float2 a;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+    return a;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+    const float2 v = unpack2(a);
+    return v.x + v.y;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ F2 both(float a) { return pack2(a, a); }
+constexpr float kLog2e = 1.4426950408889634f;
+
+// V channels in fp32, in pairs for the packed instructions (a single one in the low half).
+template <int V>
+struct Lane {
+    static constexpr int kPairs = (V + 1) / 2;
+    F2 v[kPairs];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) v[i] = 0;
+    }
+    template <typename T>
+    __device__ __forceinline__ void from(const Pack<T, V>& k) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i)
+            v[i] = pack2(k.get(2 * i), V > 1 ? k.get(2 * i + (V > 1 ? 1 : 0)) : 0.f);
+    }
+    template <typename T>
+    __device__ __forceinline__ Pack<T, V> to() const {
+        float f[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = i % 2 ? unpack2(v[i / 2]).y : unpack2(v[i / 2]).x;
+        Pack<T, V> k;
+        k.set(f);
+        return k;
+    }
+    __device__ __forceinline__ void fma(const Lane& a, const Lane& b) {   // this += a b
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) v[i] = fma2(a.v[i], b.v[i], v[i]);
+    }
+    __device__ __forceinline__ float sum() const {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) {
+            const float2 u = unpack2(v[i]);
+            t += V > 1 ? u.x + u.y : u.x;
+        }
+        return t;
+    }
+    __device__ __forceinline__ void add(const Lane& a) {
+#pragma unroll
+        for (int i = 0; i < kPairs; ++i) v[i] = add2(v[i], a.v[i]);
+    }
+};
+template <typename T, int V>
+__device__ __forceinline__ Lane<V> load_lane(const void* p, int64_t at) {
+    Pack<T, V> k;
+    k.load(static_cast<const T*>(p) + at);
+    Lane<V> l;
+    l.from(k);
+    return l;
+}
+
+// 1 / (1 + e^-v): the exponential as 2^(-v log2 e), off by the rounding of its argument (2^-24
+// of |v| log2 e), which counts where the exponential is not small against 1.  It overflows to inf
+// below -88, where the quotient is 0.
+__device__ __forceinline__ float sigmoid(float v) {
+    return __fdividef(1.f, 1.f + ex2(-kLog2e * v));
+}
+__device__ __forceinline__ F2 sigmoid2(F2 v) {
+    const float2 t = unpack2(mul2(v, both(-kLog2e)));
+    const float2 u = unpack2(add2(pack2(ex2(t.x), ex2(t.y)), both(1.f)));
+    return pack2(__fdividef(1.f, u.x), __fdividef(1.f, u.y));
+}
+__device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
+__device__ __forceinline__ F2 silu2(F2 v) { return mul2(v, sigmoid2(v)); }
 // silu and its slope s (1 + v (1 - s)).
 __device__ __forceinline__ float silu_grad(float v) {
     const float s = sigmoid(v);
     return s * fmaf(v, 1.f - s, 1.f);
+}
+__device__ __forceinline__ F2 silu_grad2(F2 v) {
+    const F2 s = sigmoid2(v), vs = mul2(v, s);           // s + v s - v s s
+    return fma2(vs, fma2(s, both(-1.f), both(1.f)), s);
 }
 
 #endif  // __CUDACC__

@@ -36,39 +36,7 @@ constexpr int kSub = 4;         // tokens whose states lie in registers, backwar
 constexpr int kParts = kBack / kSub;
 static_assert(kTile == SELSCAN_CHUNK, "tiles hold whole chunks");
 
-// Two floats for the packed instructions.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pack2(float a, float b) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(F2 r) {
-    float2 a;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
-    return a;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float sum2(F2 a) {
-    const float2 v = unpack2(a);
-    return v.x + v.y;
-}
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 // Decays 2^(D A log2 e).  The special-function unit cuts its argument off after 24 fractional
 // bits, which by itself leaves decays near 1, of which a state multiplies hundreds, 1e-8 to
 // 2.5e-8 too small on average; three quarters of half its last bit, added in the multiply-add
@@ -625,11 +593,12 @@ struct Back {
     static constexpr int kCh = kThreads / NL * 2;
     static constexpr int kNp = 4 * NL;
     static constexpr int kPart = 2 * kNp * kSub > 256 ? 2 * kNp * kSub : 256;
-    // Channels lie in the order of the threads that write them, V at a time (channel_slot); step, u
-    // and dr twice over, as the packed instructions take them.
+    // Channels lie in the order of the threads that write them, V at a time (channel_slot); step and
+    // u twice over, as the packed instructions take them.
     struct Shared {
         float4 du[kBack][kCh];               // D, D, D x, D x
-        float2 dr[kBack][kCh];               // dy silu(z), twice
+        float dr[kBack][kCh];                // dy silu(z)
+        F2 A[4][kThreads];                   // each thread's rates: they would not fit its registers
         float B[kBack][kNp], C[kBack][kNp];
         float y[kBack][kCh];                 // C . h
         float s[2][kBack][kCh];              // B . g and A . (g a h)
@@ -688,7 +657,9 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nl = lane % NL, slot = tid / NL;   // my values; my channels' slots: this and
     constexpr int kOther = CH / 2;               // that one behind it
-    const int64_t D = (int64_t)p.H * p.d, last = cu[p.num_seqs];
+    // (tokens and channels are counted in 32 bits, places in memory in 64)
+    const int32_t D = p.H * p.d;
+    const int64_t Dn = (int64_t)D * p.n;
     const T* const X = static_cast<const T*>(p.in.x);
     const T* const DT = static_cast<const T*>(p.in.dt);
     const T* const Z = static_cast<const T*>(p.in.z);
@@ -698,22 +669,24 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
     const int my[2] = {slot % VR * V + slot / VR, (slot + kOther) % VR * V + (slot + kOther) / VR};
 
     for (int64_t item = blockIdx.x; item < cut.items; item += gridDim.x) {
-        const int64_t blocks = (int64_t)cut.per_group * p.H;
-        const int64_t sg = item / blocks;
-        const int32_t cb = (int32_t)(item - sg * blocks);
+        const int32_t blocks = cut.per_group * p.H;
+        const int32_t sg = (int32_t)(item / blocks);
+        const int32_t cb = (int32_t)(item - (int64_t)sg * blocks);
         const int32_t g = cb / cut.per_group, cg = cb - g * cut.per_group;
         const int32_t c0 = cg * CH;
         const int32_t width = p.d - c0 < CH ? p.d - c0 : CH;
-        const int64_t base = (int64_t)g * p.d + c0;
-        int64_t t0, t1;
+        const int32_t base = g * p.d + c0;
+        int32_t t0, t1;
         int32_t n;
         if (cut.seg == 0) {
             n = (int32_t)sg;
             t0 = cu[n];
             t1 = cu[n + 1];
         } else {
-            t0 = sg * cut.seg;
-            t1 = t0 + cut.seg < last ? t0 + cut.seg : last;
+            const int32_t last = cu[p.num_seqs];
+            const int64_t from = sg * cut.seg, to = from + cut.seg;
+            t0 = (int32_t)(from < last ? from : last);
+            t1 = (int32_t)(to < last ? to : last);
             n = t0 < t1 ? sequence_of(cu, p.num_seqs, t1 - 1) : 0;
         }
         // four values of my two channels in a [..][D][n] tensor
@@ -722,7 +695,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             for (int q = 0; q < 2; ++q) {
                 float u[4] = {0.f, 0.f, 0.f, 0.f};
                 if (from && my[q] < width) {
-                    const float* r = from + (base + my[q]) * p.n + nl * 4;
+                    const float* r = from + ((base + my[q]) * p.n + nl * 4);
                     if (p.n % 4 == 0) {
                         if (nl * 4 < p.n) {
                             const float4 w = *reinterpret_cast<const float4*>(r);
@@ -742,7 +715,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 if (my[q] >= width) continue;
-                float* r = to + (base + my[q]) * p.n + nl * 4;
+                float* r = to + ((base + my[q]) * p.n + nl * 4);
                 const float2 lo = unpack2(v[q][0]), hi = unpack2(v[q][1]);
                 const float u[4] = {lo.x, lo.y, hi.x, hi.y};
                 if (p.n % 4 == 0) {
@@ -755,27 +728,27 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 }
             }
         };
-        F2 A[2][2], dA[2][2], r[2][2];   // rates, their gradients, the gradient from behind
-        load4(p.A, A);
+        F2 dA[2][2], r[2][2];   // gradients of the rates, the gradient from behind
+        load4(p.A, dA);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                A[q][i] = mul2(A[q][i], pack2(kLog2e, kLog2e));
+                s.A[q * 2 + i][tid] = mul2(dA[q][i], pack2(kLog2e, kLog2e));
                 dA[q][i] = 0;
             }
         const float* behind = nullptr;
-        if (t0 < t1 && t1 != cu[n + 1]) behind = maps.state + sg * D * p.n;
-        else if (p.dS_T && (t0 < t1 || cut.seg == 0)) behind = p.dS_T + n * D * p.n;
+        if (t0 < t1 && t1 != cu[n + 1]) behind = maps.state + sg * Dn;
+        else if (p.dS_T && (t0 < t1 || cut.seg == 0)) behind = p.dS_T + n * Dn;
         load4(behind, r);
         for (int i = tid; i < 2 * G::kWarps * CH; i += TH) (&s.acc[0][0][0])[i] = 0.f;
-        if (cut.seg == 0 && t0 >= t1 && p.g.dS0) store4(p.g.dS0 + n * D * p.n, r);
+        if (cut.seg == 0 && t0 >= t1 && p.g.dS0) store4(p.g.dS0 + n * Dn, r);
 
         // my vectors of a tile: V channels of a row
         auto row_of = [&](int i) { return (tid + i * TH) / VR; };
         auto col_of = [&](int i) { return (tid + i * TH) % VR * V; };
         // inputs of tokens [a, a + cnt), to shared memory
-        auto convert = [&](int64_t a, int cnt) {
+        auto convert = [&](int32_t a, int cnt) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int k = row_of(i), c = col_of(i);
@@ -785,7 +758,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
 #pragma unroll
                     for (int q = 0; q < V; ++q) {
                         s.du[k][q * VR + c / V] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        s.dr[k][q * VR + c / V] = make_float2(0.f, 0.f);
+                        s.dr[k][q * VR + c / V] = 0.f;
                     }
                     continue;
                 }
@@ -800,7 +773,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     if (p.softplus) v = softplus(v);
                     const float u = v * kx.get(q), dr = Z ? kg.get(q) * silu(kz.get(q)) : kg.get(q);
                     s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
-                    s.dr[k][q * VR + c / V] = make_float2(dr, dr);
+                    s.dr[k][q * VR + c / V] = dr;
                 }
             }
             if (packed) {
@@ -830,7 +803,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             }
         };
         // the gradients of tokens [a, a + cnt), whose sums are in shared memory
-        auto finish = [&](int64_t a, int cnt) {
+        auto finish = [&](int32_t a, int cnt) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int k = row_of(i), c = col_of(i);
@@ -845,46 +818,49 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                         kg.load(DY + at);
                     }
                 }
-                float acc[2 * V];   // for dskip, for ddt_bias
-#pragma unroll
-                for (int q = 0; q < 2 * V; ++q) acc[q] = 0.f;
-                constexpr int U = V < 4 ? V : 4;
+                constexpr int U = V < 4 ? V : 4, R = VR < 32 ? VR : 32;   // lanes of a row
 #pragma unroll
                 for (int q0 = 0; q0 < V; q0 += U) {
-                    if (!in) continue;
-                    float dx[U], ddt[U], dz[U];
+                    float acc[2 * U] = {};   // for dskip, for ddt_bias
+                    if (in) {
+                        float dx[U], dz[U];
 #pragma unroll
-                    for (int j = 0; j < U; ++j) {
-                        const int q = q0 + j, sl = q * VR + c / V;
-                        const float skip = p.skip ? p.skip[base + c + q] : 0.f;
-                        const float x = kx.get(q), s1 = s.s[0][k][sl], dr = s.dr[k][sl].x;
-                        ddt[j] = fmaf(x, s1, s.s[1][k][sl] * kLn2);
-                        if (p.softplus)
-                            ddt[j] *= sigmoid(kd.get(q) + (p.dt_bias ? p.dt_bias[base + c + q] : 0.f));
-                        dx[j] = fmaf(s.du[k][sl].x, s1, skip * dr);
-                        if (Z) dz[j] = kg.get(q) * fmaf(skip, x, s.y[k][sl]) * silu_grad(kz.get(q));
-                        acc[q] = dr * x;
-                        acc[V + q] = ddt[j];
-                    }
-                    Pack<float, U> o;
-                    o.set(dx);
-                    o.store(p.g.dx + at + q0);
-                    o.set(ddt);
-                    o.store(p.g.ddt + at + q0);
-                    if (Z) {
-                        o.set(dz);
-                        o.store(p.g.dz + at + q0);
-                    }
-                }
-                // the rows of my warp, then the tiles before
-                const int first = spread_sum<2 * V, 16, VR < 32 ? VR : 32>(acc, lane);
-                constexpr int kLeftV = spread_left(2 * V, 16, VR < 32 ? VR : 32);
-                constexpr int kSame = 32 / (VR < 32 ? VR : 32) / (2 * V / kLeftV);   // lanes with one sum
-                if (kSame <= 1 || lane / VR % kSame == 0) {
+                        for (int j = 0; j < U; ++j) {
+                            const int q = q0 + j, sl = q * VR + c / V;
+                            const float skip = p.skip ? p.skip[base + c + q] : 0.f;
+                            const float x = kx.get(q), s1 = s.s[0][k][sl], dr = s.dr[k][sl];
+                            acc[j] = dr * x;
+                            float ddt = fmaf(x, s1, s.s[1][k][sl] * kLn2);
+                            if (p.softplus)
+                                ddt *= sigmoid(kd.get(q) +
+                                               (p.dt_bias ? p.dt_bias[base + c + q] : 0.f));
+                            acc[U + j] = ddt;
+                            dx[j] = fmaf(s.du[k][sl].x, s1, skip * dr);
+                            if (Z)
+                                dz[j] = kg.get(q) * fmaf(skip, x, s.y[k][sl]) * silu_grad(kz.get(q));
+                        }
+                        Pack<float, U> o;
+                        o.set(dx);
+                        o.store(p.g.dx + at + q0);
 #pragma unroll
-                    for (int q = 0; q < kLeftV; ++q) {
-                        const int j = first + q;
-                        s.acc[j / V][warp][j % V * VR + c / V] += acc[q];
+                        for (int j = 0; j < U; ++j) dx[j] = acc[U + j];
+                        o.set(dx);
+                        o.store(p.g.ddt + at + q0);
+                        if (Z) {
+                            o.set(dz);
+                            o.store(p.g.dz + at + q0);
+                        }
+                    }
+                    // the rows of my warp, then the tiles before
+                    const int first = spread_sum<2 * U, 16, R>(acc, lane);
+                    constexpr int kLeftU = spread_left(2 * U, 16, R);
+                    constexpr int kSame = 32 / R / (2 * U / kLeftU);   // lanes with the same sum
+                    if (kSame <= 1 || lane / R % (kSame > 0 ? kSame : 1) == 0) {
+#pragma unroll
+                        for (int q = 0; q < kLeftU; ++q) {
+                            const int j = first + q;
+                            s.acc[j / U][warp][(q0 + j % U) * VR + c / V] += acc[q];
+                        }
                     }
                 }
             }
@@ -892,7 +868,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             for (int i = tid; i < cnt * NP / 2; i += TH) {
                 const int k = i / (NP / 2), j = i % (NP / 2) * 4, st = j % NP;
                 if (st >= p.n) continue;
-                const int row_at = (int)(a % kBack) + k;   // in the grid of parts
+                const int row_at = a % kBack + k;   // in the grid of parts
                 const int at = row_at % kSub * 2 * NP + j;
                 float4 v = *reinterpret_cast<const float4*>(&s.part[0][row_at / kSub][at]);
 #pragma unroll
@@ -900,7 +876,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     const float4 u = *reinterpret_cast<const float4*>(&s.part[w][row_at / kSub][at]);
                     v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
                 }
-                const int64_t row = (a + k) * p.H + g;
+                const int64_t row = (int64_t)(a + k) * p.H + g;
                 float* to = cut.per_group == 1
                                 ? (j < NP ? p.g.dB : p.g.dC) + row * p.n + st
                                 : part_BC + ((int64_t)cg * p.total_tokens * p.H + row) * 2 * p.n +
@@ -933,17 +909,28 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         auto row4 = [&](const float (&m)[kBack][NP], int k) {
             return *reinterpret_cast<const ulonglong2*>(&m[k][nl * 4]);
         };
-        auto advance = [&](int k, F2 (&h)[2][2]) {
+        struct Rates {
+            F2 v[2][2];
+        };
+        auto rates = [&]() {
+            Rates A;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) A.v[i / 2][i % 2] = s.A[i][tid];
+            return A;
+        };
+        auto advance = [&](const Rates& A, int k, F2 (&h)[2][2]) {
             const Inputs v = inputs(k);
             const ulonglong2 b = row4(s.B, k);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                h[q][0] = fma2(decay2(v.dd[q], A[q][0]), h[q][0], mul2(v.uu[q], b.x));
-                h[q][1] = fma2(decay2(v.dd[q], A[q][1]), h[q][1], mul2(v.uu[q], b.y));
+                h[q][0] = fma2(decay2(v.dd[q], A.v[q][0]), h[q][0], mul2(v.uu[q], b.x));
+                h[q][1] = fma2(decay2(v.dd[q], A.v[q][1]), h[q][1], mul2(v.uu[q], b.y));
             }
         };
         // Tokens [from, to) of the tile, at most kSub, from state h: rebuilt, then backward.
         auto sub = [&](auto whole, int from, int to, F2 (&h)[2][2], float* sums) {
+            asm volatile("" ::: "memory");
+            const Rates A = rates();
             F2 before[kSub][2][2];
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
@@ -952,7 +939,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) before[j][q][i] = h[q][i];
-                advance(from + j, h);
+                advance(A, from + j, h);
                 if (Z) {
                     const ulonglong2 c = row4(s.C, from + j);
                     float y[2];
@@ -966,22 +953,24 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             for (int j = kSub - 1; j >= 0; --j) {
                 if (!whole.value && from + j >= to) continue;
                 const int k = from + j;
+                asm volatile("" ::: "memory");   // (tokens further ahead would not fit the registers)
                 const Inputs v = inputs(k);
                 const ulonglong2 b = row4(s.B, k), c = row4(s.C, k);
                 F2 vB[2] = {0, 0}, vC[2] = {0, 0}, t1[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const F2 rr = *reinterpret_cast<const F2*>(&s.dr[k][slot + q * kOther]);
+                    const float rv = s.dr[k][slot + q * kOther];
+                    const F2 rr = pack2(rv, rv);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const F2 a = decay2(v.dd[q], A[q][i]);
+                        const F2 a = decay2(v.dd[q], A.v[q][i]);
                         const F2 gr = fma2(i ? c.y : c.x, rr, r[q][i]);   // gradient of h
                         vC[i] = fma2(h[q][i], rr, vC[i]);
                         vB[i] = fma2(gr, v.uu[q], vB[i]);
                         t1[q] = fma2(gr, i ? b.y : b.x, t1[q]);
                         const F2 ag = mul2(a, gr), w = mul2(ag, before[j][q][i]);
                         dA[q][i] = fma2(w, v.dd[q], dA[q][i]);
-                        t2[q] = fma2(w, A[q][i], t2[q]);
+                        t2[q] = fma2(w, A.v[q][i], t2[q]);
                         r[q][i] = ag;
                         h[q][i] = before[j][q][i];
                     }
@@ -1005,24 +994,24 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         };
 
         // the tile that ends before token e of a sequence that starts at `start`
-        auto tile_start = [&](int64_t e, int64_t start) {
-            int64_t a = (e - 1) / kBack * kBack;
+        auto tile_start = [&](int32_t e, int32_t start) {
+            int32_t a = (e - 1) / kBack * kBack;
             if (a < start) a = start;
             return a < t0 ? t0 : a;
         };
-        int64_t te = t1, ta = t0 < t1 ? tile_start(t1, cu[n]) : t0;
+        int32_t te = t1, ta = t0 < t1 ? tile_start(t1, cu[n]) : t0;
         __syncthreads();
-        if (te > t0) convert(ta, (int)(te - ta));
+        if (te > t0) convert(ta, te - ta);
         while (te > t0) {
             __syncthreads();
-            const int64_t start = cu[n];
-            const int cnt = (int)(te - ta);
+            const int32_t start = cu[n];
+            const int cnt = te - ta;
             // The tile in parts on the grid of kSub tokens: the states before all but the first are
             // formed on one walk, then the parts are taken from the last one on.
-            const int off = (int)(ta % kBack);             // the tile's rows of the grid: from
+            const int off = ta % kBack;             // the tile's rows of the grid: from
             const int p0 = off / kSub, p1 = (off + cnt - 1) / kSub;   // off on; its parts
-            const float* enters = ta == start ? (p.S0 ? p.S0 + n * D * p.n : nullptr)
-                                              : p.states + ta / kBack * D * p.n;
+            const float* enters = ta == start ? (p.S0 ? p.S0 + n * Dn : nullptr)
+                                              : p.states + ta / kBack * Dn;
             F2 h[2][2];
             load4(enters, h);
             auto place = [&](int part) { return reinterpret_cast<F2*>(s.part[warp][part]) + lane; };
@@ -1040,10 +1029,11 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 __syncwarp();   // the place takes the part's sums from here on
             };
             if (cnt == kBack) {
+                const Rates A = rates();
 #pragma unroll 1
                 for (int part = 1; part < kParts; ++part) {
 #pragma unroll
-                    for (int k = 0; k < kSub; ++k) advance((part - 1) * kSub + k, h);
+                    for (int k = 0; k < kSub; ++k) advance(A, (part - 1) * kSub + k, h);
                     keep(part);
                 }
 #pragma unroll 1
@@ -1052,10 +1042,11 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     sub(std::true_type(), part * kSub, (part + 1) * kSub, h, s.part[warp][part]);
                 }
             } else {
+                const Rates A = rates();
 #pragma unroll 1
                 for (int k = 0; k < cnt; ++k) {
                     if (k > 0 && (off + k) % kSub == 0) keep((off + k) / kSub);
-                    if (k + 1 < cnt) advance(k, h);
+                    if (k + 1 < cnt) advance(A, k, h);
                 }
 #pragma unroll 1
                 for (int part = p1; part >= p0; --part) {
@@ -1070,20 +1061,20 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             finish(ta, cnt);
             te = ta;
             if (te == start) {
-                if (p.g.dS0) store4(p.g.dS0 + n * D * p.n, r);
+                if (p.g.dS0) store4(p.g.dS0 + n * Dn, r);
                 if (te > t0) {
                     do --n; while (cu[n] == cu[n + 1]);
-                    load4(p.dS_T ? p.dS_T + n * D * p.n : nullptr, r);
+                    load4(p.dS_T ? p.dS_T + n * Dn : nullptr, r);
                 }
             }
             if (te > t0) {
                 ta = tile_start(te, cu[n]);
                 // (what finish reads of the inputs' places, the same threads write now; the
                 // sums' places are written behind the barrier)
-                convert(ta, (int)(te - ta));
+                convert(ta, te - ta);
             }
         }
-        store4(part_A + sg * D * p.n, dA);
+        store4(part_A + sg * Dn, dA);
         __syncthreads();
         // the warps, in order
         for (int i = tid; i < 2 * CH; i += TH) {
@@ -1091,7 +1082,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < G::kWarps; ++w) sum += s.acc[which][w][sl];
-            if (c < width) part_c[sg * 2 * D + which * D + base + c] = sum;
+            if (c < width) part_c[((int64_t)sg * 2 + which) * D + base + c] = sum;
         }
         __syncthreads();
     }
@@ -1123,47 +1114,122 @@ sum_blocks_kernel(const ScanArgs p, int32_t blocks, const float* __restrict__ pa
 
 // ---------------------------------------------------------------- decode step
 
-// One token a row: L lanes a channel, 8 values each.
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) scan_step_kernel(const ScanStepArgs p, int64_t blocks) {
-    const int64_t D = (int64_t)p.H * p.d;
-    const int64_t b = blockIdx.x / blocks;
-    const int64_t ch = (blockIdx.x - b * blocks) * (kThreads / L) + threadIdx.x / L;
-    const int li = threadIdx.x % L;
-    const bool on = ch < D;   // (all lanes of a warp take part in its sums)
-    const int64_t c = on ? ch : 0;
-    const int32_t row = p.parents ? p.parents[b] : (int32_t)b;
-    const bool live = row >= 0 && row < p.num_rows;
-    float A[kNs], h[kNs];
-    load8(p.A + c * p.n, li * kNs, p.n, A);
-    load8(live ? p.S + ((int64_t)row * D + c) * p.n : nullptr, li * kNs, p.n, h);
-    const float x = Elem<T>::load(static_cast<const T*>(p.in.x) + b * p.in.ldx + c);
-    float step = Elem<T>::load(static_cast<const T*>(p.in.dt) + b * p.in.lddt + c) +
-                 (p.dt_bias ? p.dt_bias[c] : 0.f);
-    if (p.softplus) step = softplus(step);
-    const int64_t g = c / p.d;
-    const T* B = static_cast<const T*>(p.in.B) + b * p.in.ldB + g * p.n;
-    const T* C = static_cast<const T*>(p.in.C) + b * p.in.ldC + g * p.n;
-    F2 hv[kNs / 2];
-    float y = 0.f;
+// One token for each of `rows` sequences a warp, 32 channels of a group.  A lane forms one
+// channel's step, skip and gate; the states go by NL lanes a channel, four values each, so that the
+// warp reads and writes whole lines of them, 32 / NL channels at a time, with the steps passed on
+// by exchanges.  The rates are read once for all the rows.
+constexpr int kStepThreads = 128;
+template <typename T, int NL>
+__global__ void __launch_bounds__(kStepThreads)
+scan_step_kernel(const ScanStepArgs p, int32_t per_group, int32_t rows) {
+    constexpr int kAt = 32 / NL;                // channels at a time
+    constexpr int kHold = NL <= 4 ? NL : 4;     // times whose states are loaded at once
+    const int32_t warps = per_group * p.H;
+    const int64_t item = (int64_t)blockIdx.x * (kStepThreads / 32) + threadIdx.x / 32;
+    const int32_t rb = (int32_t)(item / warps), wb = (int32_t)(item - (int64_t)rb * warps);
+    const int32_t g = wb / per_group, c0 = (wb - g * per_group) * 32;
+    if ((int64_t)rb * rows >= p.B) return;
+    const int lane = threadIdx.x & 31, k = lane % NL * 4, mine = lane / NL;
+    const int32_t width = p.d - c0 < 32 ? p.d - c0 : 32, base = g * p.d + c0;
+    const int32_t D = p.H * p.d;
+    const bool on = lane < width, whole = p.n % 4 == 0;
+    const float bias = on && p.dt_bias ? p.dt_bias[base + lane] : 0.f;
+    const float skip = on && p.skip ? p.skip[base + lane] : 0.f;
+    // four values from k on of a channel's row
+    auto load = [&](const float* at, bool live, float (&v)[4]) {
 #pragma unroll
-    for (int i = 0; i < kNs; ++i) {
-        const int k = li * kNs + i;
-        const float bv = k < p.n ? Elem<T>::load(B + k) : 0.f, cv = k < p.n ? Elem<T>::load(C + k) : 0.f;
-        const float a = decay(step, A[i] * kLog2e);
-        h[i] = fmaf(a, h[i], step * x * bv);
-        y = fmaf(h[i], cv, y);
+        for (int i = 0; i < 4; ++i) v[i] = 0.f;
+        if (!live) return;
+        if (whole) {
+            if (k < p.n) {
+                const float4 u = __ldcs(reinterpret_cast<const float4*>(at));
+                v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (k + i < p.n) v[i] = at[i];
+        }
+    };
+    float A[kHold][4];
+    auto rates = [&](int from) {
+#pragma unroll
+        for (int j = 0; j < kHold; ++j) {
+            const int ch = (from + j) * kAt + mine;
+            load(p.A + (int64_t)(base + ch) * p.n + k, ch < width, A[j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) A[j][i] *= kLog2e;
+        }
+    };
+    if (NL <= 4) rates(0);
+    const int32_t stop = (rb + 1) * (int64_t)rows < p.B ? (rb + 1) * rows : p.B;
+    for (int64_t b = (int64_t)rb * rows; b < stop; ++b) {
+        const int32_t row = p.parents ? p.parents[b] : (int32_t)b;
+        const bool live = row >= 0 && row < p.num_rows;
+        float x = 0.f, step = 0.f, gate = 1.f;
+        if (on) {
+            x = Elem<T>::load(static_cast<const T*>(p.in.x) + b * p.in.ldx + base + lane);
+            step = Elem<T>::load(static_cast<const T*>(p.in.dt) + b * p.in.lddt + base + lane) + bias;
+            if (p.in.z)
+                gate = Elem<T>::load(static_cast<const T*>(p.in.z) + b * p.in.ldz + base + lane);
+        }
+        float bv[4], cv[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool in = k + i < p.n;
+            bv[i] = in ? Elem<T>::load(static_cast<const T*>(p.in.B) + b * p.in.ldB +
+                                       (int64_t)g * p.n + k + i) : 0.f;
+            cv[i] = in ? Elem<T>::load(static_cast<const T*>(p.in.C) + b * p.in.ldC +
+                                       (int64_t)g * p.n + k + i) : 0.f;
+        }
+        if (p.softplus) step = softplus(step);
+        const float u = step * x;
+        float y = 0.f;
+#pragma unroll 1
+        for (int from = 0; from < NL; from += kHold) {
+            float h[kHold][4];
+#pragma unroll
+            for (int j = 0; j < kHold; ++j) {
+                const int ch = (from + j) * kAt + mine;
+                load(p.S + ((int64_t)row * D + base + ch) * p.n + k, live && ch < width, h[j]);
+            }
+            if (NL > 4) rates(from);
+#pragma unroll
+            for (int j = 0; j < kHold; ++j) {
+                const int ch = (from + j) * kAt + mine;
+                const float st = __shfl_sync(0xffffffffu, step, ch);
+                const float uc = __shfl_sync(0xffffffffu, u, ch);
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[j][i] = fmaf(decay(st, A[j][i]), h[j][i], uc * bv[i]);
+                    sum = fmaf(h[j][i], cv[i], sum);
+                }
+                if (ch < width) {
+                    float* out = p.S_out + ((int64_t)b * D + base + ch) * p.n + k;
+                    if (whole) {
+                        if (k < p.n)
+                            *reinterpret_cast<float4*>(out) =
+                                make_float4(h[j][0], h[j][1], h[j][2], h[j][3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (k + i < p.n) out[i] = h[j][i];
+                    }
+                }
+#pragma unroll
+                for (int o = 1; o < NL; o *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                // to the lane whose channel it is
+                const float there = __shfl_sync(0xffffffffu, sum, lane % kAt * NL);
+                if (lane / kAt == from + j) y = there;
+            }
+        }
+        if (on) {
+            y = fmaf(skip, x, y);
+            if (p.in.z) y *= silu(gate);
+            Elem<T>::store(static_cast<T*>(p.y) + b * D + base + lane, y);
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kNs / 2; ++i) hv[i] = pack2(h[2 * i], h[2 * i + 1]);
-#pragma unroll
-    for (int o = 1; o < L; o *= 2) y += __shfl_xor_sync(0xffffffffu, y, o);
-    if (!on) return;
-    store8(p.S_out + (b * D + c) * p.n, li * kNs, p.n, hv);
-    if (li != 0) return;
-    if (p.skip) y = fmaf(p.skip[c], x, y);
-    if (p.in.z) y *= silu(Elem<T>::load(static_cast<const T*>(p.in.z) + b * p.in.ldz + c));
-    Elem<T>::store(static_cast<T*>(p.y) + b * D + c, y);
 }
 
 // ---------------------------------------------------------------- host
@@ -1436,15 +1502,19 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
 }
 
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream) {
-    const int64_t D = (int64_t)a.H * a.d;
-    const int ch = kThreads / lanes_of(a.n);
-    const int64_t blocks = (D + ch - 1) / ch;
-    if (a.B * blocks > INT32_MAX) return cudaErrorInvalidValue;
+    const int32_t per_group = (a.d + 31) / 32;
+    const int64_t warps = (int64_t)per_group * a.H;
+    // as many rows a warp, up to four, as leave each SM 16 warps
+    int32_t rows = 4;
+    while (rows > 1 && (a.B + rows - 1) / rows * warps < 16 * sms()) rows /= 2;
+    const int64_t blocks = ((a.B + rows - 1) / rows * warps + 3) / 4;
+    static_assert(kStepThreads == 128, "four warps a CTA");
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
     return by_type(a.dtype, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
-        return by_lanes(a.n, [&](auto l) {
+        return by_back_lanes(a.n, [&](auto l) {   // (four values a lane, as in the backward pass)
             scan_step_kernel<T, decltype(l)::value>
-                <<<(unsigned)(a.B * blocks), kThreads, 0, stream>>>(a, blocks);
+                <<<(unsigned)blocks, kStepThreads, 0, stream>>>(a, per_group, rows);
             return cudaGetLastError();
         });
     });
