@@ -166,7 +166,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
     constexpr int NI = (kTile * VR + TH - 1) / TH;      // of a tile, a thread
     constexpr int VB = 16 / sizeof(T);                  // values of B and C at once
     constexpr int NB = (2 * kTile * NP / VB + TH - 1) / TH;
-    static_assert(V == 1 || TH % VR == 0, "a thread keeps its channels");
+    static_assert(TH % VR == 0, "a thread keeps its channels");
     // (objects of their own: a store to one does not hold up the loads from another)
     __shared__ __align__(16) typename G::Steps s_du[2];
     __shared__ __align__(16) typename G::Rows s_B[2], s_C[2];
@@ -282,19 +282,17 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         const int my_c = tid % VR * V;
         const bool in_row = my_c < width;
         auto row_of = [&](int i) { return (tid + i * TH) / VR; };
-        auto col_of = [&](int i) { return V == 1 ? (tid + i * TH) % VR : my_c; };
         float bias[V], skip[V];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            bias[k] = V > 1 && in_row && p.dt_bias ? p.dt_bias[base + my_c + k] : 0.f;
-            skip[k] = V > 1 && in_row && p.skip && PASS == kOutputs ? p.skip[base + my_c + k] : 0.f;
+            bias[k] = in_row && p.dt_bias ? p.dt_bias[base + my_c + k] : 0.f;
+            skip[k] = in_row && p.skip && PASS == kOutputs ? p.skip[base + my_c + k] : 0.f;
         }
         Pack<T, V> rx[NI], rd[NI], rz[NI], kx[NI], kz[NI];
         Pack<T, VB> rb[NB];
         auto fetch = [&](const Tile& k) {
-            // (odd rows are read where they are used)
 #pragma unroll
-            for (int i = 0; i < (V > 1 ? NI : 0); ++i) {
+            for (int i = 0; i < NI; ++i) {
                 const int r = row_of(i);
                 if (r < k.cnt && in_row) {
                     rx[i].load(X + (k.a + r) * ldx + base + my_c);
@@ -327,23 +325,15 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         auto convert = [&](const Tile& k, int side) {
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int r = row_of(i), c = col_of(i);
-                if (r >= k.cnt || c >= width) continue;
+                const int r = row_of(i);
+                if (r >= k.cnt || !in_row) continue;
                 if constexpr (V == 1) {
-                    rx[0].load(X + (k.a + r) * ldx + base + c);
-                    rd[0].load(DT + (k.a + r) * p.in.lddt + base + c);
-                    float v = rd[0].get(0) + (p.dt_bias ? p.dt_bias[base + c] : 0.f);
+                    float v = rd[i].get(0) + bias[0];
                     if (p.softplus) v = softplus(v);
-                    float u = rx[0].get(0);
-                    if (PASS == kGradMaps) {
-                        if (Z) {
-                            rz[0].load(Z + (k.a + r) * p.in.ldz + base + c);
-                            u *= silu(rz[0].get(0));
-                        }
-                    } else {
-                        u *= v;
-                    }
-                    reinterpret_cast<float2*>(s_du[side][r])[c] = make_float2(v, u);
+                    float u = rx[i].get(0);
+                    if (PASS == kGradMaps) u = Z ? u * silu(rz[i].get(0)) : u;
+                    else u *= v;
+                    reinterpret_cast<float2*>(s_du[side][r])[my_c] = make_float2(v, u);
                 } else {
 #pragma unroll
                     for (int q = 0; q < V; q += 2) {
@@ -441,17 +431,12 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             if (!p.y) return;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int r = row_of(i), c = col_of(i);
-                if (r >= k.cnt || c >= width) continue;
+                const int r = row_of(i);
+                if (r >= k.cnt || !in_row) continue;
                 float o[V];
                 if constexpr (V == 1) {
-                    o[0] = reinterpret_cast<const float*>(s_y[side][r])[c];
-                    kx[0].load(X + (k.a + r) * ldx + base + c);
-                    if (p.skip) o[0] = fmaf(p.skip[base + c], kx[0].get(0), o[0]);
-                    if (Z) {
-                        kz[0].load(Z + (k.a + r) * p.in.ldz + base + c);
-                        o[0] *= silu(kz[0].get(0));
-                    }
+                    o[0] = fmaf(skip[0], kx[i].get(0), reinterpret_cast<const float*>(s_y[side][r])[my_c]);
+                    if (Z) o[0] *= silu(kz[i].get(0));
                 } else {
 #pragma unroll
                     for (int q = 0; q < V; q += 2) {
@@ -466,7 +451,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
                 }
                 Pack<T, V> ky;
                 ky.set(o);
-                ky.store(static_cast<T*>(p.y) + (k.a + r) * D + base + c);
+                ky.store(static_cast<T*>(p.y) + (k.a + r) * D + base + my_c);
             }
         };
 
@@ -483,12 +468,10 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
             if constexpr (PASS == kOutputs)
                 if (!first) finish(before, side ^ 1);
             first = false;
-            if (V > 1) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    kx[i] = rx[i];
-                    kz[i] = rz[i];
-                }
+            for (int i = 0; i < NI; ++i) {
+                kx[i] = rx[i];
+                kz[i] = rz[i];
             }
             const bool more = has_next(now);
             Tile next = now;
@@ -538,12 +521,18 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
 
 // Joins the segments' maps: state[s] becomes the state that enters segment s (reversed: that
 // reaches it from behind).
-constexpr int kJoin = 8;   // segments loaded at once
+constexpr int kJoin = 16;   // segments loaded at once
+constexpr int kJoinEmpty = 64;   // sequences among which the join looks for empty ones
 __global__ void __launch_bounds__(kThreads)
-join_kernel(const ScanArgs p, const Cut cut, const Maps maps, bool reversed, const int32_t* status) {
+join_kernel(const ScanArgs p, const Cut cut, const Maps maps, bool reversed, const float* in,
+            float* out, const int32_t* status) {
     if (*status != KDA_OK) return;
     const int64_t D = (int64_t)p.H * p.d, i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (i >= D * p.n) return;
+    // out[n] = in[n] (or zeros) for the empty sequences, which no segment holds
+    for (int32_t n = 0; out && p.num_seqs <= kJoinEmpty && n < p.num_seqs; ++n)
+        if (p.cu_seqlens[n] == p.cu_seqlens[n + 1])
+            out[n * D * p.n + i] = in ? in[n * D * p.n + i] : 0.f;
     const int64_t last = p.cu_seqlens[p.num_seqs], segs = (last + cut.seg - 1) / cut.seg;
     const int64_t c = i / p.n;
     const float A = p.A[i] * kLog2e;
@@ -571,7 +560,7 @@ join_kernel(const ScanArgs p, const Cut cut, const Maps maps, bool reversed, con
     }
 }
 
-// out[n] = in[n] (or zeros) for the empty sequences, which no segment holds.
+// The same for more sequences than that.
 __global__ void __launch_bounds__(kThreads)
 empty_kernel(const int32_t* cu, int32_t N, int64_t row, const float* in, float* out,
              const int32_t* status) {
@@ -747,14 +736,34 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         // my vectors of a tile: V channels of a row
         auto row_of = [&](int i) { return (tid + i * TH) / VR; };
         auto col_of = [&](int i) { return (tid + i * TH) % VR * V; };
-        // inputs of tokens [a, a + cnt), to shared memory
-        auto convert = [&](int32_t a, int cnt) {
+        // Inputs of tokens [a, a + cnt), to shared memory, each to its row of the grid of tiles.  The
+        // rows around them get steps and inputs of zero, which leave the state, the gradient from
+        // behind and the rates' sums as they are.
+        auto convert = [&](int32_t a0, int cnt0) {
+            const int32_t a = a0 / kBack * kBack;
+            const int first = a0 - a, cnt = first + cnt0;   // rows [first, cnt)
+            // (single values all at once, vectors one after the other: more do not fit)
+            constexpr int kOnce = V == 1 ? NI : 1;
+            Pack<T, V> kx[kOnce], kd[kOnce], kg[kOnce], kz[kOnce];
+            auto load = [&](int i, int j) {
+                const int k = row_of(i), c = col_of(i);
+                const int64_t t = a + k;
+                if (k < first || k >= cnt || c >= width) return;
+                kx[j].load(X + t * p.in.ldx + base + c);
+                kd[j].load(DT + t * p.in.lddt + base + c);
+                kg[j].load(DY + t * D + base + c);
+                if (Z) kz[j].load(Z + t * p.in.ldz + base + c);
+            };
+            if constexpr (V == 1) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) load(i, i);
+            }
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int k = row_of(i), c = col_of(i);
-                if (k >= cnt) continue;
-                const int64_t t = a + k;
-                if (c >= width) {   // channels that are not there
+                constexpr bool kLoaded = V == 1;
+                const int k = row_of(i), c = col_of(i), j = kLoaded ? i : 0;
+                if (k >= kBack) continue;
+                if (k < first || k >= cnt || c >= width) {
 #pragma unroll
                     for (int q = 0; q < V; ++q) {
                         s.du[k][q * VR + c / V] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -762,16 +771,13 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     }
                     continue;
                 }
-                Pack<T, V> kx, kd, kg, kz;
-                kx.load(X + t * p.in.ldx + base + c);
-                kd.load(DT + t * p.in.lddt + base + c);
-                kg.load(DY + t * D + base + c);
-                if (Z) kz.load(Z + t * p.in.ldz + base + c);
+                if (!kLoaded) load(i, 0);
 #pragma unroll
                 for (int q = 0; q < V; ++q) {
-                    float v = kd.get(q) + (p.dt_bias ? p.dt_bias[base + c + q] : 0.f);
+                    float v = kd[j].get(q) + (p.dt_bias ? p.dt_bias[base + c + q] : 0.f);
                     if (p.softplus) v = softplus(v);
-                    const float u = v * kx.get(q), dr = Z ? kg.get(q) * silu(kz.get(q)) : kg.get(q);
+                    const float u = v * kx[j].get(q);
+                    const float dr = Z ? kg[j].get(q) * silu(kz[j].get(q)) : kg[j].get(q);
                     s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
                     s.dr[k][q * VR + c / V] = dr;
                 }
@@ -782,7 +788,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     const int k = j / (NP / VB), at = j % (NP / VB) * VB;
                     Pack<T, VB> b;
                     b.zero();
-                    if (k < cnt && at < p.n)
+                    if (k >= first && k < cnt && at < p.n)
                         b.load(static_cast<const T*>(which ? p.in.C : p.in.B) +
                                (a + k) * (which ? p.in.ldC : p.in.ldB) + (int64_t)g * p.n + at);
                     float* to = which ? &s.C[k][at] : &s.B[k][at];
@@ -794,7 +800,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             } else {
                 for (int i = tid; i < kBack * NP; i += TH) {
                     const int k = i / NP, j = i % NP;
-                    const bool in = k < cnt && j < p.n;
+                    const bool in = k >= first && k < cnt && j < p.n;
                     s.B[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.B) +
                                                    (a + k) * p.in.ldB + (int64_t)g * p.n + j) : 0.f;
                     s.C[k][j] = in ? Elem<T>::load(static_cast<const T*>(p.in.C) +
@@ -803,11 +809,13 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             }
         };
         // the gradients of tokens [a, a + cnt), whose sums are in shared memory
-        auto finish = [&](int32_t a, int cnt) {
+        auto finish = [&](int32_t a0, int cnt0) {
+            const int32_t a = a0 / kBack * kBack;
+            const int from = a0 - a, cnt = from + cnt0;   // rows [from, cnt)
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
                 const int k = row_of(i), c = col_of(i);
-                const bool in = k < cnt && c < width;
+                const bool in = k >= from && k < cnt && c < width;
                 const int64_t t = a + k, at = t * D + base + c;
                 Pack<T, V> kx, kd, kg, kz;
                 if (in) {
@@ -865,15 +873,14 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 }
             }
             // sums over the CTA's channels: to the outputs if it has the whole group
-            for (int i = tid; i < cnt * NP / 2; i += TH) {
+            for (int i = from * NP / 2 + tid; i < cnt * NP / 2; i += TH) {
                 const int k = i / (NP / 2), j = i % (NP / 2) * 4, st = j % NP;
                 if (st >= p.n) continue;
-                const int row_at = a % kBack + k;   // in the grid of parts
-                const int at = row_at % kSub * 2 * NP + j;
-                float4 v = *reinterpret_cast<const float4*>(&s.part[0][row_at / kSub][at]);
+                const int at = k % kSub * 2 * NP + j;
+                float4 v = *reinterpret_cast<const float4*>(&s.part[0][k / kSub][at]);
 #pragma unroll
                 for (int w = 1; w < G::kWarps; ++w) {
-                    const float4 u = *reinterpret_cast<const float4*>(&s.part[w][row_at / kSub][at]);
+                    const float4 u = *reinterpret_cast<const float4*>(&s.part[w][k / kSub][at]);
                     v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
                 }
                 const int64_t row = (int64_t)(a + k) * p.H + g;
@@ -927,14 +934,13 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 h[q][1] = fma2(decay2(v.dd[q], A.v[q][1]), h[q][1], mul2(v.uu[q], b.y));
             }
         };
-        // Tokens [from, to) of the tile, at most kSub, from state h: rebuilt, then backward.
-        auto sub = [&](auto whole, int from, int to, F2 (&h)[2][2], float* sums) {
+        // A part, rows from `from` on, from state h: rebuilt, then backward.
+        auto sub = [&](int from, F2 (&h)[2][2], float* sums) {
             asm volatile("" ::: "memory");
             const Rates A = rates();
             F2 before[kSub][2][2];
 #pragma unroll
             for (int j = 0; j < kSub; ++j) {
-                if (!whole.value && from + j >= to) break;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll
@@ -951,7 +957,6 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             }
 #pragma unroll
             for (int j = kSub - 1; j >= 0; --j) {
-                if (!whole.value && from + j >= to) continue;
                 const int k = from + j;
                 asm volatile("" ::: "memory");   // (tokens further ahead would not fit the registers)
                 const Inputs v = inputs(k);
@@ -1006,10 +1011,9 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             __syncthreads();
             const int32_t start = cu[n];
             const int cnt = te - ta;
-            // The tile in parts on the grid of kSub tokens: the states before all but the first are
-            // formed on one walk, then the parts are taken from the last one on.
-            const int off = ta % kBack;             // the tile's rows of the grid: from
-            const int p0 = off / kSub, p1 = (off + cnt - 1) / kSub;   // off on; its parts
+            // The tile in parts of kSub tokens: the states before all but the first are formed on one
+            // walk, then the parts are taken from the last one on.
+            const int off = ta % kBack, p0 = off / kSub, p1 = (off + cnt - 1) / kSub;
             const float* enters = ta == start ? (p.S0 ? p.S0 + n * Dn : nullptr)
                                               : p.states + ta / kBack * Dn;
             F2 h[2][2];
@@ -1028,34 +1032,19 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 }
                 __syncwarp();   // the place takes the part's sums from here on
             };
-            if (cnt == kBack) {
+            {
                 const Rates A = rates();
 #pragma unroll 1
-                for (int part = 1; part < kParts; ++part) {
+                for (int part = p0; part < p1; ++part) {
 #pragma unroll
-                    for (int k = 0; k < kSub; ++k) advance(A, (part - 1) * kSub + k, h);
-                    keep(part);
+                    for (int j = 0; j < kSub; ++j) advance(A, part * kSub + j, h);
+                    keep(part + 1);
                 }
+            }
 #pragma unroll 1
-                for (int part = kParts - 1; part >= 0; --part) {
-                    back_to(part);
-                    sub(std::true_type(), part * kSub, (part + 1) * kSub, h, s.part[warp][part]);
-                }
-            } else {
-                const Rates A = rates();
-#pragma unroll 1
-                for (int k = 0; k < cnt; ++k) {
-                    if (k > 0 && (off + k) % kSub == 0) keep((off + k) / kSub);
-                    if (k + 1 < cnt) advance(A, k, h);
-                }
-#pragma unroll 1
-                for (int part = p1; part >= p0; --part) {
-                    back_to(part);
-                    const int from = part == p0 ? 0 : part * kSub - off;
-                    const int to = part == p1 ? cnt : (part + 1) * kSub - off;
-                    sub(std::false_type(), from, to, h,
-                        s.part[warp][part] + (off + from) % kSub * 2 * NP);
-                }
+            for (int part = p1; part >= p0; --part) {
+                back_to(part);
+                sub(part * kSub, h, s.part[warp][part]);
             }
             __syncthreads();
             finish(ta, cnt);
@@ -1263,7 +1252,7 @@ Cut make_cut(int32_t N, int64_t T, int32_t H, int32_t d, int ch, int want) {
     Cut c = {};
     c.per_group = (d + ch - 1) / ch;
     const int64_t blocks = (int64_t)c.per_group * H, fill = want * sms();
-    if (N == 0 || N * blocks >= fill || T < (int64_t)N * 64) {
+    if (N == 0 || N * blocks >= fill || T < (int64_t)N * 64 || T < 256) {
         c.nseg = N;
     } else {
         const int64_t most = (2 * fill + blocks - 1) / blocks;   // segments that fill it twice
@@ -1351,17 +1340,14 @@ cudaError_t run_scan(const ScanArgs& a, const Cut& cut, const Maps& maps, int32_
     });
 }
 
+// (in, out: of the empty sequences)
 cudaError_t run_join(const ScanArgs& a, const Cut& cut, const Maps& maps, bool reversed,
-                     const int32_t* status, cudaStream_t stream) {
+                     const float* in, float* out, const int32_t* status, cudaStream_t stream) {
     const int64_t D = (int64_t)a.H * a.d;
     join_kernel<<<(unsigned)((D * a.n + kThreads - 1) / kThreads), kThreads, 0, stream>>>(
-        a, cut, maps, reversed, status);
-    return cudaGetLastError();
-}
-
-cudaError_t run_empty(const ScanArgs& a, const float* in, float* out, const int32_t* status,
-                      cudaStream_t stream) {
-    if (a.num_seqs == 0 || !out) return cudaSuccess;
+        a, cut, maps, reversed, in, out, status);
+    const cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess || a.num_seqs <= kJoinEmpty || !out) return err;
     const int64_t row = (int64_t)a.H * a.d * a.n;
     empty_kernel<<<(unsigned)(a.num_seqs < 1024 ? a.num_seqs : 1024), kThreads, 0, stream>>>(
         a.cu_seqlens, a.num_seqs, row, in, out, status);
@@ -1388,8 +1374,7 @@ cudaError_t run_forward(const ScanArgs& args, char* ws, int32_t* status, cudaStr
             a.S0 = copy;
         }
         cudaError_t err = run_scan<kMaps>(a, cut, maps, status, stream);
-        if (err == cudaSuccess) err = run_join(a, cut, maps, false, status, stream);
-        if (err == cudaSuccess) err = run_empty(a, a.S0, a.S_T, status, stream);
+        if (err == cudaSuccess) err = run_join(a, cut, maps, false, a.S0, a.S_T, status, stream);
         if (err != cudaSuccess) return err;
     }
     return run_scan<kOutputs>(a, cut, maps, status, stream);
@@ -1463,8 +1448,7 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
     }
     if (cut.seg) {
         err = run_scan<kGradMaps>(a, grad_map_cut(cut, a.H, a.d, a.n), maps, status, stream);
-        if (err == cudaSuccess) err = run_join(a, cut, maps, true, status, stream);
-        if (err == cudaSuccess) err = run_empty(a, a.dS_T, a.g.dS0, status, stream);
+        if (err == cudaSuccess) err = run_join(a, cut, maps, true, a.dS_T, a.g.dS0, status, stream);
         if (err != cudaSuccess) return err;
     }
     err = by_type(a.dtype, [&](auto* t) {
