@@ -591,14 +591,23 @@ struct Back {
         float B[kBack][kNp], C[kBack][kNp];
         float y[kBack][kCh];                 // C . h
         float s[2][kBack][kCh];              // B . g and A . (g a h)
-        // A warp's states before the tile's parts but the first, a place a lane; and, where a part's
-        // have been used, dB and dC of its tokens over the warp's channels.
+        // A warp's states before the tile's parts, a place a lane; and, where a part's have been
+        // used, dB and dC of its tokens over the warp's channels.
         float part[kWarps][kParts][kPart];
         float acc[2][kWarps][kCh];           // sums for dskip and ddt_bias
     };
 };
 template <int CH, int V>
 __device__ __forceinline__ int channel_slot(int c) { return c % V * (CH / V) + c / V; }
+
+// U channels' values of a parameter that may be absent.
+template <int U>
+__device__ __forceinline__ Pack<float, U> channels(const float* p, int32_t at) {
+    Pack<float, U> k;
+    if (p) k.load(p + at);
+    else k.zero();
+    return k;
+}
 
 // Sums v[0..N) over the lanes that differ in the bits LO .. HI (powers of two): each exchange
 // halves the values a lane carries, down to one, and adds it up from there on.  Returns the index of
@@ -772,14 +781,19 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                     continue;
                 }
                 if (!kLoaded) load(i, 0);
+                constexpr int U = V < 4 ? V : 4;
 #pragma unroll
-                for (int q = 0; q < V; ++q) {
-                    float v = kd[j].get(q) + (p.dt_bias ? p.dt_bias[base + c + q] : 0.f);
-                    if (p.softplus) v = softplus(v);
-                    const float u = v * kx[j].get(q);
-                    const float dr = Z ? kg[j].get(q) * silu(kz[j].get(q)) : kg[j].get(q);
-                    s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
-                    s.dr[k][q * VR + c / V] = dr;
+                for (int q0 = 0; q0 < V; q0 += U) {
+                    const Pack<float, U> bias = channels<U>(p.dt_bias, base + c + q0);
+#pragma unroll
+                    for (int q = q0; q < q0 + U; ++q) {
+                        float v = kd[j].get(q) + bias.get(q - q0);
+                        if (p.softplus) v = softplus(v);
+                        const float u = v * kx[j].get(q);
+                        const float dr = Z ? kg[j].get(q) * silu(kz[j].get(q)) : kg[j].get(q);
+                        s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
+                        s.dr[k][q * VR + c / V] = dr;
+                    }
                 }
             }
             if (packed) {
@@ -831,17 +845,18 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 for (int q0 = 0; q0 < V; q0 += U) {
                     float acc[2 * U] = {};   // for dskip, for ddt_bias
                     if (in) {
+                        const Pack<float, U> bias = channels<U>(p.dt_bias, base + c + q0);
+                        const Pack<float, U> skips = channels<U>(p.skip, base + c + q0);
                         float dx[U], dz[U];
 #pragma unroll
                         for (int j = 0; j < U; ++j) {
                             const int q = q0 + j, sl = q * VR + c / V;
-                            const float skip = p.skip ? p.skip[base + c + q] : 0.f;
+                            const float skip = skips.get(j);
                             const float x = kx.get(q), s1 = s.s[0][k][sl], dr = s.dr[k][sl];
                             acc[j] = dr * x;
                             float ddt = fmaf(x, s1, s.s[1][k][sl] * kLn2);
                             if (p.softplus)
-                                ddt *= sigmoid(kd.get(q) +
-                                               (p.dt_bias ? p.dt_bias[base + c + q] : 0.f));
+                                ddt *= sigmoid(kd.get(q) + bias.get(j));
                             acc[U + j] = ddt;
                             dx[j] = fmaf(s.du[k][sl].x, s1, skip * dr);
                             if (Z)
@@ -1008,30 +1023,25 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         __syncthreads();
         if (te > t0) convert(ta, te - ta);
         while (te > t0) {
-            __syncthreads();
             const int32_t start = cu[n];
             const int cnt = te - ta;
-            // The tile in parts of kSub tokens: the states before all but the first are formed on one
-            // walk, then the parts are taken from the last one on.
+            // The tile in parts of kSub tokens: the states before them are formed on one walk,
+            // then the parts are taken from the last one on.
             const int off = ta % kBack, p0 = off / kSub, p1 = (off + cnt - 1) / kSub;
-            const float* enters = ta == start ? (p.S0 ? p.S0 + n * Dn : nullptr)
-                                              : p.states + ta / kBack * Dn;
             F2 h[2][2];
-            load4(enters, h);
+            load4(ta == start ? (p.S0 ? p.S0 + n * Dn : nullptr) : p.states + ta / kBack * Dn, h);
+            __syncthreads();
             auto place = [&](int part) { return reinterpret_cast<F2*>(s.part[warp][part]) + lane; };
             auto keep = [&](int part) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) place(part)[i * 32] = h[i / 2][i % 2];
             };
             auto back_to = [&](int part) {
-                if (part == p0) {
-                    load4(enters, h);
-                } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) h[i / 2][i % 2] = place(part)[i * 32];
-                }
+                for (int i = 0; i < 4; ++i) h[i / 2][i % 2] = place(part)[i * 32];
                 __syncwarp();   // the place takes the part's sums from here on
             };
+            keep(p0);
             {
                 const Rates A = rates();
 #pragma unroll 1
