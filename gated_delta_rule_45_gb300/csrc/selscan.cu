@@ -76,6 +76,28 @@ struct Cut {
     int64_t items;      // nseg x blocks
 };
 
+// The sequence of `rank` in the order longest first (by number among equals): sequences of very
+// different lengths, each a CTA's, then end together.  All threads of the CTA call it; batches
+// of more than kRanked sequences keep their order.
+constexpr int kRanked = 128;
+__device__ __forceinline__ int32_t ranked_sequence(const int32_t* cu, int32_t N, int32_t rank,
+                                                   volatile int32_t* found) {
+    if (N > kRanked || N < 2) return rank;
+    for (int32_t i = threadIdx.x; i < N; i += blockDim.x) {
+        const int32_t len = cu[i + 1] - cu[i];
+        int32_t before = 0;
+        for (int32_t j = 0; j < N; ++j) {
+            const int32_t other = cu[j + 1] - cu[j];
+            before += other > len || (other == len && j < i);
+        }
+        if (before == rank) *found = i;
+    }
+    __syncthreads();
+    const int32_t n = *found;
+    __syncthreads();
+    return n;
+}
+
 // The maps of the segments, in the workspace.
 struct Maps {
     float* sum;     // [nseg][D]      sum of the step sizes
@@ -196,7 +218,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         int32_t n;
         bool reset = false;
         if (cut.seg == 0) {
-            n = (int32_t)sg;
+            n = ranked_sequence(cu, p.num_seqs, (int32_t)sg, reinterpret_cast<int32_t*>(s_du));
             t0 = cu[n];
             t1 = cu[n + 1];
         } else {
@@ -677,7 +699,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
         int32_t t0, t1;
         int32_t n;
         if (cut.seg == 0) {
-            n = (int32_t)sg;
+            n = ranked_sequence(cu, p.num_seqs, sg, reinterpret_cast<int32_t*>(&s.part));
             t0 = cu[n];
             t1 = cu[n + 1];
         } else {
@@ -1256,28 +1278,32 @@ int back_channels(int n) {
     }
 }
 
-// Whole sequences where they and the channel blocks of `ch` make at least `want` CTAs an SM, or
-// are short; else segments that do.
-Cut make_cut(int32_t N, int64_t T, int32_t H, int32_t d, int ch, int want) {
+// Whole sequences where they and the channel blocks of `ch` make `fill` CTAs an SM, or are short;
+// else segments of at least `least` tokens, as many as take the GPU's places (`each` CTAs an SM)
+// twice.  (A last round that fills them in part costs as much as a whole one: 131072 x 4096 in 960
+// pieces on 608 places took 5.25 ms, in 1216 it takes 4.6.)
+Cut make_cut(int32_t N, int64_t T, int32_t H, int32_t d, int ch, int each, int fill,
+             int least) {
     Cut c = {};
     c.per_group = (d + ch - 1) / ch;
-    const int64_t blocks = (int64_t)c.per_group * H, fill = want * sms();
-    if (N == 0 || N * blocks >= fill || T < (int64_t)N * 64 || T < 256) {
+    const int64_t blocks = (int64_t)c.per_group * H;
+    if (N == 0 || N * blocks >= fill * sms() || T < (int64_t)N * 64 || T < 256) {
         c.nseg = N;
     } else {
-        const int64_t most = (2 * fill + blocks - 1) / blocks;   // segments that fill it twice
+        int64_t most = 2 * each * sms() / blocks;
+        if (most < 1) most = 1;
         c.seg = ((T + most - 1) / most + kTile - 1) / kTile * kTile;
-        if (c.seg < 64) c.seg = 64;
+        if (c.seg < least) c.seg = least;
         c.nseg = (T + c.seg - 1) / c.seg;
     }
     c.items = c.nseg * blocks;
     return c;
 }
 Cut forward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
-    return make_cut(N, T, H, d, forward_channels(n), 3);
+    return make_cut(N, T, H, d, forward_channels(n), n <= 8 ? 8 : 4, 3, 64);
 }
 Cut backward_cut(int32_t N, int64_t T, int32_t H, int32_t d, int32_t n) {
-    return make_cut(N, T, H, d, back_channels(n), 1);
+    return make_cut(N, T, H, d, back_channels(n), n <= 8 ? 2 : 4, 1, 128);
 }
 // The maps of the gradients' recurrence are formed by the forward kernel: the same segments, but
 // its own channel blocks.
