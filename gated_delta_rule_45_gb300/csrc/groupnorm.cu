@@ -11,7 +11,8 @@
 // the parameters are read once, and their gradients are summed in registers and joined by a
 // second kernel in a fixed order.
 //
-// Bound: HBM.
+// Bound: HBM.  Measured, bf16 with a gate, 32768 x 32 x 128: forward 151 us (0.8 GB, 5.3 TB/s; 208
+// without the next row's loads ahead), backward 356 us (1.9 GB, 5.3).
 #include "layer_ops.h"
 
 #include <type_traits>

@@ -6,21 +6,32 @@
 // are inputs, for two multiply-adds each.
 //
 // Forward: a channel lies in L lanes of 8 values each (n padded to 8, 16, 32 or 64), its
-// rates and state in registers.  A CTA walks its tokens in tiles of 32: the step sizes and D x
-// are formed once a (token, channel) into shared memory, the state is carried through the
-// tile, and the sums over the state are finished (skip, gate, rounding) by another pass over
-// the tile in rows of 16 bytes.
+// rates and state in registers.  A CTA walks its tokens in tiles of 16, on the grid of `states`: the
+// step sizes and D x are formed once a (token, channel) into shared memory, the state is carried
+// through the tile, and the sums over the state are finished (skip, gate, rounding) by a pass
+// over the tile in rows of 16 bytes; the next tile's rows are loaded meanwhile, and two buffers
+// make one barrier a tile do.
 //
-// Work along the tokens: where the sequences alone fill the GPU a CTA walks a whole sequence.
-// Few long ones are cut into segments of the packed axis, regardless of sequences: the map of
-// a segment is its end state from zero and the sum of its step sizes (the product of its
-// decays is exp(A sum D)), a short pass joins the maps, and the segments are walked from
+// Work along the tokens: where the sequences alone fill the GPU a CTA walks a whole sequence, the
+// longest first.  Few long ones are cut into segments of the packed axis, regardless of sequences:
+// the map of a segment is its end state from zero and the sum of its step sizes (the product of
+// its decays is exp(A sum D)), a short pass joins the maps, and the segments are walked from
 // their entry states.  The backward pass does the same on reversed tokens.
 //
-// Backward: rebuilds the states of 8 tokens at a time in registers from `states` (every 16th
-// token), then walks them backward.
+// Backward: from `states` (every 16th token) the states before every 4th token are formed on one
+// walk; each four tokens' states are then rebuilt in registers and walked backward.  Sums over
+// the values or the channels are halved with each exchange (spread_sum); those over a CTA's
+// channels go on in a second kernel.  A tile cut short by a sequence is a whole one with rows of
+// steps and inputs of zero around it.
 //
-// Bound: the exponentials and the instructions around them; HBM for small n.
+// Bound: instructions, with the exponentials at a third of their unit's rate (32 a clock and SM).
+// Measured, bf16, n = 16 with gate and skip: 64 ragged prompts of 266240 x 2048 2.68 ms (4.4 GB,
+// 1.6 TB/s; 8.7e9 exponentials, which alone take 0.93 ms: issue 2.3 a clock and SM of 4), one of
+// 131072 x 4096 4.6 ms (cut: each exponential twice), forward of 8 x 4096 x 4096 with `states` 0.84
+// ms, backward 3.6 ms (2.75 exponentials and 30 instructions a value; issue 1.9 a clock and SM, waits
+// for shared memory, exchanges and loads in equal parts).  Two channels a lane take a tenth fewer
+// instructions but leave half the warps: 10 to 25 % slower.  Warps of their own for the passes
+// before and after the walk: 50 % slower.
 #include "layer_ops.h"
 
 #include <type_traits>
@@ -604,7 +615,7 @@ struct Back {
     static constexpr int kCh = kThreads / NL * 2;
     static constexpr int kNp = 4 * NL;
     static constexpr int kPart = 2 * kNp * kSub > 256 ? 2 * kNp * kSub : 256;
-    // Channels lie in the order of the threads that write them, V at a time (channel_slot); step and
+    // Channels lie in the order of the threads that write them, V at a time; step and
     // u twice over, as the packed instructions take them.
     struct Shared {
         float4 du[kBack][kCh];               // D, D, D x, D x
@@ -619,8 +630,14 @@ struct Back {
         float acc[2][kWarps][kCh];           // sums for dskip and ddt_bias
     };
 };
-template <int CH, int V>
-__device__ __forceinline__ int channel_slot(int c) { return c % V * (CH / V) + c / V; }
+// The place of a slot in the rows of single values: turned by `by` (its low two bits) times eight
+// places, by the row, so that lanes that hold four rows, and (by the value) four values of one
+// row, meet four different quarters of the banks.  (Within a half of the row: the halves hold a
+// thread's two channels, which are turned differently.)
+template <int CH>
+__device__ __forceinline__ int place_of(int by, int slot) {
+    return slot ^ ((by & 3) * 8 & (CH / 2 - 1));
+}
 
 // U channels' values of a parameter that may be absent.
 template <int U>
@@ -798,7 +815,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
 #pragma unroll
                     for (int q = 0; q < V; ++q) {
                         s.du[k][q * VR + c / V] = make_float4(0.f, 0.f, 0.f, 0.f);
-                        s.dr[k][q * VR + c / V] = 0.f;
+                        s.dr[k][place_of<CH>(k, q * VR + c / V)] = 0.f;
                     }
                     continue;
                 }
@@ -814,7 +831,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                         const float u = v * kx[j].get(q);
                         const float dr = Z ? kg[j].get(q) * silu(kz[j].get(q)) : kg[j].get(q);
                         s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
-                        s.dr[k][q * VR + c / V] = dr;
+                        s.dr[k][place_of<CH>(k, q * VR + c / V)] = dr;
                     }
                 }
             }
@@ -874,15 +891,16 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                         for (int j = 0; j < U; ++j) {
                             const int q = q0 + j, sl = q * VR + c / V;
                             const float skip = skips.get(j);
-                            const float x = kx.get(q), s1 = s.s[0][k][sl], dr = s.dr[k][sl];
+                            const int at1 = place_of<CH>(k ^ sl / kOther, sl), at0 = place_of<CH>(k, sl);
+                            const float x = kx.get(q), s1 = s.s[0][k][at1], dr = s.dr[k][at0];
                             acc[j] = dr * x;
-                            float ddt = fmaf(x, s1, s.s[1][k][sl] * kLn2);
+                            float ddt = fmaf(x, s1, s.s[1][k][place_of<CH>(k ^ (2 + sl / kOther), sl)] * kLn2);
                             if (p.softplus)
                                 ddt *= sigmoid(kd.get(q) + bias.get(j));
                             acc[U + j] = ddt;
                             dx[j] = fmaf(s.du[k][sl].x, s1, skip * dr);
                             if (Z)
-                                dz[j] = kg.get(q) * fmaf(skip, x, s.y[k][sl]) * silu_grad(kz.get(q));
+                                dz[j] = kg.get(q) * fmaf(skip, x, s.y[k][at1]) * silu_grad(kz.get(q));
                         }
                         Pack<float, U> o;
                         o.set(dx);
@@ -989,7 +1007,8 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
 #pragma unroll
                     for (int q = 0; q < 2; ++q) y[q] = sum2(fma2(h[q][0], c.x, mul2(h[q][1], c.y)));
                     const int at = spread_sum<2, NL / 2, 1>(y, lane);
-                    if (nl % (NL / 2) == 0) s.y[from + j][slot + at * kOther] = y[0];
+                    if (nl % (NL / 2) == 0)
+                        s.y[from + j][place_of<CH>(j ^ at, slot + at * kOther)] = y[0];
                 }
             }
 #pragma unroll
@@ -1001,7 +1020,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 F2 vB[2] = {0, 0}, vC[2] = {0, 0}, t1[2] = {0, 0}, t2[2] = {0, 0};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float rv = s.dr[k][slot + q * kOther];
+                    const float rv = s.dr[k][place_of<CH>(j, slot + q * kOther)];
                     const F2 rr = pack2(rv, rv);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -1022,8 +1041,10 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 constexpr int kLeftS = spread_left(4, NL / 2, 1);
                 if (NL <= 4 || nl % (NL > 4 ? NL / 4 : 1) == 0) {
 #pragma unroll
-                    for (int i = 0; i < kLeftS; ++i)
-                        s.s[(sat + i) / 2][k][slot + (sat + i) % 2 * kOther] = sv[i];
+                    for (int i = 0; i < kLeftS; ++i) {
+                        const int v = sat + i;
+                        s.s[v / 2][k][place_of<CH>(j ^ v, slot + v % 2 * kOther)] = sv[i];
+                    }
                 }
                 const float2 b0 = unpack2(vB[0]), b1 = unpack2(vB[1]);
                 const float2 e0 = unpack2(vC[0]), e1 = unpack2(vC[1]);

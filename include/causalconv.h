@@ -64,8 +64,8 @@ size_t causalconv_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens,
  *
  * kda_prefill_device_status(workspace) reports device-detected errors
  * (KDA_ERR_DEVICE_INPUT).  Supported: 2 <= W <= 4, 1 <= D <= 2^20,
- * total_tokens <= 2^31 - 1 - 4096, num_seqs <= 2^30, ldx < 2^40, and T x D and
- * num_seqs x D each < 2^44.
+ * total_tokens <= 2^31 - 1 - 4096, num_seqs <= 2^30, ldx < 2^40, T x D < 2^42,
+ * num_seqs x D < 2^36.
  */
 kda_status causalconv_prefill(const void* x, int64_t ldx, const float* w, const float* b,
                               const void* S0, const int32_t* cu_seqlens, int32_t num_seqs,
@@ -73,8 +73,8 @@ kda_status causalconv_prefill(const void* x, int64_t ldx, const float* w, const 
                               causalconv_activation activation, void* y, void* S_T,
                               void* workspace, size_t workspace_bytes, kda_stream_t stream);
 
-/* Bytes of device workspace causalconv_backward needs: about T x D x (W + 1) / 32
- * at most.  Returns 0 for a size it does not support. */
+/* Bytes of device workspace causalconv_backward needs: at most about T x D x (W + 1) / 8.
+ * Returns 0 for a size it does not support. */
 size_t causalconv_backward_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t D,
                                           int32_t W);
 

@@ -28,7 +28,8 @@
  *
  * The state, step sizes, decays and every sum are fp32; y is rounded once to
  * dtype.  D_t A is meant to be <= 0; any finite one gives the recurrence's
- * result as long as the decays' products over a sequence stay finite.  A decay below
+ * result as long as the states, and the decays' products over the tokens of a
+ * sequence, stay finite.  A decay below
  * 2^-126 may count as 0, and so may what products of decays below that leave of a
  * state.
  * A sequence whose values are not finite never reaches another sequence's
@@ -87,8 +88,8 @@ size_t selscan_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, in
  *
  * kda_prefill_device_status(workspace) reports device-detected errors
  * (KDA_ERR_DEVICE_INPUT).  Supported: H >= 1, d >= 1, 1 <= n <= 64,
- * H x d <= 2^20, total_tokens <= 2^31 - 1 - 4096, num_seqs <= 65535,
- * distances between rows < 2^40, T x H x d x n < 2^46.
+ * H x d <= 2^20, total_tokens <= 2^31 - 1 - 4096, num_seqs <= 2^30,
+ * distances between rows < 2^40, T x H x d x n < 2^46, num_seqs x H x d x n < 2^42.
  */
 kda_status selscan_prefill(const selscan_rows* rows, const float* A, const float* skip,
                            const float* dt_bias, const float* S0, const int32_t* cu_seqlens,
@@ -154,7 +155,8 @@ kda_status selscan_backward(const selscan_rows* rows, const float* A, const floa
  *   S_out     [B][H][d][n] fp32; may equal S when parents is NULL, else it must
  *             not overlap S
  *
- * Supported: as selscan_prefill, B and num_rows <= 2^30; B == 0 is a valid no-op.
+ * Supported: as selscan_prefill with B in T's place and B or num_rows in num_seqs'; B x H x d
+ * < 2^35; B == 0 is a valid no-op.
  */
 kda_status selscan_decode_step(const selscan_rows* rows, const float* A, const float* skip,
                                const float* dt_bias, const float* S, int32_t num_rows,
