@@ -21,7 +21,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRun = 64;     // tokens a thread, forward
+constexpr int kMaxRun = 256;    // tokens a thread, forward
 constexpr int kBatch = 8;       // rows loaded at once
 constexpr int kBackBatch = 4;   // and of both tensors, backward
 constexpr int kMinParts = 256;  // runs of the backward pass, where there are tokens for them

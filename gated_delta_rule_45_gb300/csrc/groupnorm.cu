@@ -485,7 +485,7 @@ NormGrid norm_grid(int64_t T, int32_t H, int32_t d, int V, int64_t parts) {
     g.tpb = groups / g.hpb;
     g.hblocks = (H + g.hpb - 1) / g.hpb;
     g.tblocks = (T + g.tpb - 1) / g.tpb;
-    const int64_t most = (8 * sms + g.hblocks - 1) / g.hblocks;
+    const int64_t most = (4 * sms + g.hblocks - 1) / g.hblocks;
     if (g.tblocks > most) g.tblocks = most;
     if (parts > 0 && g.tblocks * g.tpb > parts) g.tblocks = parts / g.tpb > 0 ? parts / g.tpb : 1;
     return g;

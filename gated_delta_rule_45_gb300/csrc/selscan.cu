@@ -1184,7 +1184,7 @@ scan_step_kernel(const ScanStepArgs p, int32_t per_group, int32_t rows) {
         if (!live) return;
         if (whole) {
             if (k < p.n) {
-                const float4 u = __ldcs(reinterpret_cast<const float4*>(at));
+                const float4 u = *reinterpret_cast<const float4*>(at);
                 v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
             }
         } else {

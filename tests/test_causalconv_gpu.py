@@ -77,6 +77,18 @@ def test_strided_rows(left, right, dtype):
     assert all(torch.equal(g[k], g2[k]) for k in g)
 
 
+@pytest.mark.parametrize("lens", [[], [0 if i % 3 else 2 for i in range(1500)]])
+def test_many_and_no_sequences(lens):
+    """More sequences than a CTA checks by itself, and tokens that belong to none."""
+    _check(_case(lens, (12,), 4, torch.float32, tail=9, seed=2))
+
+
+def test_no_rows():
+    c = cuda(_case([], (12,), 4, torch.bfloat16))
+    y = kda.causalconv_decode_step(c["x"], c["w"], c["b"], c["S0"])
+    assert y.shape == (0, 12)
+
+
 def test_extreme_values():
     c = _case([50], (8,), 4, torch.float32, seed=3)
     c["x"] *= 60.0      # arguments of silu from -300 to 300

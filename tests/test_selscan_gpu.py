@@ -155,6 +155,41 @@ def test_cut_along_the_tokens(lens, n, dtype):
     assert all(torch.equal(g[k], g2[k]) for k in g)
 
 
+@pytest.mark.parametrize("lens", [[0 if i % 7 == 3 else 80 for i in range(80)], [3, 0] * 700, [],
+                                  [150] * 20 + [0] + [20] * 130])
+def test_many_and_no_sequences(lens):
+    """Cut along the tokens with more sequences than the join looks over for empty ones, more
+    than a CTA checks or ranks by itself, and tokens that belong to none."""
+    _check(_case(lens, 1, 16, 4, torch.float32, tail=7, seed=len(lens)))
+
+
+def test_two_calls_at_once():
+    """On two streams, from two threads, each with its own workspace."""
+    import threading
+    cs = [cuda(_case([300, 45], 1, 64, 16, torch.bfloat16, seed=s)) for s in (1, 2)]
+    run = lambda c, **kw: kda.selscan_prefill(*_ins(c), **_kw(c), save_states=True, **kw)
+    want = [run(c) for c in cs]
+    back = [kda.selscan_backward(*_ins(c), c["dy"], c["dS_T"], **_kw(c), states=w[2])
+            for c, w in zip(cs, want)]
+    torch.cuda.synchronize()
+    streams, got, grads = [torch.cuda.Stream() for _ in cs], [None, None], [None, None]
+
+    def work(i):
+        for _ in range(20):
+            got[i] = run(cs[i], stream=streams[i])
+            grads[i] = kda.selscan_backward(*_ins(cs[i]), cs[i]["dy"], cs[i]["dS_T"],
+                                            **_kw(cs[i]), states=got[i][2], stream=streams[i])
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert torch.equal(got[i][0], want[i][0]) and torch.equal(got[i][1], want[i][1])
+        assert all(torch.equal(grads[i][k], back[i][k]) for k in back[i])
+
+
 def test_fast_and_slow_decays():
     c = _case([150, 300], 1, 16, 16, torch.float32, seed=2)
     c["A"][:, :4] = -1e-4
