@@ -303,7 +303,7 @@ conv_bwd_kernel(const ConvArgs p, const ConvGrid g, float* part, int32_t* status
         }
     }
     // part[run]: dw by weight, then db
-    float* row = part + at.run * ((int64_t)p.D * (W + 1)) + c;
+    float* row = part + at.run * sum_row(SumColumns{{(int64_t)p.D * W, p.D, 0}}) + c;
 #pragma unroll
     for (int j = 0; j < W; ++j) dw[j].template to<float>().store(row + (int64_t)j * p.D);
     db.template to<float>().store(row + (int64_t)W * p.D);
@@ -402,32 +402,42 @@ constexpr int kSumCols = 32, kSumRows = 8;
 // A CTA sums 32 columns: eight threads a column take every eighth row, in order, and their
 // sums are added in order.
 __global__ void __launch_bounds__(kSumCols * kSumRows)
-column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t n1, int64_t n2,
-                  float* out1, float* out2, const int32_t* status, int32_t turned) {
+column_sum_kernel(const float* __restrict__ part, int64_t rows, int64_t row, const SumColumns cols,
+                  const SumOutputs outs, const int32_t* status, int32_t turned) {
     if (status && *status != KDA_OK) return;
     __shared__ float s[kSumRows][kSumCols];
     const int cl = threadIdx.x % kSumCols, rl = threadIdx.x / kSumCols;
-    const int64_t col = (int64_t)blockIdx.x * kSumCols + cl, n = n1 + n2;
+    int64_t col = (int64_t)blockIdx.x * kSumCols + cl;
+    const bool on = col < cols.n[0] + cols.n[1] + cols.n[2];
     float sum = 0.f;
-    if (col < n) {
+    if (on) {
         int64_t r = rl;
         for (; r + 3 * kSumRows < rows; r += 4 * kSumRows) {
             float v[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = part[(r + k * kSumRows) * n + col];
+            for (int k = 0; k < 4; ++k) v[k] = part[(r + k * kSumRows) * row + col];
             sum += (v[0] + v[1]) + (v[2] + v[3]);
         }
-        for (; r < rows; r += kSumRows) sum += part[r * n + col];
+        for (; r < rows; r += kSumRows) sum += part[r * row + col];
     }
     s[rl][cl] = sum;
     __syncthreads();
-    if (rl != 0 || col >= n) return;
+    if (rl != 0 || !on) return;
 #pragma unroll
     for (int k = 1; k < kSumRows; ++k) sum += s[k][cl];
-    float* out = col < n1 ? out1 : out2;
-    const int64_t at = col >= n1 ? col - n1
-                       : turned > 1 ? col % (n1 / turned) * turned + col / (n1 / turned) : col;
-    if (out) out[at] = sum;
+    float* out = outs.out[0];
+    if (col < cols.n[0]) {
+        if (turned > 1)
+            col = col % (cols.n[0] / turned) * turned + col / (cols.n[0] / turned);
+    } else {
+        col -= cols.n[0];
+        out = outs.out[1];
+        if (col >= cols.n[1]) {
+            col -= cols.n[1];
+            out = outs.out[2];
+        }
+    }
+    if (out) out[col] = sum;
 }
 
 __global__ void __launch_bounds__(1024)
@@ -468,11 +478,11 @@ int backward_run(int64_t T) {
 
 }  // namespace
 
-cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t n1, int64_t n2,
-                               float* out1, float* out2, const int32_t* status,
-                               cudaStream_t stream, int32_t turned) {
-    const int64_t blocks = (n1 + n2 + kSumCols - 1) / kSumCols;
-    column_sum_kernel<<<(unsigned)blocks, kSumCols * kSumRows, 0, stream>>>(part, rows, n1, n2, out1, out2, status, turned);
+cudaError_t launch_column_sums(const float* part, int64_t rows, SumColumns n, SumOutputs out,
+                               const int32_t* status, cudaStream_t stream, int32_t turned) {
+    const int64_t blocks = (n.n[0] + n.n[1] + n.n[2] + kSumCols - 1) / kSumCols;
+    column_sum_kernel<<<(unsigned)blocks, kSumCols * kSumRows, 0, stream>>>(
+        part, rows, sum_row(n), n, out, status, turned);
     return cudaGetLastError();
 }
 
@@ -488,7 +498,7 @@ size_t conv_prefill_bytes(int32_t num_seqs, int32_t D, int32_t W, kda_dtype dtyp
 }
 size_t conv_backward_bytes(int64_t T, int32_t D, int32_t W) {
     const int run = backward_run(T);
-    return kHead + pad((size_t)((T + run - 1) / run) * D * (W + 1) * sizeof(float));
+    return kHead + pad((size_t)((T + run - 1) / run) * sum_row({(int64_t)D * W, D, 0}) * sizeof(float));
 }
 
 cudaError_t launch_conv_prefill(const ConvArgs& a, char* ws, cudaStream_t stream) {
@@ -545,8 +555,9 @@ cudaError_t launch_conv_backward(const ConvArgs& a, char* ws, cudaStream_t strea
     });
     if (err != cudaSuccess) return err;
     const int run = backward_run(a.total_tokens);
-    return launch_column_sums(part, (a.total_tokens + run - 1) / run, (int64_t)a.D * a.W, a.D, a.dw,
-                              a.db, status, stream, a.W);
+    const int64_t D = a.D;
+    return launch_column_sums(part, (a.total_tokens + run - 1) / run, {D * a.W, D, 0},
+                              {a.dw, a.db, nullptr}, status, stream, a.W);
 }
 
 cudaError_t launch_conv_step(const ConvStepArgs& a, cudaStream_t stream) {

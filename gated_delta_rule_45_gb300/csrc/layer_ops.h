@@ -94,13 +94,19 @@ cudaError_t launch_scan_prefill(const ScanArgs& a, char* ws, cudaStream_t stream
 cudaError_t launch_scan_backward(const ScanArgs& a, char* ws, cudaStream_t stream);
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
 
-// Sums of the rows of part [rows][n1 + n2] in a fixed order: the first n1 columns to out1, the
-// others to out2, either of which may be null.  Nothing is written when *status (may be
-// null) says that the offsets are malformed.  The first n1 columns are a [turned][n1 / turned]
-// matrix that goes to out1 transposed.  (causalconv.cu)
-cudaError_t launch_column_sums(const float* part, int64_t rows, int64_t n1, int64_t n2,
-                               float* out1, float* out2, const int32_t* status,
-                               cudaStream_t stream, int32_t turned = 1);
+// Sums of the rows of part in a fixed order.  A row holds n[0], n[1] and n[2] columns for out[0],
+// out[1] and out[2], any of which may be null, and is whole vectors of four long.  Nothing is
+// written when *status (may be null) says that the offsets are malformed.  The first columns are a
+// [turned][n[0] / turned] matrix that goes to out[0] transposed.  (causalconv.cu)
+struct SumColumns {
+    int64_t n[3];
+};
+struct SumOutputs {
+    float* out[3];
+};
+cudaError_t launch_column_sums(const float* part, int64_t rows, SumColumns n, SumOutputs out,
+                               const int32_t* status, cudaStream_t stream, int32_t turned = 1);
+__host__ __device__ inline int64_t sum_row(const SumColumns& n) { return (n.n[0] + n.n[1] + n.n[2] + 3) / 4 * 4; }
 // status = whether the offsets are well formed; nothing for up to kSelfCheck sequences, unless
 // `always`.
 cudaError_t launch_offsets_check(const int32_t* cu, int32_t N, int64_t T, int32_t* status,

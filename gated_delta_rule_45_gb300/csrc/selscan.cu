@@ -607,6 +607,9 @@ empty_kernel(const int32_t* cu, int32_t N, int64_t row, const float* in, float* 
 
 // ---------------------------------------------------------------- backward
 
+// A segment's sums for dA, dskip and ddt_bias, whole vectors long.
+__host__ __device__ inline int64_t part_row(int64_t D, int32_t n) { return (D * (n + 2) + 3) / 4 * 4; }
+
 // NL lanes share two channels, four values of each a lane.
 template <int NL>
 struct Back {
@@ -680,8 +683,8 @@ constexpr int spread_left(int n, int hi, int lo) {
 
 template <typename T, int NL, int V>
 __global__ void __launch_bounds__(Back<NL>::kThreads, V == 1 ? 1 : 4)
-scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A, float* part_c,
-                float* part_BC, const int32_t* status) {
+scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, float* part_BC,
+                const int32_t* status) {
     using G = Back<NL>;
     constexpr int CH = G::kCh, TH = G::kThreads, NP = G::kNp;
     constexpr int VR = CH / V;                              // vectors of a row
@@ -1116,7 +1119,8 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
                 convert(ta, te - ta);
             }
         }
-        store4(part_A + sg * Dn, dA);
+        float* const sums = part + sg * part_row(D, p.n);
+        store4(sums, dA);
         __syncthreads();
         // the warps, in order
         for (int i = tid; i < 2 * CH; i += TH) {
@@ -1124,7 +1128,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part_A,
             float sum = 0.f;
 #pragma unroll
             for (int w = 0; w < G::kWarps; ++w) sum += s.acc[which][w][sl];
-            if (c < width) part_c[((int64_t)sg * 2 + which) * D + base + c] = sum;
+            if (c < width) sums[Dn + (int64_t)which * D + base + c] = sum;
         }
         __syncthreads();
     }
@@ -1438,7 +1442,7 @@ cudaError_t run_forward(const ScanArgs& args, char* ws, int32_t* status, cudaStr
 }
 
 struct BackLayout {
-    size_t maps, part_A, part_c, part_BC, states, forward, end;
+    size_t maps, part, part_BC, states, forward, end;
 };
 BackLayout back_layout(const Cut& cut, int32_t N, int64_t T, int32_t H, int32_t d, int32_t n,
                        bool with_states) {
@@ -1447,10 +1451,8 @@ BackLayout back_layout(const Cut& cut, int32_t N, int64_t T, int32_t H, int32_t 
     size_t at = kHead;
     L.maps = at;
     at += maps_bytes(cut, D, n);
-    L.part_A = at;
-    at += pad((size_t)cut.nseg * D * n * 4);
-    L.part_c = at;
-    at += pad((size_t)cut.nseg * 2 * D * 4);
+    L.part = at;   // [segment][dA, dskip, ddt_bias]
+    at += pad((size_t)cut.nseg * part_row(D, n) * 4);
     L.part_BC = at;
     if (cut.per_group > 1) at += pad((size_t)cut.per_group * T * H * 2 * n * 4);
     L.states = at;
@@ -1487,12 +1489,11 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
     const BackLayout L = back_layout(cut, a.num_seqs, a.total_tokens, a.H, a.d, a.n,
                                      a.states != nullptr);
     const Maps maps = place_maps(cut, D, a.n, ws + L.maps);
-    float* part_A = reinterpret_cast<float*>(ws + L.part_A);
-    float* part_c = reinterpret_cast<float*>(ws + L.part_c);
+    float* part = reinterpret_cast<float*>(ws + L.part);
     float* part_BC = reinterpret_cast<float*>(ws + L.part_BC);
-    // (the backward kernels read the outcome, whatever the batch's size)
+    // (the backward kernel reads the outcome; the forward kernel leaves it there if it runs before)
     cudaError_t err = launch_offsets_check(a.cu_seqlens, a.num_seqs, a.total_tokens, status, stream,
-                                           true);
+                                           a.states && cut.seg == 0);
     if (err != cudaSuccess) return err;
     if (!a.states) {   // the forward scan once more, for the states alone
         ScanArgs f = a;
@@ -1523,8 +1524,7 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
             if (e != cudaSuccess) return e;
             const int64_t most = (int64_t)1 << 30;
             const unsigned grid = (unsigned)(cut.items < 1 ? 1 : cut.items < most ? cut.items : most);
-            kernel<<<grid, Back<NL>::kThreads, smem, stream>>>(a, cut, maps, part_A, part_c, part_BC,
-                                                               status);
+            kernel<<<grid, Back<NL>::kThreads, smem, stream>>>(a, cut, maps, part, part_BC, status);
             return cudaGetLastError();
         });
     });
@@ -1537,9 +1537,8 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
         err = cudaGetLastError();
         if (err != cudaSuccess) return err;
     }
-    err = launch_column_sums(part_A, cut.nseg, D * a.n, 0, a.g.dA, nullptr, status, stream);
-    if (err != cudaSuccess || (!a.g.dskip && !a.g.ddt_bias)) return err;
-    return launch_column_sums(part_c, cut.nseg, D, D, a.g.dskip, a.g.ddt_bias, status, stream);
+    return launch_column_sums(part, cut.nseg, {D * a.n, D, D}, {a.g.dA, a.g.dskip, a.g.ddt_bias},
+                              status, stream);
 }
 
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream) {
