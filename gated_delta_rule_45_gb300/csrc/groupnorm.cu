@@ -11,8 +11,8 @@
 // the parameters are read once, and their gradients are summed in registers and joined by a
 // second kernel in a fixed order.
 //
-// Bound: HBM.  Measured, bf16 with a gate, 32768 x 32 x 128: forward 151 us (0.8 GB, 5.3 TB/s; 208
-// without the next row's loads ahead), backward 356 us (1.9 GB, 5.3).
+// Bound: HBM.  Measured, bf16 with a gate, 32768 x 32 x 128: forward 150 us (0.8 GB, 5.4 TB/s; 208
+// without the next row's loads ahead), backward 350 us (1.9 GB, 5.4); issue slots 76 and 64 % busy.
 #include "layer_ops.h"
 
 #include <type_traits>
@@ -100,7 +100,7 @@ __device__ __forceinline__ float normalise(const Row<T, V, NV>& x, Lane<V> (&xh)
     q.zero();
 #pragma unroll
     for (int j = 0; j < NV; ++j) q.fma(xh[j], xh[j]);
-    const float r = 1.f / sqrtf(group_sum(q.sum(), lanes) * inv_d + eps);
+    const float r = rsqrtf(group_sum(q.sum(), lanes) * inv_d + eps);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -344,7 +344,7 @@ __device__ __forceinline__ void wide_stats(const NormArgs& p, const T* x, float*
             q = fmaf(u, u, q);
         }
     });
-    r = 1.f / sqrtf(block_sum(q, s) / p.d + p.eps);
+    r = rsqrtf(block_sum(q, s) / p.d + p.eps);
 }
 
 template <typename T, int V>

@@ -221,6 +221,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+__device__ __forceinline__ float rcp(float x) {   // one unit in the last place; 0 for x beyond 2^126
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 __device__ __forceinline__ float sum2(F2 a) {
     const float2 v = unpack2(a);
     return v.x + v.y;
@@ -288,12 +293,12 @@ __device__ __forceinline__ Lane<V> load_lane(const void* p, int64_t at) {
 // of |v| log2 e), which counts where the exponential is not small against 1.  It overflows to inf
 // below -88, where the quotient is 0.
 __device__ __forceinline__ float sigmoid(float v) {
-    return __fdividef(1.f, 1.f + ex2(-kLog2e * v));
+    return rcp(1.f + ex2(-kLog2e * v));
 }
 __device__ __forceinline__ F2 sigmoid2(F2 v) {
     const float2 t = unpack2(mul2(v, both(-kLog2e)));
     const float2 u = unpack2(add2(pack2(ex2(t.x), ex2(t.y)), both(1.f)));
-    return pack2(__fdividef(1.f, u.x), __fdividef(1.f, u.y));
+    return pack2(rcp(u.x), rcp(u.y));
 }
 __device__ __forceinline__ float silu(float v) { return v * sigmoid(v); }
 __device__ __forceinline__ F2 silu2(F2 v) { return mul2(v, sigmoid2(v)); }

@@ -50,7 +50,7 @@ typedef enum {
  *
  *   z             gate or NULL (then the activation takes v itself)
  *   param_heads   1 or H: heads of w and b
- *   eps           >= 0, finite
+ *   eps           >= 0, finite (with 0, a head without deviations gives NaN)
  *   y             output [T][H][d] (dtype); may equal x, or z, where those rows
  *                 are dense
  *
