@@ -9,11 +9,13 @@
 // The packed token axis is cut into runs regardless of sequences; at a sequence's first
 // token the window is replaced by the stored state.
 //
-// Bound: HBM.  Measured, bf16, W = 4 with silu: 64 ragged prompts of 266240 x 4096 735 us (4.4 GB,
-// 5.9 TB/s; 791 with runs of 64 tokens, 906 with 8-byte loads and single instructions instead of
-// pairs), 8 x 4096 x 4096 forward 109 us (4.9), backward 233 us (1.07 GB, 4.6; the activation's slope
-// and 13 multiply-adds a value, with 128 tokens a run).  Rows loaded one by one, each where the one
-// eight before was used, instead of eight at once: 916 us (registers leave one CTA an SM).
+// Bound: HBM.  Measured, bf16, W = 4 with silu: 64 ragged prompts of 266240 x 4096 692 us (4.4 GB,
+// 6.3 TB/s; 735 with a division in the sigmoid instead of the reciprocal, with that 791 in runs of
+// 64 tokens, 906 with 8-byte loads and single instructions instead of pairs), 8 x 4096 x 4096
+// forward 102 us (5.3), backward 226 us (1.07 GB, 4.8; waits for loads with 16 warps an SM, the
+// activation's slope and 13 multiply-adds a value; 128 tokens a run).  Rows loaded one by one, each
+// where the one eight before was used, instead of eight at once: 916 us for 735 (registers leave
+// one CTA an SM).
 #include "layer_ops.h"
 
 #include <type_traits>

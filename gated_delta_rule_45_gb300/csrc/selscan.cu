@@ -27,8 +27,8 @@
 // Bound: instructions, with the exponentials at a third of their unit's rate (32 a clock and SM).
 // Measured, bf16, n = 16 with gate and skip: 64 ragged prompts of 266240 x 2048 2.68 ms (4.4 GB,
 // 1.6 TB/s; 8.7e9 exponentials, which alone take 0.93 ms: issue 2.3 a clock and SM of 4), one of
-// 131072 x 4096 4.6 ms (cut: each exponential twice), forward of 8 x 4096 x 4096 with `states` 0.84
-// ms, backward 3.6 ms (2.75 exponentials and 30 instructions a value; issue 1.9 a clock and SM, waits
+// 131072 x 4096 4.6 ms (cut: each exponential twice), forward of 8 x 4096 x 4096 with `states` 0.85
+// ms, backward 3.5 ms (2.75 exponentials and 30 instructions a value; issue 1.9 a clock and SM, waits
 // for shared memory, exchanges and loads in equal parts).  Two channels a lane take a tenth fewer
 // instructions but leave half the warps: 10 to 25 % slower.  Warps of their own for the passes
 // before and after the walk: 50 % slower.
