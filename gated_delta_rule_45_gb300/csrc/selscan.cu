@@ -828,13 +828,21 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
                 for (int q0 = 0; q0 < V; q0 += U) {
                     const Pack<float, U> bias = channels<U>(p.dt_bias, base + c + q0);
 #pragma unroll
-                    for (int q = q0; q < q0 + U; ++q) {
-                        float v = kd[j].get(q) + bias.get(q - q0);
-                        if (p.softplus) v = softplus(v);
-                        const float u = v * kx[j].get(q);
-                        const float dr = Z ? kg[j].get(q) * silu(kz[j].get(q)) : kg[j].get(q);
-                        s.du[k][q * VR + c / V] = make_float4(v, v, u, u);
-                        s.dr[k][place_of<CH>(k, q * VR + c / V)] = dr;
+                    for (int q = q0; q < q0 + U; q += 2) {   // in pairs, single ones in the low half
+                        constexpr int o = V > 1 ? 1 : 0;
+                        F2 v = add2(pack2(kd[j].get(q), kd[j].get(q + o)),
+                                    pack2(bias.get(q - q0), bias.get(q - q0 + o)));
+                        if (p.softplus) v = softplus2(v);
+                        const float2 u = unpack2(mul2(v, pack2(kx[j].get(q), kx[j].get(q + o))));
+                        F2 d = pack2(kg[j].get(q), kg[j].get(q + o));
+                        if (Z) d = mul2(d, silu2(pack2(kz[j].get(q), kz[j].get(q + o))));
+                        const float2 st = unpack2(v), dr = unpack2(d);
+                        s.du[k][q * VR + c / V] = make_float4(st.x, st.x, u.x, u.x);
+                        s.dr[k][place_of<CH>(k, q * VR + c / V)] = dr.x;
+                        if (V > 1) {
+                            s.du[k][(q + o) * VR + c / V] = make_float4(st.y, st.y, u.y, u.y);
+                            s.dr[k][place_of<CH>(k, (q + o) * VR + c / V)] = dr.y;
+                        }
                     }
                 }
             }
@@ -889,7 +897,30 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
                     if (in) {
                         const Pack<float, U> bias = channels<U>(p.dt_bias, base + c + q0);
                         const Pack<float, U> skips = channels<U>(p.skip, base + c + q0);
-                        float dx[U], dz[U];
+                        // slopes of the step and of the gate, in pairs
+                        float slope[U], dz[U];
+#pragma unroll
+                        for (int j = 0; j < U; j += 2) {
+                            constexpr int o = U > 1 ? 1 : 0;
+                            const int q = q0 + j;
+                            if (p.softplus) {
+                                const float2 t = unpack2(sigmoid2(
+                                    add2(pack2(kd.get(q), kd.get(q + o)),
+                                         pack2(bias.get(j), bias.get(j + o)))));
+                                slope[j] = t.x;
+                                if (U > 1) slope[j + o] = t.y;
+                            } else {
+                                slope[j] = slope[j + o] = 1.f;
+                            }
+                            if (Z) {
+                                const float2 t = unpack2(
+                                    mul2(pack2(kg.get(q), kg.get(q + o)),
+                                         silu_grad2(pack2(kz.get(q), kz.get(q + o)))));
+                                dz[j] = t.x;
+                                if (U > 1) dz[j + o] = t.y;
+                            }
+                        }
+                        float dx[U];
 #pragma unroll
                         for (int j = 0; j < U; ++j) {
                             const int q = q0 + j, sl = q * VR + c / V;
@@ -897,13 +928,10 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
                             const int at1 = place_of<CH>(k ^ sl / kOther, sl), at0 = place_of<CH>(k, sl);
                             const float x = kx.get(q), s1 = s.s[0][k][at1], dr = s.dr[k][at0];
                             acc[j] = dr * x;
-                            float ddt = fmaf(x, s1, s.s[1][k][place_of<CH>(k ^ (2 + sl / kOther), sl)] * kLn2);
-                            if (p.softplus)
-                                ddt *= sigmoid(kd.get(q) + bias.get(j));
-                            acc[U + j] = ddt;
+                            acc[U + j] = slope[j] *
+                                fmaf(x, s1, s.s[1][k][place_of<CH>(k ^ (2 + sl / kOther), sl)] * kLn2);
                             dx[j] = fmaf(s.du[k][sl].x, s1, skip * dr);
-                            if (Z)
-                                dz[j] = kg.get(q) * fmaf(skip, x, s.y[k][at1]) * silu_grad(kz.get(q));
+                            if (Z) dz[j] *= fmaf(skip, x, s.y[k][at1]);
                         }
                         Pack<float, U> o;
                         o.set(dx);
