@@ -242,7 +242,9 @@ norm_bwd_kernel(const NormArgs p, const NormGrid g, float* part) {
         else
             load(x, z, dy, px, pz, out, on);
         Lane<V> xh[NV], gv[NV];
-        const float r = normalise(x, xh, a.lane, g.lanes, nvec, inv_d, p.center, p.eps);
+        // (a group behind the last token has a row of zeros: without an eps 0 / 0, which would
+        // reach its sums over the tokens)
+        const float r = normalise(x, xh, a.lane, g.lanes, nvec, inv_d, p.center, on ? p.eps : 1.f);
         Lane<V> q1, q2;   // g xh and g
         q1.zero();
         q2.zero();
