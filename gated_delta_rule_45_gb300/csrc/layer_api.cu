@@ -418,8 +418,9 @@ kda_status selscan_decode_step(const selscan_rows* rows, const float* A, const f
     if (st == KDA_OK) st = scan_rows_check(rows, B, H, d, n, dtype, step);
     if (st != KDA_OK) return st;
     if (B == 0) return KDA_OK;
-    // CTAs of 16 channels or more are counted in 32 bits
-    if ((int64_t)B * (((int64_t)H * d + 15) / 16) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
+    if ((int64_t)B * H * d >= (int64_t)1 << 35) return KDA_ERR_UNSUPPORTED;
+    int32_t rows_a_warp;
+    if (kda::scan_step_blocks(B, H, d, &rows_a_warp) > INT32_MAX) return KDA_ERR_UNSUPPORTED;
     if (!parents && num_rows != B) return KDA_ERR_INVALID_ARG;
     if (!A || (num_rows > 0 && !S) || !y || !S_out) return KDA_ERR_INVALID_ARG;
     const void* ptrs[] = {A, skip, dt_bias, S, parents, y, S_out};

@@ -92,6 +92,9 @@ size_t scan_backward_bytes(int32_t num_seqs, int64_t total_tokens, int32_t H, in
                            bool with_states);
 cudaError_t launch_scan_prefill(const ScanArgs& a, char* ws, cudaStream_t stream);
 cudaError_t launch_scan_backward(const ScanArgs& a, char* ws, cudaStream_t stream);
+// CTAs that launch_scan_step starts, at most INT32_MAX for a call that it can make, and the rows
+// of the batch that a warp of theirs takes.
+int64_t scan_step_blocks(int32_t B, int32_t H, int32_t d, int32_t* rows);
 cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream);
 
 // Sums of the rows of part in a fixed order.  A row holds n[0], n[1] and n[2] columns for out[0],

@@ -1573,15 +1573,20 @@ cudaError_t launch_scan_backward(const ScanArgs& args, char* ws, cudaStream_t st
                               status, stream);
 }
 
-cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream) {
-    const int32_t per_group = (a.d + 31) / 32;
-    const int64_t warps = (int64_t)per_group * a.H;
+int64_t scan_step_blocks(int32_t B, int32_t H, int32_t d, int32_t* rows) {
+    const int64_t warps = (int64_t)((d + 31) / 32) * H;
     // as many rows a warp, up to four, as leave each SM 16 warps
-    int32_t rows = 4;
-    while (rows > 1 && (a.B + rows - 1) / rows * warps < 16 * sms()) rows /= 2;
-    const int64_t blocks = ((a.B + rows - 1) / rows * warps + 3) / 4;
+    int32_t r = 4;
+    while (r > 1 && (B + (int64_t)r - 1) / r * warps < 16 * sms()) r /= 2;
+    *rows = r;
     static_assert(kStepThreads == 128, "four warps a CTA");
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    return ((B + (int64_t)r - 1) / r * warps + 3) / 4;
+}
+
+cudaError_t launch_scan_step(const ScanStepArgs& a, cudaStream_t stream) {
+    int32_t rows;
+    const int64_t blocks = scan_step_blocks(a.B, a.H, a.d, &rows);
+    const int32_t per_group = (a.d + 31) / 32;
     return by_type(a.dtype, [&](auto* t) {
         using T = std::remove_pointer_t<decltype(t)>;
         return by_back_lanes(a.n, [&](auto l) {   // (four values a lane, as in the backward pass)

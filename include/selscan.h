@@ -156,7 +156,8 @@ kda_status selscan_backward(const selscan_rows* rows, const float* A, const floa
  *             not overlap S
  *
  * Supported: as selscan_prefill with B in T's place and B or num_rows in num_seqs'; B x H x d
- * < 2^35; B == 0 is a valid no-op.
+ * < 2^35 and ceil(B / 4) x H x ceil(d / 32) <= 2^33 - 4 (which groups of one channel can pass
+ * by itself); B == 0 is a valid no-op.
  */
 kda_status selscan_decode_step(const selscan_rows* rows, const float* A, const float* skip,
                                const float* dt_bias, const float* S, int32_t num_rows,
