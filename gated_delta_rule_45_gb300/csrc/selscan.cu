@@ -63,18 +63,36 @@ __device__ __forceinline__ F2 decay2(F2 step, F2 rate) {
 }
 
 // ln(1 + e^v) = max(v, 0) + ln(1 + e), e = e^-|v|: ln(1 + e) / e on [0, 1] by a polynomial fitted
-// for the least relative error (3e-8), so that small steps keep their relative precision.
+// for the least relative error (3e-8).  e is the step itself where that is small, so it must keep
+// its relative precision: the exponent h = -|v| log2 e is off by half its last place, which for
+// v = -7 is 3e-7 of e and grows with |v| (a step of 1e-3 was off by up to 5e-7, one of e^-70 by
+// 3.5e-6).  What the rounding left out, r = -|v| - h ln 2 with ln 2 in two parts, goes back in as
+// e (1 + r): the fused multiply-add forms it from the whole product (the error-free product of
+// Ogita, Rump and Oishi).  Steps are within the exponential's 2^-22 and a few roundings.  Below
+// 2^-126 they are 0; a NaN goes by the maximum.
 constexpr int kLogTerms = 9;
 __device__ __constant__ const float kLog1p[kLogTerms] = {
     9.999999404e-01f, -4.999949336e-01f, 3.331909776e-01f, -2.484298050e-01f, 1.910600215e-01f,
     -1.366323531e-01f, 7.822583616e-02f, -2.950516902e-02f, 5.232676864e-03f};
+constexpr float kLn2Rest = -1.9046543e-09f;   // ln 2 - kLn2
+__device__ __forceinline__ float positive_part(float v) {   // or NaN
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+    return r;
+}
 __device__ __forceinline__ F2 softplus2(F2 v) {
     const float2 u = unpack2(v);
-    const F2 e = pack2(ex2(-fabsf(u.x) * kLog2e), ex2(-fabsf(u.y) * kLog2e));
+    // (no further than where e is 0, so that r stays finite)
+    const F2 w = pack2(fmaxf(-fabsf(u.x), -128.f), fmaxf(-fabsf(u.y), -128.f));
+    const F2 h = mul2(w, both(kLog2e));
+    const float2 hs = unpack2(h);
+    F2 e = pack2(ex2(hs.x), ex2(hs.y));
+    const F2 r = fma2(h, both(-kLn2Rest), fma2(h, both(-kLn2), w));
+    e = fma2(e, r, e);
     F2 q = pack2(kLog1p[kLogTerms - 1], kLog1p[kLogTerms - 1]);
 #pragma unroll
     for (int i = kLogTerms - 2; i >= 0; --i) q = fma2(q, e, pack2(kLog1p[i], kLog1p[i]));
-    return fma2(q, e, pack2(fmaxf(u.x, 0.f), fmaxf(u.y, 0.f)));
+    return fma2(q, e, pack2(positive_part(u.x), positive_part(u.y)));
 }
 __device__ __forceinline__ float softplus(float v) { return unpack2(softplus2(pack2(v, 0.f))).x; }
 
