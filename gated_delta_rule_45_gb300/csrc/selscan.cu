@@ -57,6 +57,18 @@ constexpr float kNudge = 0x1.8p-26f;
 __device__ __forceinline__ float decay(float step, float rate) {
     return ex2(fmaf(step, rate, kNudge));
 }
+// A log2 e, kept finite: a rate that the factor takes out of range (2.36e38 and more, such as the
+// type's lowest value) would give NaN at a step of 0, which the rows around a short tile have too.
+__device__ __forceinline__ float scaled_rate(float A) {
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tmin.NaN.f32 t, %1, 0f7F7FFFFF;\n\tmax.NaN.f32 %0, t, 0fFF7FFFFF;\n\t}"
+        : "=f"(r) : "f"(A * kLog2e));
+    return r;
+}
+__device__ __forceinline__ F2 scaled_rate2(F2 A) {
+    const float2 v = unpack2(A);
+    return pack2(scaled_rate(v.x), scaled_rate(v.y));
+}
 __device__ __forceinline__ F2 decay2(F2 step, F2 rate) {
     const float2 v = unpack2(fma2(step, rate, pack2(kNudge, kNudge)));
     return pack2(ex2(v.x), ex2(v.y));
@@ -282,7 +294,7 @@ scan_kernel(const ScanArgs p, const Cut cut, const Maps maps, int32_t* status) {
         auto first_state = [&](int32_t m) { load_state(p.S0 ? p.S0 + m * D * p.n : nullptr, h); };
         load_state(p.A, A);
 #pragma unroll
-        for (int i = 0; i < kNs / 2; ++i) A[i] = mul2(A[i], pack2(kLog2e, kLog2e));
+        for (int i = 0; i < kNs / 2; ++i) A[i] = scaled_rate2(A[i]);
         if (PASS == kGradMaps)
             load_state(reset && p.dS_T ? p.dS_T + n * D * p.n : nullptr, h);
         else if (t0 == cu[n])
@@ -586,7 +598,7 @@ join_kernel(const ScanArgs p, const Cut cut, const Maps maps, bool reversed, con
             out[n * D * p.n + i] = in ? in[n * D * p.n + i] : 0.f;
     const int64_t last = p.cu_seqlens[p.num_seqs], segs = (last + cut.seg - 1) / cut.seg;
     const int64_t c = i / p.n;
-    const float A = p.A[i] * kLog2e;
+    const float A = scaled_rate(p.A[i]);
     float h = 0.f;
     for (int64_t s0 = 0; s0 < segs; s0 += kJoin) {
         float e[kJoin], d[kJoin];
@@ -792,7 +804,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
         for (int q = 0; q < 2; ++q)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                s.A[q * 2 + i][tid] = mul2(dA[q][i], pack2(kLog2e, kLog2e));
+                s.A[q * 2 + i][tid] = scaled_rate2(dA[q][i]);
                 dA[q][i] = 0;
             }
         const float* behind = nullptr;
@@ -1253,7 +1265,7 @@ scan_step_kernel(const ScanStepArgs p, int32_t per_group, int32_t rows) {
             const int ch = (from + j) * kAt + mine;
             load(p.A + (int64_t)(base + ch) * p.n + k, ch < width, A[j]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) A[j][i] *= kLog2e;
+            for (int i = 0; i < 4; ++i) A[j][i] = scaled_rate(A[j][i]);
         }
     };
     if (NL <= 4) rates(0);

@@ -29,9 +29,11 @@
  * The state, step sizes, decays and every sum are fp32; y is rounded once to
  * dtype.  D_t A is meant to be <= 0; any finite one gives the recurrence's
  * result as long as the states, and the decays' products over the tokens of a
- * sequence, stay finite.  A decay below
- * 2^-126 may count as 0, and so may what products of decays below that leave of a
- * state.
+ * sequence, stay finite, and backward their gradients, the products of both and
+ * of those with a rate.  A decay below 2^-126 may count as 0, and so may a step
+ * below that and what products of decays below that leave of a state.  Rates
+ * beyond 2.3e38 in size (the type's lowest value, -inf) count as that: they leave
+ * nothing of a state at any step that is not 0.
  * A sequence whose values are not finite never reaches another sequence's
  * outputs.  Results do not depend on timing: the same call on the same inputs
  * gives the same bits.
