@@ -45,6 +45,7 @@ constexpr int kNs = 8;          // state values a lane, forward
 constexpr int kBack = SELSCAN_CHUNK;   // tokens of a backward tile
 constexpr int kSub = 4;         // tokens whose states lie in registers, backward
 constexpr int kParts = kBack / kSub;
+constexpr int kSumTokens = 512;   // whose sums for the parameters are added up by themselves
 static_assert(kTile == SELSCAN_CHUNK, "tiles hold whole chunks");
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -812,6 +813,40 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
         else if (p.dS_T && (t0 < t1 || cut.seg == 0)) behind = p.dS_T + n * Dn;
         load4(behind, r);
         for (int i = tid; i < 2 * G::kWarps * CH; i += TH) (&s.acc[0][0][0])[i] = 0.f;
+        // The sums for dA, dskip and ddt_bias of at most kSumTokens tokens lie in registers and s.acc,
+        // those of the item in its row of `part`: a sequence of any length then loses no more to
+        // roundings than kSumTokens of its tokens and as many sums do.
+        float* const sums = part + sg * part_row(D, p.n);
+        store4(sums, dA);
+        auto each_acc = [&](auto&& f) {   // (a column is the same thread's each time)
+            for (int i = tid; i < 2 * CH; i += TH) {
+                const int which = i / CH, sl = i % CH, c = sl % VR * V + sl / VR;
+                if (c < width) f(sums[Dn + (int64_t)which * D + base + c], which, sl);
+            }
+        };
+        each_acc([&](float& to, int, int) { to = 0.f; });
+        auto add_sums = [&]() {
+            F2 at[2][2];
+            load4(sums, at);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    at[q][i] = add2(at[q][i], dA[q][i]);
+                    dA[q][i] = 0;
+                }
+            store4(sums, at);
+            __syncthreads();
+            each_acc([&](float& to, int which, int sl) {   // the warps, in order
+                float sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < G::kWarps; ++w) {
+                    sum += s.acc[which][w][sl];
+                    s.acc[which][w][sl] = 0.f;
+                }
+                to += sum;
+            });
+        };
         if (cut.seg == 0 && t0 >= t1 && p.g.dS0) store4(p.g.dS0 + n * Dn, r);
 
         // my vectors of a tile: V channels of a row
@@ -1170,6 +1205,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
                     load4(p.dS_T ? p.dS_T + n * Dn : nullptr, r);
                 }
             }
+            if (te <= t0 || te % kSumTokens == 0) add_sums();
             if (te > t0) {
                 ta = tile_start(te, cu[n]);
                 // (what finish reads of the inputs' places, the same threads write now; the
@@ -1177,18 +1213,7 @@ scan_bwd_kernel(const ScanArgs p, const Cut cut, const Maps maps, float* part, f
                 convert(ta, te - ta);
             }
         }
-        float* const sums = part + sg * part_row(D, p.n);
-        store4(sums, dA);
-        __syncthreads();
-        // the warps, in order
-        for (int i = tid; i < 2 * CH; i += TH) {
-            const int which = i / CH, sl = i % CH, c = sl % VR * V + sl / VR;
-            float sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < G::kWarps; ++w) sum += s.acc[which][w][sl];
-            if (c < width) sums[Dn + (int64_t)which * D + base + c] = sum;
-        }
-        __syncthreads();
+        __syncthreads();   // (the next item's sums)
     }
 }
 
