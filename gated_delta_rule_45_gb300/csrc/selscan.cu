@@ -12,8 +12,10 @@
 // over the tile in rows of 16 bytes; the next tile's rows are loaded meanwhile, and two buffers
 // make one barrier a tile do.
 //
-// Work along the tokens: where the sequences alone fill the GPU a CTA walks a whole sequence, the
-// longest first.  Few long ones are cut into segments of the packed axis, regardless of sequences:
+// Work along the tokens: where the sequences are many enough to fill the GPU a CTA walks a whole
+// sequence, the longest first.  That goes by their number: a batch of many with one far longer than
+// the rest is bound by that one's CTAs (64 x 2048 channels with one of 200000 tokens of 266213: 24.4
+// ms for 2.9 of equal ones, backward 105 for 12.4).  Few long ones are cut into segments of the packed axis, regardless of sequences:
 // the map of a segment is its end state from zero and the sum of its step sizes (the product of
 // its decays is exp(A sum D)), a short pass joins the maps, and the segments are walked from
 // their entry states.  The backward pass does the same on reversed tokens.
@@ -25,10 +27,10 @@
 // steps and inputs of zero around it.
 //
 // Bound: instructions, with the exponentials at a third of their unit's rate (32 a clock and SM).
-// Measured, bf16, n = 16 with gate and skip: 64 ragged prompts of 266240 x 2048 2.68 ms (4.4 GB,
-// 1.6 TB/s; 8.7e9 exponentials, which alone take 0.93 ms: issue 2.3 a clock and SM of 4), one of
-// 131072 x 4096 4.6 ms (cut: each exponential twice), forward of 8 x 4096 x 4096 with `states` 0.85
-// ms, backward 3.5 ms (2.75 exponentials and 30 instructions a value; issue 1.9 a clock and SM, waits
+// Measured, bf16, n = 16 with gate and skip: 64 ragged prompts of 266240 x 2048 2.71 ms (4.4 GB,
+// 1.6 TB/s; 8.7e9 exponentials, which alone take 0.93 ms: issue 2.2 a clock and SM of 4), one of
+// 131072 x 4096 4.67 ms (cut: each exponential twice), forward of 8 x 4096 x 4096 with `states` 0.86
+// ms, backward 3.5 ms (2.75 exponentials and 31 instructions a value; issue 2.15 a clock and SM, waits
 // for shared memory, exchanges and loads in equal parts).  Two channels a lane take a tenth fewer
 // instructions but leave half the warps: 10 to 25 % slower.  Warps of their own for the passes
 // before and after the walk: 50 % slower.
@@ -118,8 +120,8 @@ struct Cut {
     int64_t items;      // nseg x blocks
 };
 
-// The sequence of `rank` in the order longest first (by number among equals): sequences of very
-// different lengths, each a CTA's, then end together.  All threads of the CTA call it; batches
+// The sequence of `rank` in the order longest first (by number among equals): sequences of
+// different lengths, each a CTA's, then end together, if none takes longer than its share.  All threads of the CTA call it; batches
 // of more than kRanked sequences keep their order.
 constexpr int kRanked = 128;
 __device__ __forceinline__ int32_t ranked_sequence(const int32_t* cu, int32_t N, int32_t rank,
@@ -1393,7 +1395,8 @@ int back_channels(int n) {
 // (a walk takes 130 ns a token, cutting 20 us: 64 tokens of 64 channels 14 us whole and 31 cut);
 // else segments of at least `least` tokens, as many as take the GPU's places (`each` CTAs an SM)
 // twice.  (A last round that fills them in part costs as much as a whole one: 131072 x 4096 in 960
-// pieces on 608 places took 5.25 ms, in 1216 it takes 4.6.)
+// pieces on 608 places took 5.25 ms, in 1216 4.6.)  The lengths are on the device: the choice is made
+// by N and T alone.
 Cut make_cut(int32_t N, int64_t T, int32_t H, int32_t d, int ch, int each, int fill,
              int least) {
     Cut c = {};

@@ -1261,7 +1261,8 @@ def selscan_prefill_into(x, dt, A, B, C, S0, cu_seqlens, y, S_T, workspace, *, D
     [H, d, n] fp32; D, dt_bias: [H, d] fp32 or None; S0: [N, H, d, n] fp32 or None; cu_seqlens:
     int32 [N+1] on the device; y: like x; S_T: like S0 (may be S0); states: [ceil(T /
     SELSCAN_CHUNK), H, d, n] fp32 or None, kept for ``selscan_backward``; workspace: uint8, at
-    least ``selscan_workspace_size`` bytes."""
+    least ``selscan_workspace_size`` bytes.  One sequence far longer than many others of its
+    batch is done sooner by a call of its own."""
     T, N, H, d, n, code, r = _scan_inputs(x, dt, A, B, C, S0, cu_seqlens, D, z, dt_bias)
     _check("y", y, x.dtype, x.shape)
     _check("S_T", S_T, torch.float32, (N, H, d, n))
@@ -1337,7 +1338,8 @@ def selscan_backward_into(x, dt, A, B, C, S0, cu_seqlens, dy, dS_T, grads, works
                           stream=None) -> None:
     """Enqueue selscan_backward into preallocated fp32 gradients.
 
-    Inputs as ``selscan_prefill_into``; dy: like x; dS_T: [N, H, d, n] fp32 or None; states:
+    Inputs as ``selscan_prefill_into``; dy: like x (the fp32 dx of an operator behind is cast
+    for bf16, as for the other backward passes); dS_T: [N, H, d, n] fp32 or None; states:
     what selscan_prefill saved, or None (the forward scan runs again); grads: dict with "dx",
     "ddt" [T, H, d], "dB", "dC" [T, H, n], "dA" [H, d, n], with a gate "dz" [T, H, d], and
     optionally "dD", "ddt_bias" [H, d] and "dS0" [N, H, d, n]; workspace: uint8, at least

@@ -88,6 +88,11 @@ size_t selscan_prefill_workspace_size(int32_t num_seqs, int64_t total_tokens, in
  *   workspace    selscan_prefill_workspace_size bytes, 16-byte aligned, not
  *                shared by calls that may run concurrently
  *
+ * Long sequences are spread over the GPU by their tokens where num_seqs x H x d is
+ * too small to fill it, whatever their lengths: in a batch of many, one that is far
+ * longer than the rest is walked by itself (some 125 ns a token, backward 525), and is
+ * done sooner by a call of its own.
+ *
  * kda_prefill_device_status(workspace) reports device-detected errors
  * (KDA_ERR_DEVICE_INPUT).  Supported: H >= 1, d >= 1, 1 <= n <= 64,
  * H x d <= 2^20, total_tokens <= 2^31 - 1 - 4096, num_seqs <= 2^30,
@@ -102,6 +107,9 @@ kda_status selscan_prefill(const selscan_rows* rows, const float* A, const float
 
 /* Bytes of device workspace selscan_backward needs on the current device; `with_states` is
  * 0 when the call passes no `states` (they are then recomputed into the workspace).
+ * Where a group's channels take several CTAs (128, 64, 32 or 16 channels each, for n up
+ * to 8, 16, 32 or 64) their sums for dB and dC come first: 8 T H n bytes a CTA of a group
+ * (1.1 GB for 131072 x 4096 channels of 16 values, 17 GB of 64).
  * Returns 0 for a size it does not support. */
 size_t selscan_backward_workspace_size(int32_t num_seqs, int64_t total_tokens, int32_t H,
                                        int32_t d, int32_t n, int32_t with_states);
@@ -110,7 +118,7 @@ size_t selscan_backward_workspace_size(int32_t num_seqs, int64_t total_tokens, i
 typedef struct {
     float *dx, *ddt;        /* [T][H][d]; ddt with respect to dt (before softplus) */
     float *dB, *dC;         /* [T][H][n] */
-    float *dz;              /* [T][H][d], or NULL (must be NULL without a gate) */
+    float *dz;              /* [T][H][d]; NULL without a gate, and only then */
     float *dA;              /* [H][d][n] */
     float *dskip, *ddt_bias;  /* [H][d], or NULL (not written) */
     float *dS0;             /* [N][H][d][n], or NULL (not written) */
